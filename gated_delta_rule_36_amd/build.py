@@ -13,6 +13,7 @@ from concurrent.futures import ThreadPoolExecutor
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
+LAYER = os.path.join(CSRC, "layer")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIBRARY = os.path.join(PKG, "libkda.so")
@@ -23,11 +24,13 @@ ARCH = "gfx950"
 # vector arithmetic only.
 COMMON = ["-O3", "-fPIC", "-std=c++17", f"--offload-arch={ARCH}", "-Wall",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-          f"-I{INCLUDE}", f"-I{CSRC}"]
+          f"-I{INCLUDE}", f"-I{CSRC}", f"-I{LAYER}"]
 
 
 def sources():
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC)
+    """Every source under csrc/: the KDA forward pass, and in layer/ the
+    operators around it."""
+    return sorted(os.path.join(d, f) for d in (CSRC, LAYER) for f in os.listdir(d)
                   if f.endswith((".hip", ".cpp")))
 
 

@@ -349,6 +349,9 @@ extern "C" const char *kda_status_string(kda_status status)
     case KDA_ERR_WORKSPACE: return "workspace is NULL, not 16-byte aligned, too small, or overlaps a tensor";
     case KDA_ERR_ALIGNMENT: return "a tensor pointer is misaligned (q, k, v, g, out, states: 16 bytes; beta 2; A_log, dt_bias 4; cu_seqlens 8)";
     case KDA_ERR_OPTION: return "invalid options: unknown value, non-zero reserved field, or a kernel / inverse / sigmoid combination not implemented for this call";
+    case KDA_ERR_SHAPE: return "a width, head, state, group or norm size is not a supported one";
+    case KDA_ERR_DTYPE: return "weights, gates and residual streams must be bf16 or fp32";
+    case KDA_ERR_STRIDE: return "a stride is negative, or its extent overflows int64";
     }
     return "unknown status";
 }

@@ -1,0 +1,204 @@
+// Device helpers shared by the layer kernels: eight-element loads and stores
+// at any element alignment, sums over lanes, and the map from work slots to
+// sequences.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kda_device.h"
+#include "layer_internal.h"
+
+namespace kda {
+namespace layer {
+
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+// The same sixteen bytes at element alignment: rows of odd widths and slices
+// of fused projections start anywhere.  Global memory serves unaligned
+// 16-byte accesses directly, so one code path covers every stride.
+typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b)
+{
+    const bf16x2_t v = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
+    return __builtin_bit_cast(uint32_t, v);
+}
+__device__ __forceinline__ float lo_f32(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float hi_f32(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
+__device__ __forceinline__ void unpack8(u32x4_t u, float f[8])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = lo_f32(u[i]);
+        f[2 * i + 1] = hi_f32(u[i]);
+    }
+}
+__device__ __forceinline__ u32x4_t pack8(const float f[8])
+{
+    return u32x4_t{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                   pack_bf16x2(f[6], f[7])};
+}
+
+// Eight bf16 at p, of which the first `count` exist (the others read as 0).
+__device__ __forceinline__ u32x4_t load8_raw(const uint16_t *p, int count)
+{
+    if (count >= 8)
+        return *reinterpret_cast<const u32x4_a2 *>(p);
+    u32x4_t u = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+        if (i < count)
+            u[i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
+    return u;
+}
+__device__ __forceinline__ void store8_raw(uint16_t *p, u32x4_t u, int count)
+{
+    if (count >= 8) {
+        *reinterpret_cast<u32x4_a2 *>(p) = u;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+        if (i < count)
+            p[i] = static_cast<uint16_t>(u[i / 2] >> (16 * (i & 1)));
+}
+// Eight elements of kind KIND at element index `at`, as fp32.
+__device__ __forceinline__ void load8(const void *base, int kind, int64_t at, int count, float f[8])
+{
+    if (kind == kBf16) {
+        unpack8(load8_raw(static_cast<const uint16_t *>(base) + at, count), f);
+        return;
+    }
+    const float *p = static_cast<const float *>(base) + at;
+    if (count >= 8) {
+        const f32x4_t a = *reinterpret_cast<const f32x4_a4 *>(p), b = *reinterpret_cast<const f32x4_a4 *>(p + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[i] = a[i];
+            f[4 + i] = b[i];
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = i < count ? p[i] : 0.0f;
+}
+__device__ __forceinline__ void store8(void *base, int kind, int64_t at, int count, const float f[8])
+{
+    if (kind == kBf16) {
+        store8_raw(static_cast<uint16_t *>(base) + at, pack8(f), count);
+        return;
+    }
+    float *p = static_cast<float *>(base) + at;
+    if (count >= 8) {
+        *reinterpret_cast<f32x4_a4 *>(p) = f32x4_t{f[0], f[1], f[2], f[3]};
+        *reinterpret_cast<f32x4_a4 *>(p + 4) = f32x4_t{f[4], f[5], f[6], f[7]};
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+        if (i < count)
+            p[i] = f[i];
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float x)
+{
+    return x + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xf, 0xf, false));
+}
+// The sum over aligned groups of L lanes (1..64, a power of two), in every
+// lane: quad permutations, the half-row and row mirrors, then exchanges of
+// 16-lane rows and of wave halves.  All lanes of the group must be active.
+template <int L>
+__device__ __forceinline__ float lane_sum(float x)
+{
+    if constexpr (L >= 2) x = dpp_add<0xb1>(x);
+    if constexpr (L >= 4) x = dpp_add<0x4e>(x);
+    if constexpr (L >= 8) x = dpp_add<0x141>(x);
+    if constexpr (L >= 16) x = dpp_add<0x140>(x);
+    if constexpr (L >= 32) {
+        const uint32_t u = __float_as_uint(x);
+        const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+        const uint32_t r0 = r[0], r1 = r[1];
+        x = __uint_as_float(r0) + __uint_as_float(r1);
+    }
+    if constexpr (L >= 64) {
+        const uint32_t u = __float_as_uint(x);
+        const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+        const uint32_t r0 = r[0], r1 = r[1];
+        x = __uint_as_float(r0) + __uint_as_float(r1);
+    }
+    return x;
+}
+
+__device__ __forceinline__ float silu_f32(float x) { return x * sigmoid_f32(x); }
+
+// Sequences are cut into tiles of `len` tokens that start at the sequence's
+// first token.  In a batch every sequence has ceil(T / len) tiles (one if
+// T = 0).  Packed sequence n owns the slots from cu[n] / len + n on: at least
+// one, and at least as many as it has tiles, since
+// ceil((b - a) / len) <= floor(b / len) - floor(a / len) + 1.  So the host
+// can size the grid (T / len + N slots) without reading cu_seqlens, and a
+// slot finds its sequence by search.
+struct Tile {
+    int64_t n, begin, end, row;  // sequence, its token range, its batch row
+    int64_t index;               // tile within the sequence; its tokens may be none
+    bool valid;                  // false: a slot no tile uses
+};
+
+__device__ __forceinline__ int64_t clamp_offset(const Seqs &s, int64_t n)
+{
+    const int64_t v = s.cu[n];
+    return v < 0 ? 0 : (v > s.T ? s.T : v);
+}
+
+__device__ __forceinline__ Tile find_tile(const Seqs &s, int64_t len, int64_t slot)
+{
+    Tile t;
+    if (!s.cu) {
+        const int64_t per = s.T > 0 ? (s.T + len - 1) / len : 1;
+        t.n = slot / per;
+        t.index = slot - t.n * per;
+        t.begin = 0;
+        t.end = s.T;
+        t.row = t.n;
+        t.valid = true;
+        return t;
+    }
+    // the last n with cu[n] / len + n <= slot; 64 probes a round.  Offsets
+    // out of order still end at some n in [0, N).
+    const int lane = static_cast<int>(__lane_id());
+    int64_t lo = 0, hi = s.N;
+    while (hi - lo > 1) {
+        const int64_t step = (hi - lo + 63) / 64, n = lo + lane * step;
+        const bool below = n < hi && clamp_offset(s, n) / len + n <= slot;
+        const int count = __popcll(__ballot(below));
+        if (count == 0)
+            break;
+        lo += (count - 1) * step;
+        hi = hi < lo + step ? hi : lo + step;
+    }
+    t.n = lo;
+    t.begin = clamp_offset(s, lo);
+    t.end = clamp_offset(s, lo + 1);
+    if (t.end < t.begin)
+        t.end = t.begin;
+    t.row = 0;
+    t.index = slot - (t.begin / len + lo);
+    t.valid = t.index == 0 || (t.index > 0 && t.index < (t.end - t.begin + len - 1) / len);
+    return t;
+}
+
+inline int64_t tile_slots(const Seqs &s, int64_t len)
+{
+    if (s.cu)
+        return s.T / len + s.N;
+    return s.N * (s.T > 0 ? (s.T + len - 1) / len : 1);
+}
+
+}  // namespace layer
+}  // namespace kda

@@ -1,0 +1,94 @@
+// Internal interface between the C-ABI front end of the layer operators
+// (layer_api.cpp) and their HIP kernels.  Not part of the public ABI.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stdint.h>
+
+namespace kda {
+namespace layer {
+
+// Element kinds of parameters, residual streams and states (kda_dtype values).
+enum Kind : int { kNone = 0, kBf16 = 1, kFp32 = 2 };
+enum Act : int { kActNone = 0, kActSilu = 1, kActSigmoid = 2 };
+
+constexpr int64_t kMaxTaps = 8;         // W of the convolution
+constexpr int64_t kMaxNormSize = 16384; // elements one norm spans
+
+// Sequences: a batch (cu == nullptr: N sequences of T tokens, one per batch
+// row) or packed along the token axis of one row.
+struct Seqs {
+    const int64_t *cu;
+    int64_t N, T;
+};
+
+struct ConvParams {
+    const uint16_t *x;
+    int64_t xb, xt;  // element strides of batch row and token
+    const void *weight, *bias;
+    int weight_kind;
+    uint16_t *out;
+    const void *init_state;
+    void *final_state;
+    int init_kind, final_kind;
+    Seqs seqs;
+    int64_t D;
+    int act, l2norm;
+    float l2eps;
+};
+hipError_t launch_conv(const ConvParams &p, int W, hipStream_t stream);
+
+struct GatedParams {
+    const uint16_t *x, *gate;  // gate may be nullptr
+    int64_t xr, gr;            // element strides of a row
+    const void *weight;        // [D]
+    int weight_kind;
+    uint16_t *out;
+    int64_t rows, D, group;
+    int act, gate_first;
+    float eps;
+};
+hipError_t launch_gated_norm(const GatedParams &p, hipStream_t stream);
+
+struct ResidParams {
+    const uint16_t *x;
+    int64_t xr;
+    const void *residual;  // or nullptr
+    void *residual_out;    // or nullptr
+    int residual_kind, residual_out_kind;
+    const void *post_weight, *weight;  // or nullptr
+    int post_kind, weight_kind;
+    const void *gate;  // or nullptr; row r reads gate row r / gate_period
+    int gate_kind;
+    int64_t gr, gate_period;
+    uint16_t *out;  // or nullptr
+    int64_t rows, D;
+    float residual_scale, block_scale, eps;
+};
+hipError_t launch_residual_norm(const ResidParams &p, hipStream_t stream);
+
+struct SsmParams {
+    const uint16_t *x, *dt, *b, *c, *z;  // z may be nullptr
+    int64_t xb, xt, db, dtt, bb, bt, cb, ct, zb, zt;  // element strides of batch row and token
+    uint16_t *out;
+    const float *A_log, *D, *dt_bias;  // D, dt_bias may be nullptr
+    const void *init_state;
+    void *final_state;
+    int init_kind, final_kind;
+    Seqs seqs;
+    int64_t H, P, G, N;
+    int softplus;
+    // segmented form: seg tokens a segment; slabs and log decays per slot
+    int64_t seg;
+    float *slabs, *logs;
+};
+// Tokens per chunk of the chunked kernel; segments are multiples of it.
+constexpr int64_t kSsmChunk = 32;
+// Calls without cu_seqlens of at most this many tokens take the token
+// recurrence.
+constexpr int64_t kSsmRecurrentMaxTokens = 8;
+
+hipError_t launch_ssm_recurrent(const SsmParams &p, hipStream_t stream);
+
+}  // namespace layer
+}  // namespace kda

@@ -72,13 +72,22 @@ typedef enum kda_status {
                                   16 bytes, beta 2, A_log and dt_bias 4,
                                   cu_seqlens 8 (allocator memory and whole
                                   token rows of it always are) */
-    KDA_ERR_OPTION = 12        /* kda_options: an unknown value, a non-zero
+    KDA_ERR_OPTION = 12,       /* kda_options: an unknown value, a non-zero
                                   reserved field, or a kernel / inverse /
                                   sigmoid combination that no kernel of the
-                                  library implements for this call */
+                                  library implements for this call; the layer
+                                  operators: an unknown activation or flag, or
+                                  a non-zero reserved field */
+    KDA_ERR_SHAPE = 13,        /* layer operators: a width, head, state, group
+                                  or norm size outside the supported ones */
+    KDA_ERR_DTYPE = 14,        /* layer operators: a weight, gate or residual
+                                  dtype that is neither bf16 nor fp32 */
+    KDA_ERR_STRIDE = 15        /* layer operators: a negative stride, or one
+                                  whose extent overflows int64 */
 } kda_status;
 
-/* Element type of initial_state / final_state. */
+/* Element type of initial_state / final_state (and of the layer operators'
+ * weights, gates and residual streams). */
 typedef enum kda_dtype {
     KDA_DTYPE_NONE = 0,
     KDA_DTYPE_BF16 = 1,
@@ -295,8 +304,213 @@ const char *kda_status_string(kda_status status);
  */
 const char *kda_fwd_kernel(int64_t T, int varlen, const kda_options *options);
 
+/* -------------------------------------------------------------------------
+ * The layer operators: what surrounds a recurrent mixer in a model, and the
+ * scalar-decay recurrence that hybrid models alternate with KDA.  The rules
+ * above hold for them too: device pointers on the current device, nothing
+ * allocated, every check on the host before anything is enqueued, no state
+ * between calls, asynchronous on `stream`.  Activations are bf16 with
+ * fp32 arithmetic and one rounding to nearest even at the end.  The arguments
+ * come in a struct whose unused fields are 0.  Outputs are contiguous; inputs
+ * may be slices of wider rows, given by element strides of the batch row and
+ * of the token (>= 0) with the channels of a token adjacent.  Token tensors
+ * need no alignment beyond their element's; out and the states 16 bytes.
+ * Outputs must not overlap inputs, except where it is said.
+ * ---------------------------------------------------------------------- */
+
+typedef enum kda_activation {
+    KDA_ACT_NONE = 0,
+    KDA_ACT_SILU = 1,    /* v / (1 + e^-v) */
+    KDA_ACT_SIGMOID = 2  /* 1 / (1 + e^-v) */
+} kda_activation;
+
+/*
+ * kda_short_conv - the short causal depthwise convolution in front of a
+ * mixer, with its activation and, for query and key heads, their L2 norm
+ * (kda_fwd takes q and k as the caller normalised them):
+ *
+ *   y[t,c]   = act(bias[c] + sum_j weight[c,j] x[t - W + 1 + j, c])
+ *   out[t,c] = y[t,c], or with l2norm = L > 0
+ *              y[t,c] / sqrt(l2norm_eps + sum of y[t,.]^2 over the L channels
+ *              of c's group), groups of L channels from channel 0 on
+ *
+ * Inputs before a sequence's first token are its initial_state's.
+ *
+ *   x              bf16 [B,T,D], strides x_stride_b, x_stride_t.
+ *   weight, bias   [D,W] and [D] or NULL, both of weight_dtype.
+ *   out            bf16 [B,T,D], contiguous.  Rows outside every packed
+ *                  sequence are not written.
+ *   initial_state, final_state
+ *                  [N,W-1,D] of their dtypes (equal if both are given), the
+ *                  last W - 1 inputs before / of the sequence, oldest first;
+ *                  NULL = zeros / not written.  They may be one buffer.  A
+ *                  sequence shorter than W - 1 keeps the newest inputs of its
+ *                  initial state; an empty one passes it through.
+ *   cu_seqlens, num_seqs, B, T   as for kda_fwd.
+ *   D              channels, 1 <= D <= 2^24.
+ *   W              taps, 1 <= W <= 8 (KDA_ERR_SHAPE otherwise).
+ *   activation     KDA_ACT_NONE or KDA_ACT_SILU.
+ *   l2norm         0, 64, 128 or 256, dividing D (KDA_ERR_SHAPE otherwise).
+ *   l2norm_eps     finite, >= 0 (KDA_ERR_SCALE otherwise).
+ */
+typedef struct kda_conv_args {
+    const void *x;
+    int64_t x_stride_b, x_stride_t;
+    const void *weight;
+    const void *bias;
+    void *out;
+    const void *initial_state;
+    void *final_state;
+    const int64_t *cu_seqlens;
+    int64_t num_seqs, B, T, D, W;
+    int32_t weight_dtype, initial_state_dtype, final_state_dtype; /* kda_dtype */
+    int32_t activation;                                           /* kda_activation */
+    int64_t l2norm;
+    double l2norm_eps;
+    int64_t reserved;
+} kda_conv_args;
+kda_status kda_short_conv(const kda_conv_args *args, void *stream);
+
+/*
+ * kda_ssm_fwd - the selective state space scan with one decay per head, over
+ * prompts and single tokens.  Per (sequence, head) and token (state S is
+ * P x N, fp32):
+ *
+ *   dt_t = softplus(dt + dt_bias[h])     (dt + dt_bias[h] without softplus)
+ *   S    = exp(-exp(A_log[h]) dt_t) S + dt_t x_t b_t^T
+ *   y_t  = S c_t + D[h] x_t
+ *   out_t = y_t silu(z_t)                (y_t without z)
+ *
+ *   x, z, out      bf16 [B,T,H,P]; z may be NULL.  out is contiguous.
+ *   dt             bf16 [B,T,H].
+ *   b, c           bf16 [B,T,G,N]; heads h with the same h / (H / G) share a
+ *                  group's b and c (G divides H).
+ *   A_log, D, dt_bias  fp32 [H]; D and dt_bias may be NULL (0).
+ *   softplus       1 or 0.  Without it a negative dt grows the state.
+ *   initial_state, final_state  [N_seq,H,P,N] of their dtypes, as for
+ *                  kda_fwd (they may be one buffer).
+ *   cu_seqlens, num_seqs, B, T, H   as for kda_fwd.
+ *   P              a multiple of 32, at most 256; N is 32, 64, 128 or 256
+ *                  (KDA_ERR_SHAPE otherwise).
+ *   seg_tokens     tokens a segment: sequences longer than that are cut into
+ *                  segments that run in parallel, joined in fp32 (the state
+ *                  at a segment's start is affine in the one before, by one
+ *                  factor per head).  0 lets the library choose from the
+ *                  sizes; otherwise a multiple of 32 (KDA_ERR_SHAPE).  Calls
+ *                  without cu_seqlens of at most 8 tokens run token by token,
+ *                  whatever seg_tokens is.
+ *   workspace, workspace_bytes   DEVICE scratch, 16-byte aligned, at least
+ *                  kda_ssm_workspace_bytes(args) bytes (which may be 0), as
+ *                  for kda_fwd_scan (KDA_ERR_WORKSPACE otherwise).
+ *
+ * A non-finite x, b or c reaches the outputs of its whole 32-token chunk and
+ * of every later token of its sequence; it never reaches another sequence.
+ */
+typedef struct kda_ssm_args {
+    const void *x;
+    const void *dt;
+    const void *b;
+    const void *c;
+    const void *z;
+    void *out;
+    int64_t x_stride_b, x_stride_t, dt_stride_b, dt_stride_t, b_stride_b, b_stride_t;
+    int64_t c_stride_b, c_stride_t, z_stride_b, z_stride_t;
+    const float *A_log;
+    const float *D;
+    const float *dt_bias;
+    const void *initial_state;
+    void *final_state;
+    const int64_t *cu_seqlens;
+    int64_t num_seqs, B, T, H, P, G, N;
+    int32_t initial_state_dtype, final_state_dtype; /* kda_dtype */
+    int32_t softplus;
+    int32_t reserved;
+    int64_t seg_tokens;
+    void *workspace;
+    int64_t workspace_bytes;
+} kda_ssm_args;
+kda_status kda_ssm_fwd(const kda_ssm_args *args, void *stream);
+
+/*
+ * Bytes of workspace kda_ssm_fwd needs for these sizes, cu_seqlens (tested
+ * for NULL, never read) and seg_tokens; the pointers to tensors are ignored.
+ * -1 where the sizes are ones kda_ssm_fwd refuses.
+ */
+int64_t kda_ssm_workspace_bytes(const kda_ssm_args *args);
+
+/*
+ * kda_gated_norm - the norm of a mixer's output with its gate, over groups of
+ * `group` channels (D / group of them in a row):
+ *
+ *   out = v / sqrt(eps + mean of v^2 over the group) * weight * act(gate),
+ *         v = x                                     (gate_first = 0)
+ *   out = v / sqrt(eps + mean of v^2 over the group) * weight,
+ *         v = x * act(gate)                         (gate_first = 1)
+ *
+ *   x, gate        bf16 [rows, D], element strides x_stride, gate_stride of a
+ *                  row; gate may be NULL (a plain norm).
+ *   weight         [D] of weight_dtype.
+ *   out            bf16 [rows, D], contiguous.
+ *   group          divides D, 1 <= group <= 16384 (KDA_ERR_SHAPE otherwise).
+ *   activation     KDA_ACT_SIGMOID or KDA_ACT_SILU (ignored without gate).
+ *   eps            finite, >= 0 (KDA_ERR_SCALE otherwise).
+ * rows = 0 does nothing.
+ */
+typedef struct kda_gated_norm_args {
+    const void *x;
+    const void *gate;
+    const void *weight;
+    void *out;
+    int64_t x_stride, gate_stride, rows, D, group;
+    int32_t weight_dtype; /* kda_dtype */
+    int32_t activation;   /* kda_activation */
+    int32_t gate_first;   /* 0 or 1 */
+    int32_t reserved;
+    double eps;
+} kda_gated_norm_args;
+kda_status kda_gated_norm(const kda_gated_norm_args *args, void *stream);
+
+/*
+ * kda_residual_norm - the residual update between two blocks with the norm
+ * after the one, its gate and scales, and the norm before the next:
+ *
+ *   y = x, or x / sqrt(eps + mean x^2) * post_weight
+ *   r = residual_scale * residual + block_scale * gate * y
+ *   residual_out = r
+ *   out = r / sqrt(eps + mean r^2) * weight       (from the unrounded r)
+ *
+ *   x              bf16 [rows, D], element stride x_stride of a row.
+ *   residual       [rows, D] of residual_dtype, contiguous; NULL = 0.
+ *   residual_out   [rows, D] of residual_out_dtype, contiguous; NULL = not
+ *                  written.  It may be `residual`, if the dtypes are equal.
+ *   post_weight    [D] of post_weight_dtype; NULL = no norm after the block.
+ *   gate           of gate_dtype; row r reads the D values at
+ *                  (r / gate_period) * gate_stride: one gate for all rows
+ *                  (gate_stride 0), per sequence (gate_period = its rows) or
+ *                  per row (gate_period 1).  NULL = 1.
+ *   weight, out    [D] of weight_dtype and bf16 [rows, D], contiguous; both
+ *                  NULL: no norm before the next block.
+ *   D              1 <= D <= 16384 (KDA_ERR_SHAPE otherwise).
+ *   residual_scale, block_scale  finite; eps finite, >= 0 (KDA_ERR_SCALE).
+ * rows = 0 does nothing.
+ */
+typedef struct kda_residual_norm_args {
+    const void *x;
+    const void *residual;
+    void *residual_out;
+    const void *post_weight;
+    const void *gate;
+    const void *weight;
+    void *out;
+    int64_t x_stride, gate_stride, gate_period, rows, D;
+    int32_t residual_dtype, residual_out_dtype, post_weight_dtype, gate_dtype, weight_dtype; /* kda_dtype */
+    int32_t reserved;
+    double residual_scale, block_scale, eps;
+} kda_residual_norm_args;
+kda_status kda_residual_norm(const kda_residual_norm_args *args, void *stream);
+
 /* ABI version of this header (bumped on any signature change). */
-#define KDA_ABI_VERSION 4
+#define KDA_ABI_VERSION 5
 int kda_abi_version(void);
 
 #ifdef __cplusplus
