@@ -170,12 +170,58 @@ kda_status check_ssm_sizes(const kda_ssm_args &a, Seqs *s)
 
 }  // namespace
 
+namespace {
+
+// How a scan call with valid sizes runs.
+struct SsmPlan {
+    bool recurrent = false;
+    int64_t seg = 0;              // tokens a segment (chunked kernel)
+    int64_t slots = 0, slab = 0;  // slots and floats a slot, slab = 0 without segments
+    int64_t bytes = 0;            // workspace
+};
+
+// Calls without cu_seqlens of up to kSsmRecurrentMaxTokens tokens: the token
+// recurrence.  The others: whole sequences if those fill the GPU, else
+// segments of about the tokens that give each of 256 workgroups an equal share
+// (at least kMinSegment, below which joining costs more than it gains).
+// Packed sequences are always cut at that length, since one of them may hold
+// most of the tokens.  False if the workspace overflows.
+bool ssm_plan(const kda_ssm_args &a, const Seqs &s, SsmPlan *plan)
+{
+    constexpr int64_t kTarget = 256, kMinSegment = 128, c = kda::layer::kSsmChunk;
+    if (!s.cu && s.T <= kda::layer::kSsmRecurrentMaxTokens) {
+        plan->recurrent = true;
+        return true;
+    }
+    const int64_t blocks = a.G * ((a.H / a.G * (a.P / 32) + kda::layer::kSsmUnits - 1) / kda::layer::kSsmUnits);
+    const int64_t longest = s.T > c ? (s.T + c - 1) / c * c : c;
+    int64_t seg = a.seg_tokens;
+    if (seg == 0) {
+        seg = longest;
+        const int64_t sequences = s.cu ? 1 : s.N;
+        if (sequences * blocks < kTarget) {
+            const int64_t share = (sequences * s.T * blocks + kTarget - 1) / kTarget;
+            seg = share < kMinSegment ? kMinSegment : (share + c - 1) / c * c;
+        }
+    }
+    plan->seg = seg < longest ? seg : longest;
+    plan->slots = kda::layer::tile_slots(s, plan->seg);
+    if (plan->seg >= longest)
+        return true;
+    plan->slab = a.H * a.P * a.N;
+    int64_t n;
+    return mul_ok(plan->slots, 4 * (plan->slab + a.H), &n) && add_ok(n, 15, &plan->bytes) && (plan->bytes &= ~int64_t(15)) >= 0;
+}
+
+}  // namespace
+
 extern "C" int64_t kda_ssm_workspace_bytes(const kda_ssm_args *args)
 {
     Seqs s;
-    if (!args || check_ssm_sizes(*args, &s) != KDA_OK)
+    SsmPlan plan;
+    if (!args || check_ssm_sizes(*args, &s) != KDA_OK || !ssm_plan(*args, s, &plan))
         return -1;
-    return 0;
+    return plan.bytes;
 }
 
 extern "C" kda_status kda_ssm_fwd(const kda_ssm_args *args, void *stream)
@@ -214,10 +260,12 @@ extern "C" kda_status kda_ssm_fwd(const kda_ssm_args *args, void *stream)
         misaligned(a.out, 16) || misaligned(a.initial_state, 16) || misaligned(a.final_state, 16) ||
         misaligned(a.A_log, 4) || misaligned(a.D, 4) || misaligned(a.dt_bias, 4) || misaligned(a.cu_seqlens, 8))
         return KDA_ERR_ALIGNMENT;
-    const int64_t need = kda_ssm_workspace_bytes(args);
-    if (need > 0) {
-        if (!a.workspace || a.workspace_bytes < need || misaligned(a.workspace, 16) ||
-            any_overlap(span(a.workspace, need), {sx, sd, sb, sc, sz, sA, sD, st_, su, so, si, sf}))
+    SsmPlan plan;
+    if (!ssm_plan(a, p.seqs, &plan))
+        return KDA_ERR_SIZE;
+    if (plan.bytes > 0) {
+        if (!a.workspace || a.workspace_bytes < plan.bytes || misaligned(a.workspace, 16) ||
+            any_overlap(span(a.workspace, plan.bytes), {sx, sd, sb, sc, sz, sA, sD, st_, su, so, si, sf}))
             return KDA_ERR_WORKSPACE;
     }
     p.x = static_cast<const uint16_t *>(a.x);
@@ -250,7 +298,14 @@ extern "C" kda_status kda_ssm_fwd(const kda_ssm_args *args, void *stream)
     p.softplus = a.softplus;
     if (p.seqs.N == 0 || (tokens == 0 && !a.final_state))
         return KDA_OK;
-    return launched(kda::layer::launch_ssm_recurrent(p, static_cast<hipStream_t>(stream)));
+    if (plan.recurrent)
+        return launched(kda::layer::launch_ssm_recurrent(p, static_cast<hipStream_t>(stream)));
+    p.seg = plan.seg;
+    if (plan.slab > 0) {
+        p.slabs = static_cast<float *>(a.workspace);
+        p.logs = p.slabs + plan.slots * plan.slab;
+    }
+    return launched(kda::layer::launch_ssm_chunk(p, static_cast<hipStream_t>(stream)));
 }
 
 extern "C" kda_status kda_gated_norm(const kda_gated_norm_args *args, void *stream)

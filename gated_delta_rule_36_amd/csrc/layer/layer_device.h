@@ -193,12 +193,5 @@ __device__ __forceinline__ Tile find_tile(const Seqs &s, int64_t len, int64_t sl
     return t;
 }
 
-inline int64_t tile_slots(const Seqs &s, int64_t len)
-{
-    if (s.cu)
-        return s.T / len + s.N;
-    return s.N * (s.T > 0 ? (s.T + len - 1) / len : 1);
-}
-
 }  // namespace layer
 }  // namespace kda

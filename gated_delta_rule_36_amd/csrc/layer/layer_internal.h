@@ -22,6 +22,14 @@ struct Seqs {
     int64_t N, T;
 };
 
+// Work slots for tiles of len tokens (see find_tile in layer_device.h).
+inline int64_t tile_slots(const Seqs &s, int64_t len)
+{
+    if (s.cu)
+        return s.T / len + s.N;
+    return s.N * (s.T > 0 ? (s.T + len - 1) / len : 1);
+}
+
 struct ConvParams {
     const uint16_t *x;
     int64_t xb, xt;  // element strides of batch row and token
@@ -78,7 +86,8 @@ struct SsmParams {
     Seqs seqs;
     int64_t H, P, G, N;
     int softplus;
-    // segmented form: seg tokens a segment; slabs and log decays per slot
+    // chunked kernel: tokens a segment; with more than one segment a sequence,
+    // a state [H,P,N] and log decays [H] per work slot (else nullptr)
     int64_t seg;
     float *slabs, *logs;
 };
@@ -89,6 +98,9 @@ constexpr int64_t kSsmChunk = 32;
 constexpr int64_t kSsmRecurrentMaxTokens = 8;
 
 hipError_t launch_ssm_recurrent(const SsmParams &p, hipStream_t stream);
+hipError_t launch_ssm_chunk(const SsmParams &p, hipStream_t stream);
+// Units of 32 columns a workgroup of the chunked kernel takes.
+constexpr int64_t kSsmUnits = 8;
 
 }  // namespace layer
 }  // namespace kda
