@@ -181,11 +181,12 @@ struct SsmPlan {
 };
 
 // Calls without cu_seqlens of up to kSsmRecurrentMaxTokens tokens: the token
-// recurrence.  The others: whole sequences if those fill the GPU, else
-// segments of about the tokens that give each of 256 workgroups an equal share
-// (at least kMinSegment, below which joining costs more than it gains).
-// Packed sequences are always cut at that length, since one of them may hold
-// most of the tokens.  False if the workspace overflows.
+// recurrence.  The others: as many segments as give every compute unit of 256
+// one workgroup and no more (one fits a unit, and a second round costs as much
+// as the first), of kMinSegment tokens or more, below which joining them costs
+// more than it gains.  A batch is cut into equal parts; of packed sequences,
+// whose lengths are not known here, each is taken to end half a segment early.
+// False if the workspace overflows.
 bool ssm_plan(const kda_ssm_args &a, const Seqs &s, SsmPlan *plan)
 {
     constexpr int64_t kTarget = 256, kMinSegment = 128, c = kda::layer::kSsmChunk;
@@ -193,16 +194,21 @@ bool ssm_plan(const kda_ssm_args &a, const Seqs &s, SsmPlan *plan)
         plan->recurrent = true;
         return true;
     }
-    const int64_t blocks = a.G * ((a.H / a.G * (a.P / 32) + kda::layer::kSsmUnits - 1) / kda::layer::kSsmUnits);
+    const int64_t columns = kda::layer::kSsmWaves * kda::layer::kSsmColumns;
+    const int64_t blocks = a.G * ((a.H / a.G * a.P + columns - 1) / columns);
     const int64_t longest = s.T > c ? (s.T + c - 1) / c * c : c;
     int64_t seg = a.seg_tokens;
     if (seg == 0) {
-        seg = longest;
-        const int64_t sequences = s.cu ? 1 : s.N;
-        if (sequences * blocks < kTarget) {
-            const int64_t share = (sequences * s.T * blocks + kTarget - 1) / kTarget;
-            seg = share < kMinSegment ? kMinSegment : (share + c - 1) / c * c;
-        }
+        int64_t parts = kTarget / blocks;  // segments in all
+        if (s.cu)
+            parts = parts - s.N / 2 > parts / 2 ? parts - s.N / 2 : parts / 2;
+        else
+            parts /= s.N;
+        if (parts < 1)
+            parts = 1;
+        seg = ((s.T + parts - 1) / parts + c - 1) / c * c;
+        if (seg < kMinSegment)
+            seg = kMinSegment;
     }
     plan->seg = seg < longest ? seg : longest;
     plan->slots = kda::layer::tile_slots(s, plan->seg);

@@ -20,6 +20,7 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 // of fused projections start anywhere.  Global memory serves unaligned
 // 16-byte accesses directly, so one code path covers every stride.
 typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
 typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b)
@@ -137,6 +138,28 @@ __device__ __forceinline__ float lane_sum(float x)
 
 __device__ __forceinline__ float silu_f32(float x) { return x * sigmoid_f32(x); }
 
+// log(1 + e^v) = max(v, 0) + log1p(u), u = e^-|v|, or v itself above `plain`:
+// 20, where the two agree in fp32, or below everything for steps that are not
+// to be transformed.  Most steps are far below 1, so u and its log1p have to be
+// good relative to themselves: the product |v| log2(e) is carried to twice its
+// digits, and log1p(u) = 2 artanh(u / (2 + u)) as its series in z = u / (2 + u)
+// <= 1/3 (z^15 / 15 left out, 1e-8 of the sum).  A few 2^-24 in all.
+__device__ __forceinline__ float dt_plain_above(int softplus) { return softplus ? 20.0f : -__builtin_inff(); }
+__device__ __forceinline__ float softplus_f32(float v, float plain)
+{
+    const float n = v < -150.0f ? -150.0f : -fabsf(v), hi = n * kLog2eF;  // e^-150 is 0
+    const float lo = fmaf(n, 1.92596303e-8f, fmaf(n, kLog2eF, -hi));  // log2(e) = kLog2eF + 1.93e-8
+    const float e = exp2_f32(hi), u = fmaf(e, lo * 0.693147181f, e);
+    const float z = u * __builtin_amdgcn_rcpf(2.0f + u), w = z * z;
+    float s = fmaf(w, 1.0f / 13, 1.0f / 11);
+    s = fmaf(w, s, 1.0f / 9);
+    s = fmaf(w, s, 1.0f / 7);
+    s = fmaf(w, s, 1.0f / 5);
+    s = fmaf(w, s, 1.0f / 3);
+    s = 2.0f * fmaf(w * z, s, z);
+    return v > plain ? v : fmaxf(v, 0.0f) + s;
+}
+
 // Sequences are cut into tiles of `len` tokens that start at the sequence's
 // first token.  In a batch every sequence has ceil(T / len) tiles (one if
 // T = 0).  Packed sequence n owns the slots from cu[n] / len + n on: at least
@@ -145,51 +168,55 @@ __device__ __forceinline__ float silu_f32(float x) { return x * sigmoid_f32(x); 
 // can size the grid (T / len + N slots) without reading cu_seqlens, and a
 // slot finds its sequence by search.
 struct Tile {
-    int64_t n, begin, end, row;  // sequence, its token range, its batch row
-    int64_t index;               // tile within the sequence; its tokens may be none
-    bool valid;                  // false: a slot no tile uses
+    int64_t n, row;       // sequence, its batch row
+    uint32_t begin, end;  // its tokens
+    uint32_t index;       // tile within the sequence; its tokens may be none
+    bool valid;           // false: a slot no tile uses
 };
 
-__device__ __forceinline__ int64_t clamp_offset(const Seqs &s, int64_t n)
+// Offsets are at most T < 2^31, and so are slots (the grid's limit): all of
+// this is 32-bit arithmetic.
+__device__ __forceinline__ uint32_t clamp_offset(const Seqs &s, int64_t n)
 {
     const int64_t v = s.cu[n];
-    return v < 0 ? 0 : (v > s.T ? s.T : v);
+    return static_cast<uint32_t>(v < 0 ? 0 : (v > s.T ? s.T : v));
 }
 
-__device__ __forceinline__ Tile find_tile(const Seqs &s, int64_t len, int64_t slot)
+__device__ __forceinline__ Tile find_tile(const Seqs &s, uint32_t len, uint32_t slot)
 {
     Tile t;
     if (!s.cu) {
-        const int64_t per = s.T > 0 ? (s.T + len - 1) / len : 1;
-        t.n = slot / per;
-        t.index = slot - t.n * per;
+        const uint32_t T = static_cast<uint32_t>(s.T), per = T > 0 ? (T + len - 1) / len : 1, n = slot / per;
+        t.n = n;
+        t.row = n;
+        t.index = slot - n * per;
         t.begin = 0;
-        t.end = s.T;
-        t.row = t.n;
+        t.end = T;
         t.valid = true;
         return t;
     }
     // the last n with cu[n] / len + n <= slot; 64 probes a round.  Offsets
     // out of order still end at some n in [0, N).
-    const int lane = static_cast<int>(__lane_id());
-    int64_t lo = 0, hi = s.N;
+    const uint32_t lane = __lane_id();
+    uint32_t lo = 0, hi = static_cast<uint32_t>(s.N);
     while (hi - lo > 1) {
-        const int64_t step = (hi - lo + 63) / 64, n = lo + lane * step;
+        const uint32_t step = (hi - lo + 63) / 64, n = lo + lane * step;
         const bool below = n < hi && clamp_offset(s, n) / len + n <= slot;
-        const int count = __popcll(__ballot(below));
+        const uint32_t count = __popcll(__ballot(below));
         if (count == 0)
             break;
         lo += (count - 1) * step;
         hi = hi < lo + step ? hi : lo + step;
     }
     t.n = lo;
+    t.row = 0;
     t.begin = clamp_offset(s, lo);
     t.end = clamp_offset(s, lo + 1);
     if (t.end < t.begin)
         t.end = t.begin;
-    t.row = 0;
-    t.index = slot - (t.begin / len + lo);
-    t.valid = t.index == 0 || (t.index > 0 && t.index < (t.end - t.begin + len - 1) / len);
+    const uint32_t first = t.begin / len + lo;
+    t.index = slot - first;
+    t.valid = slot == first || (slot > first && t.index < (t.end - t.begin + len - 1) / len);
     return t;
 }
 

@@ -99,8 +99,8 @@ constexpr int64_t kSsmRecurrentMaxTokens = 8;
 
 hipError_t launch_ssm_recurrent(const SsmParams &p, hipStream_t stream);
 hipError_t launch_ssm_chunk(const SsmParams &p, hipStream_t stream);
-// Units of 32 columns a workgroup of the chunked kernel takes.
-constexpr int64_t kSsmUnits = 8;
+// Waves of a workgroup of the chunked kernel, and columns a wave takes.
+constexpr int64_t kSsmWaves = 8, kSsmColumns = 32;
 
 }  // namespace layer
 }  // namespace kda

@@ -25,14 +25,13 @@ constexpr int kTile = 32;  // tokens a tile, >= kMaxTaps - 1
 constexpr int kBatch = 4;  // rows in flight
 
 template <int W>
-__global__ __launch_bounds__(64 * kWaves) void conv_kernel(ConvParams p, int64_t tasks, int cblocks)
+__global__ __launch_bounds__(64 * kWaves) void conv_kernel(ConvParams p, uint32_t tasks, uint32_t cblocks)
 {
     const int lane = threadIdx.x & 63;
-    const int64_t task = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + (threadIdx.x >> 6));
+    const uint32_t task = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + (threadIdx.x >> 6));
     if (task >= tasks)
         return;
-    const int64_t slot = task / cblocks;
-    const int cb = static_cast<int>(task - slot * cblocks);
+    const uint32_t slot = task / cblocks, cb = task - slot * cblocks;
     const Tile tile = find_tile(p.seqs, kTile, slot);
     const int64_t c0 = (static_cast<int64_t>(cb) * 64 + lane) * 8;
     const int count = static_cast<int>(p.D - c0 < 8 ? p.D - c0 : 8);
@@ -40,8 +39,8 @@ __global__ __launch_bounds__(64 * kWaves) void conv_kernel(ConvParams p, int64_t
         return;
 
     const int64_t len = tile.end - tile.begin;
-    const int64_t t0 = tile.index * kTile, t1 = t0 + kTile < len ? t0 + kTile : len;
-    const uint16_t *x = p.x + tile.row * p.xb + tile.begin * p.xt + c0;  // token 0 of the sequence
+    const int64_t t0 = static_cast<int64_t>(tile.index) * kTile, t1 = t0 + kTile < len ? t0 + kTile : len;
+    const uint16_t *x = p.x + tile.row * p.xb + static_cast<int64_t>(tile.begin) * p.xt + c0;  // token 0 of the sequence
     uint16_t *out = p.out + (tile.row * p.seqs.T + tile.begin) * p.D + c0;
 
     float win[W - 1 + kBatch][8];  // rows t - W + 1 .. t + kBatch - 1
@@ -145,8 +144,8 @@ hipError_t launch(const ConvParams &p, hipStream_t stream)
     const int64_t blocks = (tasks + kWaves - 1) / kWaves;
     if (blocks > INT32_MAX / kWaves)
         return hipErrorInvalidConfiguration;
-    conv_kernel<W><<<dim3(static_cast<uint32_t>(blocks)), dim3(64 * kWaves), 0, stream>>>(p, tasks,
-                                                                                          static_cast<int>(cblocks));
+    conv_kernel<W><<<dim3(static_cast<uint32_t>(blocks)), dim3(64 * kWaves), 0, stream>>>(
+        p, static_cast<uint32_t>(tasks), static_cast<uint32_t>(cblocks));
     return hipGetLastError();
 }
 

@@ -1,25 +1,34 @@
-// The selective state space scan in chunks of 32 tokens on matrix
-// instructions.  Per head, with a_t = -e^A_log log2(e) dt_t, G_t the sum of a
-// over the chunk up to and with token t, R_t the sum over the tokens after t
-// and S the state [P, N] in front of the chunk:
-//   M[t,s] = (c_t . b_s) dt_s 2^(G_t - G_s)  (s <= t),  M[t,t] += D
-//   y_t    = 2^(G_t) S c_t + sum_s M[t,s] x_s,  out_t = y_t silu(z_t)
-//   S     <- 2^(G_last) S + sum_s (dt_s 2^(R_s) x_s) b_s^T
-// No exponent is positive, so nothing overflows however strong the decay.  A
-// difference of G loses what a strong decay in the same chunk rounds away, so
-// G is held in fixed point: 32-bit integers in a unit of 2^-29 .. 2^-30 of the
-// chunk's sum of |a|, whose sums and differences are exact.  Decays below
+// The selective state space scan in tiles of 64 tokens, two blocks of 32, on
+// matrix instructions.  Per head, with a_t = -e^A_log log2(e) dt_t, G_t the
+// sum of a over the block up to and with token t, R_t the sum over its tokens
+// after t, T the whole block's sum, w_t = dt_t 2^(R_t), and S the state [P, N]
+// in front of the tile:
+//   first block   y_t = 2^(G_t) S c_t + sum_(s <= t) (c_t . b_s) 2^(G_t - G_s) dt_s x_s
+//   second block  y_t = 2^(G_t) (2^(T_0) S c_t + sum_(first block) (c_t . b_s) w_s x_s)
+//                       + the same sum over its own tokens
+//   out_t = (y_t + D x_t) silu(z_t)
+//   S <- 2^(T_1) (2^(T_0) S + sum_0 w_s x_s b_s^T) + sum_1 w_s x_s b_s^T
+// Since 2^(G_t - G_s) dt_s = 2^(G_t - T) w_s, the sum over a block's own tokens
+// takes the same weighted x as the state: 2^(G_t - T) sum (c_t . b_s) w_s x_s,
+// and c b^T, which the heads of a group share, is the other factor.  That
+// holds while 2^-T stays well inside fp32's range; a block that decays by more
+// than 2^-64 forms M[t,s] = (c_t . b_s) 2^(G_t - G_s) dt_s itself (a third more
+// vector work for that block).  No other exponent is positive, so nothing
+// overflows however strong the decay.
+//
+// A difference of G loses what a strong decay in the same block rounds away,
+// so G is held in fixed point: 32-bit integers in a unit of 2^-29 .. 2^-30 of
+// the block's sum of |a|, whose sums and differences are exact.  Decays below
 // 2^-160 count as that (both are 0 in fp32), so a unit is at most 2^-17.  R is
-// summed in fp32 from the chunk's end, so that the weights of the newest
+// summed in fp32 from the block's end, so that the weights of the newest
 // tokens, which make up most of the state, are the most exact.
 //
 // One wave owns a unit: 32 of a head's P columns, with the fp32 state [32, N]
 // in accumulators for a whole segment of the sequence.  A workgroup of eight
 // waves takes eight consecutive units of one group (P = 64: four heads), which
-// share b and c.  Tiles of 64 tokens (two chunks) of b, c and x go through
-// registers into LDS, the next tile's loads in flight while this one is
-// computed; the products c b^T are formed once per workgroup, one 16 x 16 tile
-// a wave.  x is read from memory once per pass, 64 bytes a token and unit.
+// share b, c and c b^T (formed once a tile, 16 x 16 tiles spread over the
+// waves).  b, c and x go through registers into LDS, the next tile's loads in
+// flight while this one is computed.  x is read from memory once per pass.
 //
 // Operands.  v_mfma_f32_32x32x16_bf16 contracts 16 slots; lane (l32, half)
 // holds slots 8 half .. 8 half + 7 of row / column l32, and accumulator
@@ -27,18 +36,18 @@
 // slot stands for is free as long as both operands agree:
 //   over n:  slot e of step (tile, j) is n = 32 tile + 16 j + 8 (e / 4) + 4 half + e % 4,
 //            so a state accumulator is the operand as it stands;
-//   over s:  slot e of step j is s = 8 (e % 4) + 4 half + 2 j + e / 4, so M as
-//            the product c b^T leaves it is the operand, and the four tokens a
-//            transposing LDS read takes are 8 rows apart, which with rows of
-//            2 mod 16 dwords puts them in distinct banks.
+//   over s:  slot e of step j is s = 8 (e % 4) + 4 half + 2 j + e / 4, the order
+//            of an accumulator over s, and the four tokens a transposing LDS
+//            read takes are 8 rows apart, which with rows of 2 mod 16 dwords
+//            puts them in distinct banks.
 // Row / column l32 of the unit stands for column p = 16 ((l32 >> 2) & 1) +
 // 4 (l32 >> 3) + l32 % 4, so that a lane ends with 16 adjacent columns of its
 // token's output.
 //
-// x, b and c are bf16 and enter as they are.  M, the state and the weighted x
-// are fp32 and enter as two bf16 parts (the value rounded, and the rest
-// rounded: good to 2^-16 of itself), so the state keeps fp32's accuracy to
-// better than 2^-18 over its norm and out is good to its one final rounding.
+// x, b and c are bf16 and enter as they are.  Of the fp32 factors, S, c b^T and
+// M enter as two bf16 parts (the value rounded, and the rest rounded: good to
+// 2^-16 of itself), which leaves out its one final rounding; the weighted x
+// enters the state as three (2^-24), so the state is as exact as fp32.
 #include "layer_device.h"
 
 namespace kda {
@@ -50,9 +59,19 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int CH = static_cast<int>(kSsmChunk);
-constexpr int TM = 2 * CH;  // tokens a tile
-constexpr int NW = 8;       // waves, units a workgroup
+constexpr int CH = static_cast<int>(kSsmChunk);  // tokens a block
+constexpr int TM = 2 * CH;                       // tokens a tile
+constexpr int NW = static_cast<int>(kSsmWaves);  // waves, units a workgroup
+constexpr float kSteep = -80.0f;                 // tiles that decay by more form M
+// Log decays from a block to the tile's or segment's end.  Up to kFaint its
+// weighted x enters the state in two parts: their rounding, 2^-16 of the block's
+// own contribution, is below 2^-20 of what the newest tokens bring.  Below
+// kNothing the weights are 0 in fp32 whatever finite x and b they meet.
+constexpr float kFaint = -4.0f, kNothing = -300.0f;
+template <int V>
+struct Int {
+    constexpr int operator()() const { return V; }
+};
 constexpr int kThreads = 64 * NW;
 constexpr int kXPitch = NW * 32 + 4;  // bf16 elements of an x row in LDS
 
@@ -81,17 +100,33 @@ __device__ __forceinline__ void lds_barrier()
 {
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
-// v = hi + lo, each rounded to bf16.
-__device__ __forceinline__ void split8(const float v[8], bf16x8_t *hi, bf16x8_t *lo)
+// Nothing is scheduled across this.
+__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
+// x, computed here and not before: what is derived from it inside a loop stays
+// there instead of occupying a register through all of it.
+__device__ __forceinline__ int here(int x)
 {
-    u32x4_t h, l;
+    asm volatile("" : "+v"(x));
+    return x;
+}
+__device__ __forceinline__ const char *bytes(const uint16_t *p) { return reinterpret_cast<const char *>(p); }
+// v as the sum of parts[0..PARTS-1], each the rest rounded to bf16.
+template <int PARTS>
+__device__ __forceinline__ void split8(float v[8], bf16x8_t parts[PARTS])
+{
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        h[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-        l[i] = pack_bf16x2(v[2 * i] - lo_f32(h[i]), v[2 * i + 1] - hi_f32(h[i]));
+    for (int k = 0; k < PARTS; ++k) {
+        u32x4_t h;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+            if (k + 1 < PARTS) {
+                v[2 * i] -= lo_f32(h[i]);
+                v[2 * i + 1] -= hi_f32(h[i]);
+            }
+        }
+        parts[k] = __builtin_bit_cast(bf16x8_t, h);
     }
-    *hi = __builtin_bit_cast(bf16x8_t, h);
-    *lo = __builtin_bit_cast(bf16x8_t, l);
 }
 
 template <int CTRL, int ROWS>
@@ -131,18 +166,22 @@ __device__ __forceinline__ float after32(float x, int lane)
     return x + ((lane & 16) ? 0.0f : (lane < 32 ? r1 : r3));
 }
 
-__device__ __forceinline__ float softplus_f32(float v) { return v > 20.0f ? v : log1pf(expf(v)); }
-
 template <int N, bool OUT>
 struct Shared {
     static constexpr int kPitch = N + 4;
-    uint16_t b[TM][kPitch];
-    uint16_t c[OUT ? TM : 1][kPitch];
-    uint16_t x[TM][kXPitch];
-    float cb[OUT ? TM / CH : 1][CH][CH + 4];  // [t][s] = c_t . b_s of a chunk
-    // per wave and token: G in its chunk's units, dt, dt 2^R
-    int g[NW][TM];
-    float d[NW][TM], w[NW][TM];
+    alignas(16) uint16_t b[TM][kPitch];
+    alignas(16) uint16_t c[OUT ? TM : 1][kPitch];
+    alignas(16) uint16_t x[TM][kXPitch];
+    // c_t . b_s as an operand, [rounded, rest][j][half][t][slot]: the first
+    // block with itself, the second with itself, the second's t with the first's s
+    alignas(16) uint16_t cb[OUT ? 3 : 1][2][2][2][CH][8];
+    // per head of the workgroup, for the tiles in turn: G of a token in its
+    // block's unit, dt, w; the blocks' T and units
+    alignas(16) int g[2][NW][OUT ? TM : 4];
+    alignas(16) float d[2][NW][OUT ? TM : 4];
+    alignas(16) float w[2][NW][TM];
+    float total[2][NW][2], unit[2][NW][2];
+    float dt_plain;  // dt + bias above this is taken as it is
 };
 
 // Column of a unit that row / column l32 of its matrices stands for.
@@ -190,51 +229,61 @@ __device__ __forceinline__ void store_state(void *base, int kind, int64_t at, co
 
 // OUT: the pass that writes out (and the final state).  Otherwise the pass
 // that forms every segment's own state (from zero) and decay, for all
-// segments but a sequence's last.
+// segments but a sequence's last; it walks the tiles backwards with weights up
+// to the segment's end, so that the accumulators never decay.
 template <int N, bool OUT>
 __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int units, int ublocks)
 {
-    constexpr int NT = N / 32, PB = N / 8;                 // state tiles; 16-byte pieces of a b row
+    constexpr int NT = N / 32, PB = N / 8, PX = NW * 4;  // state tiles; 16-byte pieces of a b and an x row
     // tokens of b (and c) and of x that the threads load at once, and how often
     constexpr int SB = kThreads / PB < TM ? kThreads / PB : TM, kLoadB = TM / SB;
-    constexpr int SX = kThreads / (NW * 4), kLoadX = TM / SX;
+    constexpr int SX = kThreads / PX, kLoadX = TM / SX;
     constexpr int kPitch = Shared<N, OUT>::kPitch;
+    constexpr int kStep = OUT ? TM : -TM;
+    // With 256 state columns the registers hold no tile in flight.
+    constexpr bool kAhead = N <= 128 || !OUT;
     __shared__ __align__(16) Shared<N, OUT> sh;
 
-    const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, half = lane >> 5, l16 = lane & 15, odd = (lane >> 4) & 1;
+    const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t gb = p.G * ublocks;
-    const int64_t slot = blockIdx.x / gb;
-    const int rest = static_cast<int>(blockIdx.x - slot * gb), grp = rest / ublocks, ub = rest - grp * ublocks;
-    const Tile tile = find_tile(p.seqs, p.seg, slot);
-    const int64_t t0 = tile.index * p.seg, left = tile.end - tile.begin - t0;
-    const bool last = left <= p.seg;
+    const uint32_t gb = static_cast<uint32_t>(p.G) * ublocks, slot = blockIdx.x / gb, in_slot = blockIdx.x - slot * gb;
+    const int grp = in_slot / ublocks, ub = in_slot - grp * ublocks;
+    const uint32_t seg = static_cast<uint32_t>(p.seg);
+    const Tile tile = find_tile(p.seqs, seg, slot);
+    const uint32_t t0 = tile.index * seg, left = tile.end - tile.begin - t0;
+    const bool last = left <= seg;
     if (!tile.valid || (!OUT && last))
         return;
-    const int tokens = static_cast<int>(last ? left : p.seg);  // of this segment
+    const int tokens = static_cast<int>(last ? left : seg);  // of this segment
 
-    const int u = ub * NW + wave;  // unit within the group
+    const int u0 = ub * NW, u = u0 + wave;  // units within the group
     const bool active = u < units;
     const int per_head = static_cast<int>(p.P / 32);
-    const int hg = (active ? u : 0) / per_head, colblk = (active ? u : 0) - hg * per_head;
-    const int64_t h = grp * (p.H / p.G) + hg;
-    const int64_t first = tile.begin + t0;                  // the segment's first token in its row
-    const int64_t col = h * p.P + colblk * 32 + 16 * half;  // the lane's first output column
-    // This thread's places in memory: piece 0 of a tile's b, c and x, the
-    // token `lane` of dt, the token l32 of z and out; they advance by chunks
-    // or tiles.
-    const int bt0 = tid / PB, bc0 = tid % PB * 8, xt0 = tid / (NW * 4), xc0 = tid % (NW * 4) * 8;
-    const uint16_t *bp = p.b + tile.row * p.bb + (first + bt0) * p.bt + static_cast<int64_t>(grp) * N + bc0;
-    const uint16_t *cp = p.c + tile.row * p.cb + (first + bt0) * p.ct + static_cast<int64_t>(grp) * N + bc0;
-    const uint16_t *xp = p.x + tile.row * p.xb + (first + xt0) * p.xt + (static_cast<int64_t>(grp) * units + ub * NW) * 32 + xc0;
-    const uint16_t *dp = p.dt + tile.row * p.db + (first + lane) * p.dtt + h;
-    const uint16_t *zp = OUT && p.z ? p.z + tile.row * p.zb + (first + l32) * p.zt + col : nullptr;
-    uint16_t *op = p.out + (tile.row * p.seqs.T + first + l32) * p.H * p.P + col;
-    const int64_t state_at = ((tile.n * p.H + h) * p.P + colblk * 32 + unit_column(l32)) * N + 4 * half;
-    float *slab = p.slabs + ((slot * p.H + h) * p.P + colblk * 32) * N + 4 * lane;  // [NT * 4][lane][4]
+    const int head0 = u0 / per_head, heads = ((u0 + NW < units ? u0 + NW : units) - 1) / per_head - head0 + 1;
+    const int hg = active ? u / per_head : head0, colblk = active ? u - hg * per_head : 0, hs = hg - head0;
+    const int h = grp * static_cast<int>(p.H / p.G) + hg, width = static_cast<int>(p.H * p.P);
+    const int64_t first = static_cast<int64_t>(tile.begin) + t0;               // the segment's first token in its row
+    const int start = OUT ? 0 : (tokens - 1) / TM * TM;  // the first tile walked
+    const bool keeps_dt = wave < heads;                  // wave k < heads: works out head k's decays
+    const int dh = h - hg + head0 + (keeps_dt ? wave : 0);
+    // Places in memory: a base per wave, which moves with the tiles, and 32-bit
+    // lane offsets.  Of a tile's b, c and x a wave loads whole rows of 16-byte
+    // pieces; of z and out, lane (l32, half) takes 16 columns of token l32.
+    const int wb = wave * (64 / PB), wx0 = wave * (64 / PX);  // the first row of either kind
+    const char *bp = bytes(p.b + tile.row * p.bb + (first + start + wb) * p.bt + grp * N);
+    const char *cp = bytes(p.c + tile.row * p.cb + (first + start + wb) * p.ct + grp * N);
+    const char *xp = bytes(p.x + tile.row * p.xb + (first + start + wx0) * p.xt + (grp * units + u0) * 32);
+    const char *dp = bytes(p.dt + tile.row * p.db + (first + start) * p.dtt + dh);
+    const int wcol = h * static_cast<int>(p.P) + colblk * 32;  // the unit's first output column
+    const char *zp = OUT && p.z ? bytes(p.z + tile.row * p.zb + first * p.zt + wcol) : nullptr;
+    char *op = reinterpret_cast<char *>(p.out + (tile.row * p.seqs.T + first) * width + wcol);
+    // The unit in the states, and in the slabs [H][P / 32][4 N / 32][lane][4].
+    const int64_t state_at = ((tile.n * p.H + h) * p.P + colblk * 32) * N;
+    float *const slab = p.slabs + ((static_cast<int64_t>(slot) * p.H + h) * p.P + colblk * 32) * N;
 
-    const float rate = -expf(p.A_log[h]) * kLog2eF;
-    const float dt_bias = p.dt_bias ? p.dt_bias[h] : 0.0f, skip = OUT && p.D ? p.D[h] : 0.0f;
+    const float rate = -expf(p.A_log[dh]) * kLog2eF;
+    const float dt_bias = p.dt_bias ? p.dt_bias[dh] : 0.0f;
+    const float skip = OUT && p.D ? p.D[h] : 0.0f;
 
     f32x16_t s[NT];
     if (OUT && active && p.slabs) {
@@ -242,243 +291,462 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const f32x4_t v = *reinterpret_cast<const f32x4_t *>(slab + (4 * nt + i) * 256);
+                const f32x4_t v = *reinterpret_cast<const f32x4_t *>(slab + (4 * nt + i) * 256 + 4 * lane);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) s[nt][4 * i + q] = v[q];
             }
     } else {
-        load_state<N>(p.init_state, OUT && active ? p.init_kind : kNone, state_at, s);
+        load_state<N>(p.init_state, OUT && active ? p.init_kind : kNone,
+                      state_at + unit_column(lane & 31) * N + 4 * (lane >> 5), s);
     }
-    float log_sum = 0.0f;
-    float diag[16];  // D where row s = 8 i + 4 half + q is the lane's own token
+    // Where the unit's final state goes, if it does; bit 0: in bf16.
+    char *final_at = nullptr;
+    if (OUT && last && p.final_state)
+        final_at = static_cast<char *>(p.final_state) + (p.final_kind == kFp32 ? 4 * state_at : 2 * state_at + 1);
+    if (OUT && tid < 256) {
+        // c b^T is 0 above the diagonal; a block's upper right 16 x 16 is never
+        // written again: t < 16, s >= 16 are slots e with e % 4 >= 2
+        const int part = tid >> 7, blk = (tid >> 6) & 1, j = (tid >> 5) & 1, hf = (tid >> 4) & 1;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) diag[r] = 8 * (r >> 2) + 4 * half + (r & 3) == l32 ? skip : 0.0f;
+        for (int e = 0; e < 8; ++e)
+            if (e & 2)
+                sh.cb[blk][part][j][hf][tid & 15][e] = 0;
+    }
 
     u32x4_t rb[kLoadB], rc[OUT ? kLoadB : 1], rx[kLoadX];
     uint32_t rdt = 0;
-    const bool x_here = xc0 < units * 32 - ub * NW * 32;  // a column of a unit that exists
-    // Loads the tile from token tt on (of which `tokens - tt` exist) and moves on to the next.
+    float after = 0.0f;  // sum of a over the tiles after this one (!OUT; this wave's dt head)
+    // Loads the tile from token tt on and moves on to the next.
     const auto fetch = [&](int tt) {
+        const int ln = here(lane), bt0 = wb + ln / PB, xt0 = wx0 + ln / PX;
+        const uint32_t b_off = 2 * (ln / PB * static_cast<uint32_t>(p.bt) + ln % PB * 8);
+        const uint32_t c_off = 2 * (ln / PB * static_cast<uint32_t>(p.ct) + ln % PB * 8);
+        const uint32_t x_off = 2 * (ln / PX * static_cast<uint32_t>(p.xt) + ln % PX * 8);
+        const bool x_here = ln % PX * 8 < (units - u0) * 32;  // a column of a unit that exists
+        const char *bq = bp, *cq = cp, *xq = xp;
+        if (tt + TM <= tokens) {
 #pragma unroll
-        for (int k = 0; k < kLoadB; ++k) {
-            const bool ok = bt0 < SB && tt + bt0 + k * SB < tokens;
-            rb[k] = ok ? *reinterpret_cast<const u32x4_a2 *>(bp) : u32x4_t{0, 0, 0, 0};
-            bp += SB * p.bt;
-            if constexpr (OUT) {
-                rc[k] = ok ? *reinterpret_cast<const u32x4_a2 *>(cp) : u32x4_t{0, 0, 0, 0};
-                cp += SB * p.ct;
+            for (int k = 0; k < kLoadB; ++k) {
+                if (SB * PB == kThreads || bt0 < SB) {
+                    rb[k] = *reinterpret_cast<const u32x4_a2 *>(bq + b_off);
+                    if constexpr (OUT)
+                        rc[k] = *reinterpret_cast<const u32x4_a2 *>(cq + c_off);
+                }
+                bq += 2 * SB * p.bt;
+                cq += 2 * SB * p.ct;
+            }
+#pragma unroll
+            for (int k = 0; k < kLoadX; ++k) {
+                if (x_here)
+                    rx[k] = *reinterpret_cast<const u32x4_a2 *>(xq + x_off);
+                xq += 2 * SX * p.xt;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kLoadB; ++k) {
+                const bool ok = bt0 < SB && tt + bt0 + k * SB < tokens;
+                rb[k] = ok ? *reinterpret_cast<const u32x4_a2 *>(bq + b_off) : u32x4_t{0, 0, 0, 0};
+                if constexpr (OUT)
+                    rc[k] = ok ? *reinterpret_cast<const u32x4_a2 *>(cq + c_off) : u32x4_t{0, 0, 0, 0};
+                bq += 2 * SB * p.bt;
+                cq += 2 * SB * p.ct;
+            }
+#pragma unroll
+            for (int k = 0; k < kLoadX; ++k) {
+                const bool ok = x_here && tt + xt0 + k * SX < tokens;
+                rx[k] = ok ? *reinterpret_cast<const u32x4_a2 *>(xq + x_off) : u32x4_t{0, 0, 0, 0};
+                xq += 2 * SX * p.xt;
             }
         }
-#pragma unroll
-        for (int k = 0; k < kLoadX; ++k) {
-            const bool ok = x_here && tt + xt0 + k * SX < tokens;
-            rx[k] = ok ? *reinterpret_cast<const u32x4_a2 *>(xp) : u32x4_t{0, 0, 0, 0};
-            xp += SX * p.xt;
+        bp += 2 * kStep * p.bt;
+        cp += 2 * kStep * p.ct;
+        xp += 2 * kStep * p.xt;
+    };
+    // dt of the tile from token tt on, loaded one step ahead of its use
+    const auto fetch_dt = [&](int tt) {
+        const int ln = here(lane);
+        rdt = 0;
+        if (keeps_dt && tt >= 0 && tt + ln < tokens)
+            rdt = *reinterpret_cast<const uint16_t *>(dp + 2 * ln * p.dtt);
+        dp += 2 * kStep * p.dtt;
+    };
+    // What the loaded dt of the tile from token tt on comes to, into its half of the buffers.
+    const auto step_dt = [&](int tt, float plain) {
+        const int ln = here(lane), buf = (tt / TM) & 1;
+        const float raw = bf16_to_f32(static_cast<uint16_t>(rdt)) + dt_bias;
+        const float dt = tt + ln < tokens ? softplus_f32(raw, plain) : 0.0f;
+        const float a = fmaxf(rate * dt, -160.0f);
+        float r = after32(a, ln);
+        if constexpr (OUT) {
+            const float abs_sum = prefix32(fabsf(a));
+            const float s0 = read_lane(abs_sum, 31), s1 = read_lane(abs_sum, 63);
+            // 2^e <= sum < 2^(e + 1): a unit of 2^(e - 29)
+            const uint32_t e = __float_as_uint(fmaxf(ln < 32 ? s0 : s1, 0x1p-60f)) & 0x7f800000u;
+            const float unit = __uint_as_float(e - (29u << 23));
+            const int g = prefix32(static_cast<int>(rintf(a * __uint_as_float((254u << 23) - e + (29u << 23)))));
+            sh.g[buf][wave][ln] = g;
+            sh.d[buf][wave][ln] = dt;
+            const float total = unit * static_cast<float>(g);
+            if ((ln & 31) == 31) {
+                sh.unit[buf][wave][ln >> 5] = unit;
+                sh.total[buf][wave][ln >> 5] = total;
+            }
+            // a gentle tile weighs its first block up to the tile's end
+            const float b1 = read_lane(r + a, 32), both = read_lane(total, 31) + read_lane(total, 63);
+            r += ln < 32 && kAhead && both >= kSteep ? b1 : 0.0f;
+        } else {
+            // from the block's end to the segment's
+            const float b0 = read_lane(r + a, 0), b1 = read_lane(r + a, 32);
+            if (ln == 0) {
+                sh.total[buf][wave][0] = b1 + after;
+                sh.total[buf][wave][1] = after;
+            }
+            r += ln < 32 ? b1 + after : after;
+            after += b0 + b1;
         }
-        rdt = tt + lane < tokens ? *dp : 0;
-        dp += TM * p.dtt;
+        sh.w[buf][wave][ln] = dt * exp2_f32(r);
     };
     const auto put = [](uint16_t *dst, u32x4_t v) {  // rows are 8-byte aligned
         *reinterpret_cast<u32x2_t *>(dst) = u32x2_t{v[0], v[1]};
         *reinterpret_cast<u32x2_t *>(dst + 4) = u32x2_t{v[2], v[3]};
     };
 
-    // With 256 state columns the registers hold no tile in flight.
-    constexpr bool kAhead = N <= 128 || !OUT;
-    if (kAhead && tokens > 0)
-        fetch(0);
-    // lane parts of the LDS addresses: the transposing reads of b and x, the plain reads of c
-    const uint32_t b_tr = lds_addr(&sh.b[4 * half + 8 * (l16 >> 2)][16 * odd + 4 * (l16 & 3)]);
-    const int kappa = 4 * odd + (l16 & 3);
-    const uint32_t x_tr = lds_addr(&sh.x[4 * half + 8 * (l16 >> 2)][wave * 32 + 16 * (kappa & 1) + 4 * (kappa >> 1)]);
+    if (tokens > 0) {
+        fetch_dt(start);
+        if (kAhead)
+            fetch(start);
+        const float plain = dt_plain_above(p.softplus);
+        if (tid == 0)
+            sh.dt_plain = plain;
+        if (keeps_dt)
+            step_dt(start, plain);
+        fetch_dt(start + kStep);
+    }
+    // The tiles of c b^T this wave forms: two for a wave without a head, the
+    // rest for the others.
+    const int spare = NW - heads, share = 2 * spare < 10 ? 2 * spare : 10;
+    int ids = 0xffff;
+    if (OUT) {
+        for (int id = 0; id < 10; ++id)
+            if (wave == (id < share ? heads + id % spare : (id - share) % heads))
+                ids = (ids << 8 | id) & 0xffff;
+    }
 
-    for (int tt = 0; tt < tokens; tt += TM) {
+    for (int tt = start; OUT ? tt < tokens : tt >= 0; tt += kStep) {
+        if (tokens == 0)
+            break;
         if (!kAhead)
             fetch(tt);
-#pragma unroll
-        for (int k = 0; k < kLoadB; ++k) {
-            if (bt0 < SB) {
-                put(&sh.b[bt0 + k * SB][bc0], rb[k]);
-                if constexpr (OUT)
-                    put(&sh.c[bt0 + k * SB][bc0], rc[k]);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < kLoadX; ++k) {
-            put(&sh.x[xt0 + k * SX][xc0], rx[k]);
-        }
-        int g;       // of token tt + lane within its chunk, in units of
-        float unit;  // this many bits (the chunk's lanes share it)
         {
-            const float raw = bf16_to_f32(static_cast<uint16_t>(rdt)) + dt_bias;
-            const float dt = tt + lane < tokens ? (p.softplus ? softplus_f32(raw) : raw) : 0.0f;
-            const float a = fmaxf(rate * dt, -160.0f);
-            const float abs_sum = prefix32(fabsf(a));
-            const float s0 = read_lane(abs_sum, 31), s1 = read_lane(abs_sum, 63);
-            // 2^e <= sum < 2^(e + 1): a unit of 2^(e - 29)
-            const uint32_t e = __float_as_uint(fmaxf(lane < 32 ? s0 : s1, 0x1p-60f)) & 0x7f800000u;
-            unit = __uint_as_float(e - (29u << 23));
-            g = prefix32(static_cast<int>(rintf(a * __uint_as_float((254u << 23) - e + (29u << 23)))));
-            sh.g[wave][lane] = g;
-            sh.d[wave][lane] = dt;
-            sh.w[wave][lane] = dt * exp2_f32(after32(a, lane));
+            const int ln = here(lane), bt0 = wb + ln / PB, bc0 = ln % PB * 8;
+#pragma unroll
+            for (int k = 0; k < kLoadB; ++k) {
+                if (SB * PB == kThreads || bt0 < SB) {
+                    put(&sh.b[bt0 + k * SB][bc0], rb[k]);
+                    if constexpr (OUT)
+                        put(&sh.c[bt0 + k * SB][bc0], rc[k]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kLoadX; ++k) put(&sh.x[wx0 + ln / PX + k * SX][ln % PX * 8], rx[k]);
         }
         lds_barrier();
-        if (kAhead && tt + TM < tokens)
-            fetch(tt + TM);
+        const int buf = (tt / TM) & 1;
+        const bool more = OUT ? tt + TM < tokens : tt > 0;
+        // The next tile's dt, and this one's c b^T, a wave each where it can be.
+        if (more) {
+            if (keeps_dt)
+                step_dt(tt + kStep, sh.dt_plain);
+            fetch_dt(tt + 2 * kStep);
+        }
         if constexpr (OUT) {
-            // c b^T: wave w forms rows 16 (w >> 1 & 1) .. of t, columns 16 (w & 1) .. of s of chunk w >> 2
-            const int q = wave >> 2, ts = 16 * ((wave >> 1) & 1), ss = 16 * (wave & 1);
-            if (ss > ts) {
-                *reinterpret_cast<f32x4_t *>(&sh.cb[q][ts + l16][ss + 4 * (lane >> 4)]) = f32x4_t{0, 0, 0, 0};
-            } else {
+            const int ln = here(lane), l16 = ln & 15, g4 = ln >> 4;
+            for (int k = 0; k < 2; ++k) {
+                const int id = (ids >> (8 * k)) & 0xff;
+                if (id == 0xff)
+                    break;
+                const int ti = id < 1 ? 0 : (id < 3 ? 1 : (id < 6 ? 2 : 3)), si = id - ti * (ti + 1) / 2;
                 f32x4_t acc = {0, 0, 0, 0};
 #pragma unroll
-                for (int k = 0; k < NT; ++k) {
-                    const uint16_t *pb = &sh.b[CH * q + ss + l16][32 * k + 8 * (lane >> 4)];
-                    const uint16_t *pc = &sh.c[CH * q + ts + l16][32 * k + 8 * (lane >> 4)];
+                for (int n = 0; n < NT; ++n) {
+                    const uint16_t *pb = &sh.b[16 * si + l16][32 * n + 8 * g4];
+                    const uint16_t *pc = &sh.c[16 * ti + l16][32 * n + 8 * g4];
                     const bf16x8_t vb = cat8(*reinterpret_cast<const u32x2_t *>(pb), *reinterpret_cast<const u32x2_t *>(pb + 4));
                     const bf16x8_t vc = cat8(*reinterpret_cast<const u32x2_t *>(pc), *reinterpret_cast<const u32x2_t *>(pc + 4));
                     acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb, vc, acc, 0, 0, 0);
                 }
-                // lane holds t = ts + l16, s = ss + 4 (lane / 16) + r; the tokens
-                // after t are 0 here (ss < ts leaves none)
+                // the lane's t = 16 ti + l16, s = 16 si + 4 g4 + r
+                const int blk = (ti >> 1) == (si >> 1) ? ti >> 1 : 2;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[r] = ss == ts && 4 * (lane >> 4) + r > l16 ? 0.0f : acc[r];
-                *reinterpret_cast<f32x4_t *>(&sh.cb[q][ts + l16][ss + 4 * (lane >> 4)]) = acc;
+                for (int r = 0; r < 4; ++r) {
+                    const float v = si == ti && 4 * g4 + r > l16 ? 0.0f : acc[r];
+                    const uint32_t hi = pack_bf16x2(v, v);
+                    const uint32_t lo = pack_bf16x2(v - lo_f32(hi), 0.0f);
+                    const int e = 2 * (si & 1) + (g4 >> 1) + 4 * (r & 1);
+                    sh.cb[blk][0][r >> 1][g4 & 1][16 * (ti & 1) + l16][e] = static_cast<uint16_t>(hi);
+                    sh.cb[blk][1][r >> 1][g4 & 1][16 * (ti & 1) + l16][e] = static_cast<uint16_t>(lo);
+                }
             }
             lds_barrier();
         }
-#pragma unroll 1
-        for (int q = 0; q < TM / CH; ++q) {
-            const int r0 = CH * q;
-            if (tt + r0 >= tokens || !active)
-                break;
-            const float bits = read_lane(unit, r0);
-            const float total = bits * static_cast<float>(__builtin_amdgcn_readlane(g, r0 + CH - 1));
-            bf16x8_t xa[2];  // x_s, column l32, tokens in contraction order
+        u32x4_t rz[2][2];  // z of the lane's token of either block, asked for before the next tile
+        if (OUT && zp && active) {
+            const int ln = here(lane), l32 = ln & 31;
+            const uint32_t z_off = 2 * (l32 * static_cast<uint32_t>(p.zt) + 16 * (ln >> 5));
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                xa[j] = cat8(lds_tr(x_tr + 2 * kXPitch * (r0 + 2 * j)), lds_tr(x_tr + 2 * kXPitch * (r0 + 2 * j + 1)));
-
-            if constexpr (OUT) {
-                f32x16_t y;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) y[r] = 0.0f;
-                // S c_t
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint16_t *pc = &sh.c[r0 + l32][32 * nt + 16 * j + 4 * half];
-                        const bf16x8_t vc = cat8(*reinterpret_cast<const u32x2_t *>(pc), *reinterpret_cast<const u32x2_t *>(pc + 8));
-                        float v[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = s[nt][8 * j + e];
-                        bf16x8_t hi, lo;
-                        split8(v, &hi, &lo);
-                        y = mfma(hi, vc, y);
-                        y = mfma(lo, vc, y);
-                    }
-                const int gt = sh.g[wave][r0 + l32];
-                const float eg = exp2_f32(bits * static_cast<float>(gt));
-#pragma unroll
-                for (int r = 0; r < 16; ++r) y[r] *= eg;
-                // M[t, s], t = l32, s = 8 i + 4 half + e; c b^T is 0 for s > t,
-                // where the factor only has to stay finite
-                float m[4][4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int s0 = 8 * i + 4 * half;
-                    const f32x4_t cb = *reinterpret_cast<const f32x4_t *>(&sh.cb[q][l32][s0]);
-                    const i32x4_t gs = *reinterpret_cast<const i32x4_t *>(&sh.g[wave][r0 + s0]);
-                    const f32x4_t ds = *reinterpret_cast<const f32x4_t *>(&sh.d[wave][r0 + s0]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float span = fminf(bits * static_cast<float>(gt - gs[e]), 120.0f);
-                        m[i][e] = fmaf(cb[e] * ds[e], exp2_f32(span), diag[4 * i + e]);
-                    }
+            for (int q = 0; q < 2; ++q) {
+                if (tt + CH * q + l32 < tokens) {
+                    rz[q][0] = *reinterpret_cast<const u32x4_a2 *>(zp + z_off);
+                    rz[q][1] = *reinterpret_cast<const u32x4_a2 *>(zp + 16 + z_off);
                 }
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float v[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = m[e & 3][2 * j + (e >> 2)];
-                    bf16x8_t hi, lo;
-                    split8(v, &hi, &lo);
-                    y = mfma(xa[j], hi, y);
-                    y = mfma(xa[j], lo, y);
-                }
-                if (tt + r0 + l32 < tokens) {
-                    float f[16];
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) f[r] = y[r];
-                    if (zp) {
-                        float z[16];
-                        unpack8(*reinterpret_cast<const u32x4_a2 *>(zp), z);
-                        unpack8(*reinterpret_cast<const u32x4_a2 *>(zp + 8), z + 8);
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) f[r] *= silu_f32(z[r]);
-                    }
-                    *reinterpret_cast<u32x4_t *>(op) = pack8(f);
-                    *reinterpret_cast<u32x4_t *>(op + 8) = pack8(f + 8);
-                }
-                if (zp)
-                    zp += CH * p.zt;
-                op += CH * p.H * p.P;
+                zp += 2 * CH * p.zt;
             }
-
-            // S <- 2^total S + (w x) b^T
-            bf16x8_t whi[2], wlo[2];
-            {
+        }
+        if (kAhead && more)
+            fetch(tt + kStep);
+        if (active) {
+            // Where a SIMD's waves have got to: the one behind goes first, so
+            // that neither runs alone at the end.
+            __builtin_amdgcn_s_setprio(3);
+            const int ln = here(lane), l32 = ln & 31, half = ln >> 5, l16 = ln & 15, odd = (ln >> 4) & 1;
+            // of the transposing reads of b and x
+            const uint32_t b_tr = lds_addr(&sh.b[4 * half + 8 * (l16 >> 2)][16 * odd + 4 * (l16 & 3)]);
+            const int kappa = 4 * odd + (l16 & 3);
+            const uint32_t x_tr = lds_addr(&sh.x[4 * half + 8 * (l16 >> 2)][wave * 32 + 16 * (kappa & 1) + 4 * (kappa >> 1)]);
+            // x_s of a block, column l32, tokens in contraction order
+            const auto load_x = [&](int q, int j) {
+                const uint32_t a = x_tr + 2 * kXPitch * (CH * q + 2 * j);
+                return cat8(lds_tr(a), lds_tr(a + 2 * kXPitch));
+            };
+            // w_s x_s in parts
+            const auto weighted = [&](auto parts, int q, bf16x8_t(&wx)[2][3]) {
                 float w[4][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const f32x4_t v = *reinterpret_cast<const f32x4_t *>(&sh.w[wave][r0 + 8 * i + 4 * half]);
+                    const f32x4_t v = *reinterpret_cast<const f32x4_t *>(&sh.w[buf][hs][CH * q + 8 * i + 4 * half]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) w[i][e] = v[e];
                 }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     float v[8];
-                    unpack8(__builtin_bit_cast(u32x4_t, xa[j]), v);
+                    unpack8(__builtin_bit_cast(u32x4_t, load_x(q, j)), v);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[e] *= w[e & 3][2 * j + (e >> 2)];
-                    split8(v, &whi[j], &wlo[j]);
+                    split8<parts()>(v, wx[j]);
                 }
-            }
-            const float keep = exp2_f32(total);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[nt][r] *= keep;
+            };
+            // S += parts k0 .. k1 - 1 of sum_s w_s x_s b_s^T over block q
+            const auto update = [&](int q, auto k0, auto k1, int nt, const bf16x8_t(&wx)[2][3]) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const uint32_t a = b_tr + 2 * kPitch * (r0 + 2 * j) + 64 * nt;
+                    const uint32_t a = b_tr + 2 * kPitch * (CH * q + 2 * j) + 64 * nt;
                     const bf16x8_t vb = cat8(lds_tr(a), lds_tr(a + 2 * kPitch));
-                    s[nt] = mfma(vb, whi[j], s[nt]);
-                    s[nt] = mfma(vb, wlo[j], s[nt]);
+#pragma unroll
+                    for (int k = k0(); k < k1(); ++k) s[nt] = mfma(vb, wx[j][k], s[nt]);
+                }
+                if constexpr (!kAhead)
+                    fence();  // registers are short: no operand is read early
+            };
+            // The last part, where the block is near enough to need it.
+            const auto refine = [&](int q) {
+                bf16x8_t wx[2][3];
+                weighted(Int<3>(), q, wx);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) update(q, Int<2>(), Int<3>(), nt, wx);
+            };
+            if constexpr (!OUT) {
+#pragma unroll 1
+                for (int q = 1; q >= 0; --q) {
+                    const float rest = read_lane(sh.total[buf][hs][q], 0);  // from the block's end to the segment's
+                    if (rest < kNothing)
+                        break;
+                    bf16x8_t wx[2][3];
+                    weighted(Int<2>(), q, wx);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) update(q, Int<0>(), Int<2>(), nt, wx);
+                    if (rest > kFaint)
+                        refine(q);
+                }
+            } else {
+                const bool updates = more || final_at;
+                const float total0 = read_lane(sh.total[buf][hs][0], 0), total1 = read_lane(sh.total[buf][hs][1], 0);
+                const bool gentle = kAhead && total0 + total1 >= kSteep;  // never with 256 state columns
+                f32x16_t y[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) y[q][r] = 0.0f;
+                // y += S c_t of both blocks
+                const auto add_carried = [&]() {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if constexpr (!kAhead)
+                            fence();
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float v[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) v[e] = s[nt][8 * j + e];
+                            bf16x8_t parts[2];
+                            split8<2>(v, parts);
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                const uint16_t *pc = &sh.c[CH * q + l32][32 * nt + 16 * j + 4 * half];
+                                const bf16x8_t vc = cat8(*reinterpret_cast<const u32x2_t *>(pc), *reinterpret_cast<const u32x2_t *>(pc + 8));
+                                y[q] = mfma(parts[0], vc, y[q]);
+                                y[q] = mfma(parts[1], vc, y[q]);
+                            }
+                        }
+                    }
+                };
+                // y[q] += sum_s (c_t . b_s) w_s x_s over the tokens s that c b^T number blk has
+                const auto add_weighted = [&](int q, int blk, const bf16x8_t(&wx)[2][3]) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const bf16x8_t hi = *reinterpret_cast<const bf16x8_t *>(sh.cb[blk][0][j][half][l32]);
+                        const bf16x8_t lo = *reinterpret_cast<const bf16x8_t *>(sh.cb[blk][1][j][half][l32]);
+                        y[q] = mfma(wx[j][0], hi, y[q]);
+                        y[q] = mfma(wx[j][1], hi, y[q]);
+                        y[q] = mfma(wx[j][0], lo, y[q]);
+                    }
+                };
+                const auto decay_state = [&](float keep) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) s[nt][r] *= keep;
+                };
+                const auto log_to = [&](int q) {  // G of the lane's token of block q
+                    return read_lane(sh.unit[buf][hs][q], 0) * static_cast<float>(sh.g[buf][hs][CH * q + l32]);
+                };
+                // out of block q from f y[q]
+                const auto finish = [&](int q, float f) {
+                    if (tt + CH * q + l32 < tokens) {
+                        float o[16];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint16_t *px = &sh.x[CH * q + l32][wave * 32 + 16 * half + 8 * k];
+                            const u32x2_t x0 = *reinterpret_cast<const u32x2_t *>(px), x1 = *reinterpret_cast<const u32x2_t *>(px + 4);
+                            unpack8(u32x4_t{x0[0], x0[1], x1[0], x1[1]}, o + 8 * k);
+                        }
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) o[r] = fmaf(f, y[q][r], skip * o[r]);
+                        if (zp) {
+                            float z[16];
+                            unpack8(rz[q][0], z);
+                            unpack8(rz[q][1], z + 8);
+#pragma unroll
+                            for (int r = 0; r < 16; ++r) o[r] *= silu_f32(z[r]);
+                        }
+                        const uint32_t o_off = 2 * (l32 * static_cast<uint32_t>(width) + 16 * half);
+                        *reinterpret_cast<u32x4_t *>(op + o_off) = pack8(o);
+                        *reinterpret_cast<u32x4_t *>(op + 16 + o_off) = pack8(o + 8);
+                    }
+                    op += 2 * CH * width;
+                };
+                if (gentle) {
+                    decay_state(exp2_f32(total0 + total1));
+                    add_carried();
+                    __builtin_amdgcn_s_setprio(2);
+                    bf16x8_t wx[2][3];
+                    weighted(Int<2>(), 0, wx);
+                    add_weighted(0, 0, wx);
+                    add_weighted(1, 2, wx);
+                    if (updates) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) update(0, Int<0>(), Int<2>(), nt, wx);
+                    }
+                    finish(0, exp2_f32(log_to(0) - (total0 + total1)));
+                    __builtin_amdgcn_s_setprio(1);
+                    weighted(Int<3>(), 1, wx);
+                    add_weighted(1, 1, wx);
+                    if (updates) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) update(1, Int<0>(), Int<3>(), nt, wx);
+                        if (total1 > kFaint)
+                            refine(0);
+                    }
+                    finish(1, exp2_f32(log_to(1) - total1));
+                } else {
+                    add_carried();
+                    __builtin_amdgcn_s_setprio(2);
+                    const float keep0 = exp2_f32(total0);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) y[1][r] *= keep0;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float total = q ? total1 : total0, log_t = log_to(q);
+                        bf16x8_t wx[2][3];
+                        weighted(Int<2>(), q, wx);
+                        if (q == 0)
+                            add_weighted(1, 2, wx);
+                        if (updates) {
+                            decay_state(exp2_f32(total));
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) update(q, Int<0>(), Int<2>(), nt, wx);
+                            if (q == 1 || total1 > kFaint)
+                                refine(q);
+                        }
+                        // M[t, s] = (c_t . b_s) dt_s 2^(G_t - G_s) over the block's own tokens
+                        const float f = exp2_f32(log_t);
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) y[q][r] *= f;
+                        const float unit = read_lane(sh.unit[buf][hs][q], 0);
+                        const int gt = sh.g[buf][hs][CH * q + l32];
+#pragma unroll 1
+                        for (int j = 0; j < 2; ++j) {
+                            const u32x4_t hi = *reinterpret_cast<const u32x4_t *>(sh.cb[q][0][j][half][l32]);
+                            const u32x4_t lo = *reinterpret_cast<const u32x4_t *>(sh.cb[q][1][j][half][l32]);
+                            float m[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                // c b^T is 0 for s > t, where the factor only has to stay finite
+                                const int at = CH * q + 8 * (e & 3) + 4 * half + 2 * j + (e >> 2);
+                                const float span = fminf(unit * static_cast<float>(gt - sh.g[buf][hs][at]), 120.0f);
+                                const float cb = e & 1 ? hi_f32(hi[e / 2]) + hi_f32(lo[e / 2]) : lo_f32(hi[e / 2]) + lo_f32(lo[e / 2]);
+                                m[e] = cb * sh.d[buf][hs][at] * exp2_f32(span);
+                            }
+                            bf16x8_t parts[2];
+                            split8<2>(m, parts);
+                            const bf16x8_t xa = load_x(q, j);
+                            y[q] = mfma(xa, parts[0], y[q]);
+                            y[q] = mfma(xa, parts[1], y[q]);
+                        }
+                        finish(q, 1.0f);
+                    }
                 }
             }
-            log_sum += total;
+            __builtin_amdgcn_s_setprio(3);
         }
         lds_barrier();
+        if constexpr (!OUT) {
+            // nothing earlier reaches the segment's end: the weights are 0
+            bool nothing = true;
+            for (int k = 0; k < heads; ++k) nothing &= read_lane(sh.total[buf][k][0], 0) < kNothing;
+            if (nothing)
+                break;
+        }
     }
 
-    if (!active)
-        return;
     if constexpr (OUT) {
-        if (last && p.final_state)
-            store_state<N>(p.final_state, p.final_kind, state_at, s);
+        if (active && final_at) {
+            const int ln = here(lane);
+            const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(final_at) & 1);
+            store_state<N>(final_at - odd, odd ? kBf16 : kFp32, unit_column(ln & 31) * N + 4 * (ln >> 5), s);
+        }
     } else {
+        if (active) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<f32x4_t *>(slab + (4 * nt + i) * 256) =
-                    f32x4_t{s[nt][4 * i], s[nt][4 * i + 1], s[nt][4 * i + 2], s[nt][4 * i + 3]};
-        if (colblk == 0 && lane == 0)
-            p.logs[slot * p.H + h] = log_sum;
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<f32x4_t *>(slab + (4 * nt + i) * 256 + 4 * lane) =
+                        f32x4_t{s[nt][4 * i], s[nt][4 * i + 1], s[nt][4 * i + 2], s[nt][4 * i + 3]};
+        }
+        // several workgroups may hold columns of one head: they write the same value
+        if (keeps_dt && lane == 0)
+            p.logs[static_cast<int64_t>(slot) * p.H + dh] = after;
     }
 }
 
@@ -488,20 +756,20 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
 constexpr int kJoinThreads = 256;
 __global__ __launch_bounds__(kJoinThreads) void ssm_join_kernel(SsmParams p, int64_t quads)
 {
-    const int64_t per = (quads + kJoinThreads - 1) / kJoinThreads;
-    const int64_t chain = blockIdx.x / per;
-    const int64_t q = (blockIdx.x - chain * per) * kJoinThreads + threadIdx.x;  // quad within the head's slab
-    const int64_t n = chain / p.H, h = chain - n * p.H;
-    int64_t slot, len;
+    const uint32_t per = (static_cast<uint32_t>(quads) + kJoinThreads - 1) / kJoinThreads, chain = blockIdx.x / per;
+    const uint32_t q = (blockIdx.x - chain * per) * kJoinThreads + threadIdx.x;  // quad within the head's slab
+    const uint32_t heads = static_cast<uint32_t>(p.H), seg = static_cast<uint32_t>(p.seg);
+    const int64_t n = chain / heads, h = chain - static_cast<uint32_t>(n) * heads;
+    uint32_t len = static_cast<uint32_t>(p.seqs.T);
+    int64_t slot;
     if (p.seqs.cu) {
-        const int64_t a = clamp_offset(p.seqs, n), b = clamp_offset(p.seqs, n + 1);
-        slot = a / p.seg + n;
+        const uint32_t a = clamp_offset(p.seqs, n), b = clamp_offset(p.seqs, n + 1);
+        slot = a / seg + n;
         len = b > a ? b - a : 0;
-    } else {
-        slot = n * (p.seqs.T > 0 ? (p.seqs.T + p.seg - 1) / p.seg : 1);
-        len = p.seqs.T;
     }
-    const int64_t count = len > 0 ? (len + p.seg - 1) / p.seg : 1;
+    const uint32_t count = len > 0 ? (len + seg - 1) / seg : 1;
+    if (!p.seqs.cu)
+        slot = n * count;
     if (q >= quads)
         return;
     f32x4_t run = {0, 0, 0, 0};
@@ -520,12 +788,26 @@ __global__ __launch_bounds__(kJoinThreads) void ssm_join_kernel(SsmParams p, int
     const int64_t step = p.H * p.P * p.N;
     float *slab = p.slabs + (slot * p.H + h) * p.P * p.N + 4 * q;
     const float *logs = p.logs + slot * p.H + h;
-    for (int64_t k = 0; k + 1 < count; ++k) {
-        const f32x4_t own = *reinterpret_cast<const f32x4_t *>(slab + k * step);
-        const float keep = exp2_f32(logs[k * p.H]);
-        *reinterpret_cast<f32x4_t *>(slab + k * step) = run;
+    // eight segments' loads at once: a store of this loop could be what the
+    // next load reads, as far as the compiler knows
+    constexpr uint32_t kAhead = 8;
+    for (uint32_t k0 = 0; k0 + 1 < count; k0 += kAhead) {
+        f32x4_t own[kAhead];
+        float keep[kAhead];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) run[e] = fmaf(keep, run[e], own[e]);
+        for (uint32_t i = 0; i < kAhead; ++i)
+            if (k0 + i + 1 < count) {
+                own[i] = *reinterpret_cast<const f32x4_t *>(slab + (k0 + i) * step);
+                keep[i] = logs[(k0 + i) * p.H];
+            }
+#pragma unroll
+        for (uint32_t i = 0; i < kAhead; ++i)
+            if (k0 + i + 1 < count) {
+                *reinterpret_cast<f32x4_t *>(slab + (k0 + i) * step) = run;
+                const float f = exp2_f32(keep[i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) run[e] = fmaf(f, run[e], own[i][e]);
+            }
     }
     *reinterpret_cast<f32x4_t *>(slab + (count - 1) * step) = run;
 }

@@ -17,8 +17,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ float softplus_f32(float v) { return v > 20.0f ? v : log1pf(expf(v)); }
-
 template <int N, int ROWS>
 __global__ __launch_bounds__(kThreads) void ssm_recurrent_kernel(SsmParams p)
 {
@@ -70,7 +68,7 @@ __global__ __launch_bounds__(kThreads) void ssm_recurrent_kernel(SsmParams p)
     uint16_t *os = p.out + (row * p.seqs.T * p.H + h) * p.P + pb * ROWS + r0;
     for (int64_t t = begin; t < end; ++t) {
         const float raw = bf16_to_f32(p.dt[row * p.db + t * p.dtt + h]) + dt_bias;
-        const float dt = p.softplus ? softplus_f32(raw) : raw;
+        const float dt = softplus_f32(raw, dt_plain_above(p.softplus));
         const float keep = exp2_f32(rate * dt);
         float b[E4][4], c[E4][4];
 #pragma unroll
