@@ -46,10 +46,11 @@ def _device(x):
 
 
 def _dense(name, t, device, shape, *dtypes):
-    """A contiguous tensor of exactly `shape`, or None."""
+    """The pointer of a contiguous tensor of exactly `shape`, or None."""
     if t is None:
         return None
-    _tensor(name, t, device, *dtypes)
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.device != device:
+        _tensor(name, t, device, *dtypes)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if not t.is_contiguous():
@@ -77,6 +78,8 @@ def _row_stride(name, t):
     shape, strides = t.shape, t.stride()
     if shape[-1] != 1 and strides[-1] != 1:
         raise ValueError(f"{name}: the channels of a row must be adjacent, got strides {strides}")
+    if t.is_contiguous():
+        return shape[-1]
     found, step = None, None
     for size, stride in zip(reversed(shape[:-1]), reversed(strides[:-1])):
         if size == 1:
@@ -103,25 +106,22 @@ def _sequences(cu_seqlens, device, B, T, check):
     return cu_seqlens.data_ptr(), n, n
 
 
-def _state(name, t, device, shape):
-    if t is None:
-        return None, _lib.KDA_DTYPE_NONE
-    return _dense(name, t, device, shape, _BF16, torch.float32), _CODES[t.dtype]
-
-
-def _weight(name, t, device, shape):
+def _typed(name, t, device, shape):
+    """(pointer, dtype code) of a contiguous bf16 or fp32 tensor of exactly `shape`, or of None."""
     if t is None:
         return None, _lib.KDA_DTYPE_NONE
     return _dense(name, t, device, shape, _BF16, torch.float32), _CODES[t.dtype]
 
 
 def _call(entry, args, device):
-    """Enqueue on the current stream of `device`."""
-    if torch.cuda.current_device() == device.index:
-        status = entry(args, torch.cuda.current_stream(device).cuda_stream)
+    """Enqueue on the current stream of `device` (its handle straight from torch's C layer: the Stream object
+    that torch.cuda.current_stream builds costs as much as the launch)."""
+    index = device.index
+    if torch._C._cuda_getDevice() == index:
+        status = entry(args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            status = entry(args, torch.cuda.current_stream(device).cuda_stream)
+            status = entry(args, torch._C._cuda_getCurrentRawStream(index))
     if status != _lib.KDA_OK:
         raise (KdaError if status == _lib.KDA_ERR_LAUNCH else KdaArgumentError)(status)
 
@@ -159,13 +159,13 @@ def short_conv(x: torch.Tensor, weight: torch.Tensor, out: torch.Tensor,
     if weight.dim() != 2:
         raise ValueError(f"weight must be [D,W], got {list(weight.shape)}")
     W = weight.shape[1]
-    pw, wcode = _weight("weight", weight, device, (D, W))
+    pw, wcode = _typed("weight", weight, device, (D, W))
     pb = _dense("bias", bias, device, (D,), weight.dtype)
     if activation not in (None, "silu"):
         raise ValueError(f"activation must be 'silu' or None, got {activation!r}")
     pc, num, N = _sequences(cu_seqlens, device, B, T, check_cu_seqlens)
-    pi, icode = _state("initial_state", initial_state, device, (N, W - 1, D))
-    pf, fcode = _state("final_state", final_state, device, (N, W - 1, D))
+    pi, icode = _typed("initial_state", initial_state, device, (N, W - 1, D))
+    pf, fcode = _typed("final_state", final_state, device, (N, W - 1, D))
     _call(_lib.load().kda_short_conv,
           _lib.ConvArgs(px, sb, st, pw, pb, po, pi, pf, pc, num, B, T, D, W, wcode, icode, fcode,
                         _ACTIVATIONS[activation], l2norm or 0, l2norm_eps, 0), device)
@@ -211,8 +211,8 @@ def ssm_fwd(x: torch.Tensor, dt: torch.Tensor, b: torch.Tensor, c: torch.Tensor,
     pD = _dense("D", D, device, (H,), torch.float32)
     pt = _dense("dt_bias", dt_bias, device, (H,), torch.float32)
     pu, num, seqs = _sequences(cu_seqlens, device, B, T, check_cu_seqlens)
-    pi, icode = _state("initial_state", initial_state, device, (seqs, H, P, N))
-    pf, fcode = _state("final_state", final_state, device, (seqs, H, P, N))
+    pi, icode = _typed("initial_state", initial_state, device, (seqs, H, P, N))
+    pf, fcode = _typed("final_state", final_state, device, (seqs, H, P, N))
     if segment_tokens is not None and (not isinstance(segment_tokens, int) or isinstance(segment_tokens, bool)
                                        or segment_tokens < 1):
         raise ValueError(f"segment_tokens must be a positive int or None, got {segment_tokens!r}")
@@ -256,8 +256,9 @@ def gated_norm(x: torch.Tensor, gate: Optional[torch.Tensor], weight: torch.Tens
             raise ValueError(f"gate must be {list(shape)}, got {list(gate.shape)}")
         gs = _row_stride("gate", gate)
     po = _dense("out", out, device, shape, _BF16)
-    _tensor("weight", weight, device, _BF16, torch.float32)
-    pw, wcode = _weight("weight", weight, device, (D,))
+    if weight is None:
+        raise TypeError("weight must be a torch.Tensor")
+    pw, wcode = _typed("weight", weight, device, (D,))
     if activation not in ("sigmoid", "silu"):
         raise ValueError(f"activation must be 'sigmoid' or 'silu', got {activation!r}")
     if D == 0:
@@ -323,10 +324,10 @@ def residual_norm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: Opt
         raise ValueError("weight and out go together")
     if out is None and residual_out is None:
         raise ValueError("out or residual_out must be given")
-    pr, rcode = _weight("residual", residual, device, shape)
-    pq, qcode = _weight("residual_out", residual_out, device, shape)
-    pp, pcode = _weight("post_weight", post_weight, device, (D,))
-    pw, wcode = _weight("weight", weight, device, (D,))
+    pr, rcode = _typed("residual", residual, device, shape)
+    pq, qcode = _typed("residual_out", residual_out, device, shape)
+    pp, pcode = _typed("post_weight", post_weight, device, (D,))
+    pw, wcode = _typed("weight", weight, device, (D,))
     po = _dense("out", out, device, shape, _BF16)
     pg, gcode, period, gs = None, _lib.KDA_DTYPE_NONE, 0, 0
     if gate is not None:
