@@ -45,38 +45,73 @@ __device__ __forceinline__ u32x4_t pack8(const float f[8])
                    pack_bf16x2(f[6], f[7])};
 }
 
-// Eight bf16 at p, of which the first `count` exist (the others read as 0).
-__device__ __forceinline__ u32x4_t load8_raw(const uint16_t *p, int count)
+// The eight elements a lane takes of a row of `size`: from `at` on.  The last
+// lane of a row whose size is no multiple of eight steps back to the row's
+// last eight and does not own the first `skip` of them (eight, for a lane past
+// the row): loads are whole wherever the row holds eight elements, so no lane
+// waits for its own single ones, and only stores go one by one.  A row of
+// fewer than eight has one lane that owns `size` elements, loaded singly.
+struct Eight {
+    int64_t at;
+    int skip, count;  // elements skip .. count - 1 are the lane's
+};
+__device__ __forceinline__ Eight eight_of(int64_t at, int64_t size)
 {
-    if (count >= 8)
-        return *reinterpret_cast<const u32x4_a2 *>(p);
+    Eight v = {at, 0, 8};
+    if (size < 8) {
+        v.at = 0;
+        v.count = static_cast<int>(size);
+        v.skip = at == 0 ? 0 : v.count;
+    } else if (at + 8 > size) {
+        v.at = size - 8;
+        v.skip = at < size ? static_cast<int>(at + 8 - size) : 8;
+    }
+    return v;
+}
+__device__ __forceinline__ bool owns(const Eight &v, int e) { return e >= v.skip && e < v.count; }
+
+// Zero for what is not the lane's, whatever lies there.
+__device__ __forceinline__ void keep_own(const Eight &v, float f[8])
+{
+    if (v.skip == 0 && v.count == 8)
+        return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (!owns(v, i))
+            f[i] = 0.0f;
+}
+
+__device__ __forceinline__ u32x4_t load8_raw(const uint16_t *p, const Eight &v)
+{
+    if (v.count == 8)
+        return *reinterpret_cast<const u32x4_a2 *>(p + v.at);
     u32x4_t u = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 7; ++i)
-        if (i < count)
-            u[i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
+        if (i < v.count)
+            u[i / 2] |= static_cast<uint32_t>(p[v.at + i]) << (16 * (i & 1));
     return u;
 }
-__device__ __forceinline__ void store8_raw(uint16_t *p, u32x4_t u, int count)
+__device__ __forceinline__ void store8_raw(uint16_t *p, u32x4_t u, const Eight &v)
 {
-    if (count >= 8) {
-        *reinterpret_cast<u32x4_a2 *>(p) = u;
+    if (v.skip == 0 && v.count == 8) {
+        *reinterpret_cast<u32x4_a2 *>(p + v.at) = u;
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
-        if (i < count)
-            p[i] = static_cast<uint16_t>(u[i / 2] >> (16 * (i & 1)));
+    for (int i = 0; i < 8; ++i)
+        if (owns(v, i))
+            p[v.at + i] = static_cast<uint16_t>(u[i / 2] >> (16 * (i & 1)));
 }
-// Eight elements of kind KIND at element index `at`, as fp32.
-__device__ __forceinline__ void load8(const void *base, int kind, int64_t at, int count, float f[8])
+// The same of kind `kind`, as fp32; `base` at element `row`.
+__device__ __forceinline__ void load8(const void *base, int kind, int64_t row, const Eight &v, float f[8])
 {
     if (kind == kBf16) {
-        unpack8(load8_raw(static_cast<const uint16_t *>(base) + at, count), f);
+        unpack8(load8_raw(static_cast<const uint16_t *>(base) + row, v), f);
         return;
     }
-    const float *p = static_cast<const float *>(base) + at;
-    if (count >= 8) {
+    const float *p = static_cast<const float *>(base) + row + v.at;
+    if (v.count == 8) {
         const f32x4_t a = *reinterpret_cast<const f32x4_a4 *>(p), b = *reinterpret_cast<const f32x4_a4 *>(p + 4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -86,23 +121,23 @@ __device__ __forceinline__ void load8(const void *base, int kind, int64_t at, in
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = i < count ? p[i] : 0.0f;
+    for (int i = 0; i < 8; ++i) f[i] = i < v.count ? p[i] : 0.0f;
 }
-__device__ __forceinline__ void store8(void *base, int kind, int64_t at, int count, const float f[8])
+__device__ __forceinline__ void store8(void *base, int kind, int64_t row, const Eight &v, const float f[8])
 {
     if (kind == kBf16) {
-        store8_raw(static_cast<uint16_t *>(base) + at, pack8(f), count);
+        store8_raw(static_cast<uint16_t *>(base) + row, pack8(f), v);
         return;
     }
-    float *p = static_cast<float *>(base) + at;
-    if (count >= 8) {
+    float *p = static_cast<float *>(base) + row + v.at;
+    if (v.skip == 0 && v.count == 8) {
         *reinterpret_cast<f32x4_a4 *>(p) = f32x4_t{f[0], f[1], f[2], f[3]};
         *reinterpret_cast<f32x4_a4 *>(p + 4) = f32x4_t{f[4], f[5], f[6], f[7]};
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
-        if (i < count)
+    for (int i = 0; i < 8; ++i)
+        if (owns(v, i))
             p[i] = f[i];
 }
 
