@@ -243,6 +243,9 @@ extern "C" kda_status kda_ssm_fwd(const kda_ssm_args *args, void *stream)
         st = check_states(a.initial_state, a.initial_state_dtype, a.final_state, a.final_state_dtype);
     if (st != KDA_OK)
         return st;
+    SsmPlan plan;
+    if (!ssm_plan(a, p.seqs, &plan))
+        return KDA_ERR_SIZE;
     const int64_t tokens = a.B * a.T, inner = a.H * a.P, state = p.seqs.N * inner * a.N;
     int64_t nx, nd, nb, nc, nz;
     if (!extent(a.B, a.x_stride_b, a.T, a.x_stride_t, inner, 2, &nx) ||
@@ -250,6 +253,10 @@ extern "C" kda_status kda_ssm_fwd(const kda_ssm_args *args, void *stream)
         !extent(a.B, a.b_stride_b, a.T, a.b_stride_t, a.G * a.N, 2, &nb) ||
         !extent(a.B, a.c_stride_b, a.T, a.c_stride_t, a.G * a.N, 2, &nc) ||
         !extent(a.B, a.z_stride_b, a.T, a.z_stride_t, inner, 2, &nz))
+        return KDA_ERR_STRIDE;
+    if (!plan.recurrent && a.T > 1 &&
+        (a.x_stride_t > kda::layer::kSsmMaxStride || a.b_stride_t > kda::layer::kSsmMaxStride ||
+         a.c_stride_t > kda::layer::kSsmMaxStride || (a.z && a.z_stride_t > kda::layer::kSsmMaxZStride)))
         return KDA_ERR_STRIDE;
     if ((tokens > 0 && (!a.x || !a.dt || !a.b || !a.c || !a.out)) || !a.A_log)
         return KDA_ERR_NULL_POINTER;
@@ -266,9 +273,6 @@ extern "C" kda_status kda_ssm_fwd(const kda_ssm_args *args, void *stream)
         misaligned(a.out, 16) || misaligned(a.initial_state, 16) || misaligned(a.final_state, 16) ||
         misaligned(a.A_log, 4) || misaligned(a.D, 4) || misaligned(a.dt_bias, 4) || misaligned(a.cu_seqlens, 8))
         return KDA_ERR_ALIGNMENT;
-    SsmPlan plan;
-    if (!ssm_plan(a, p.seqs, &plan))
-        return KDA_ERR_SIZE;
     if (plan.bytes > 0) {
         if (!a.workspace || a.workspace_bytes < plan.bytes || misaligned(a.workspace, 16) ||
             any_overlap(span(a.workspace, plan.bytes), {sx, sd, sb, sc, sz, sA, sD, st_, su, so, si, sf}))

@@ -82,8 +82,9 @@ typedef enum kda_status {
                                   or norm size outside the supported ones */
     KDA_ERR_DTYPE = 14,        /* layer operators: a weight, gate or residual
                                   dtype that is neither bf16 nor fp32 */
-    KDA_ERR_STRIDE = 15        /* layer operators: a negative stride, or one
-                                  whose extent overflows int64 */
+    KDA_ERR_STRIDE = 15        /* layer operators: a negative stride, one
+                                  whose extent overflows int64, or a token
+                                  stride beyond kda_ssm_fwd's */
 } kda_status;
 
 /* Element type of initial_state / final_state (and of the layer operators'
@@ -381,7 +382,10 @@ kda_status kda_short_conv(const kda_conv_args *args, void *stream);
  *   y_t  = S c_t + D[h] x_t
  *   out_t = y_t silu(z_t)                (y_t without z)
  *
- *   x, z, out      bf16 [B,T,H,P]; z may be NULL.  out is contiguous.
+ *   x, z, out      bf16 [B,T,H,P]; z may be NULL.  out is contiguous.  For
+ *                  more than 8 tokens, or packed ones, the token strides of
+ *                  x, b and c are at most 2^27 elements and that of z 2^26
+ *                  (KDA_ERR_STRIDE otherwise).
  *   dt             bf16 [B,T,H].
  *   b, c           bf16 [B,T,G,N]; heads h with the same h / (H / G) share a
  *                  group's b and c (G divides H).

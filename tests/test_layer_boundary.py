@@ -292,3 +292,20 @@ def test_row_and_gate_strides():
     assert _tokens("x", wide[..., 8:24].unflatten(-1, (2, 8)), cpu, (2, 3, 2, 8))[1:] == (120, 40)
     with pytest.raises(ValueError, match="adjacent"):
         _tokens("x", t(2, 3, 8, 2).transpose(2, 3), cpu, (2, 3, 2, 8))
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(T=9, x_stride_t=(1 << 27) + 1), _lib.KDA_ERR_STRIDE),
+    (dict(T=9, b_stride_t=(1 << 27) + 1), _lib.KDA_ERR_STRIDE),
+    (dict(T=9, c_stride_t=(1 << 27) + 1), _lib.KDA_ERR_STRIDE),
+    (dict(T=9, z_stride_t=(1 << 26) + 1), _lib.KDA_ERR_STRIDE),
+    (dict(T=2, cu_seqlens=A[9], num_seqs=2, z_stride_t=(1 << 26) + 1), _lib.KDA_ERR_STRIDE),
+    # allowed ones get as far as the next check, here that of a pointer
+    (dict(T=9, x_stride_t=1 << 27, b_stride_t=1 << 27, c_stride_t=1 << 27, z_stride_t=1 << 26, A_log=None),
+     _lib.KDA_ERR_NULL_POINTER),
+    (dict(T=9, z=None, z_stride_t=1 << 30, A_log=None), _lib.KDA_ERR_NULL_POINTER),
+    (dict(T=8, x_stride_t=1 << 30, z_stride_t=1 << 30, A_log=None), _lib.KDA_ERR_NULL_POINTER),
+    (dict(T=1, cu_seqlens=A[9], num_seqs=2, x_stride_t=1 << 30, z_stride_t=1 << 30, A_log=None), _lib.KDA_ERR_NULL_POINTER),
+])
+def test_ssm_token_stride_limits(over, code):
+    assert call("kda_ssm_fwd", _lib.SsmArgs, SSM, over) == code

@@ -651,3 +651,26 @@ def test_offsets_beyond_32_bits():
     kda.gated_norm(a["x"][0].flatten(-2).contiguous(), None, wn, n)
     kda.gated_norm(x[0].flatten(-2), None, wn, nfar)
     assert torch.equal(n, nfar)
+
+
+def test_ssm_largest_token_strides():
+    """x, b, c and z at the largest token strides the chunked scan takes, with the widest rows of lanes (N = 32)."""
+    g = torch.Generator().manual_seed(15)
+    T, H, P, N, far = 70, 2, 32, 32, 1 << 26
+    a = {k: on_gpu(v) for k, v in ssm_inputs(g, 1, T, H, P, 1, N, 1).items()}
+    base = torch.zeros(2 * far * (T // 2) + 4096, dtype=BF16, device="cuda")  # 8.8 GiB
+
+    def place(v, at, stride, count):
+        w = v[0, 0].numel()
+        t = base.as_strided((1, count, w), (0, stride, 1), at)
+        t.copy_(v[:, :count].reshape(1, count, w))
+        return t.unflatten(-1, v.shape[2:])
+
+    rest = (a["A_log"], a["D"], a["dt_bias"])
+    for near, count, stride in (("z", T, far), ("xbc", T // 2, 2 * far)):
+        got = {k: place(a[k], 512 * i, stride, count) if k in near else a[k][:, :count] for i, k in enumerate("xbcz")}
+        out, far_out = (torch.empty(1, count, H, P, dtype=BF16, device="cuda") for _ in range(2))
+        dt = a["dt"][:, :count]
+        kda.ssm_fwd(a["x"][:, :count], dt, a["b"][:, :count], a["c"][:, :count], out, *rest, a["z"][:, :count])
+        kda.ssm_fwd(got["x"], dt, got["b"], got["c"], far_out, *rest, got["z"])
+        assert torch.equal(out, far_out)
