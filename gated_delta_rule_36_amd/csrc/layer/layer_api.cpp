@@ -84,7 +84,10 @@ kda_status check_states(const void *init, int32_t init_dtype, const void *fin, i
     return init && fin && init_dtype != fin_dtype ? KDA_ERR_STATE_DTYPE : KDA_OK;
 }
 
-kda_status launched(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_LAUNCH; }
+kda_status launched(hipError_t e)
+{
+    return e == hipSuccess ? KDA_OK : e == hipErrorInvalidConfiguration ? KDA_ERR_SIZE : KDA_ERR_LAUNCH;
+}
 
 }  // namespace
 

@@ -30,6 +30,11 @@ inline int64_t tile_slots(const Seqs &s, int64_t len)
     return s.N * (s.T > 0 ? (s.T + len - 1) / len : 1);
 }
 
+// Whether a grid of one dimension takes this many workgroups: a launch counts
+// its threads in 32 bits.  Launches that do not fit return
+// hipErrorInvalidConfiguration.
+inline bool grid_fits(int64_t blocks, int threads) { return blocks <= UINT32_MAX / threads; }
+
 struct ConvParams {
     const uint16_t *x;
     int64_t xb, xt;  // element strides of batch row and token

@@ -32,6 +32,11 @@ namespace {
 template <int TPR>
 constexpr int kThreads = TPR > 64 ? TPR : 256;
 
+// Workgroups come in lines of 2^kLineShift: the rows of a large batch are more
+// than one dimension of a grid takes (2^32 threads).
+constexpr int kLineShift = 20;
+__device__ __forceinline__ int64_t block_index() { return static_cast<int64_t>(blockIdx.y) << kLineShift | blockIdx.x; }
+
 // Sum over the TPR threads of a row.  `part` is LDS for TPR > 64; a second
 // sum in the same kernel takes another one, so one barrier serves each.
 template <int TPR>
@@ -62,7 +67,7 @@ __global__ __launch_bounds__(kThreads<TPR>) void gated_norm_kernel(GatedParams p
 {
     __shared__ float part[kThreads<TPR> / 64];
     const int r = threadIdx.x / TPR, l = threadIdx.x % TPR;
-    const int64_t g = static_cast<int64_t>(blockIdx.x) * (kThreads<TPR> / TPR) + r;
+    const int64_t g = block_index() * (kThreads<TPR> / TPR) + r;
     if (g >= groups)
         return;  // whole rows: TPR threads leave together
     const int64_t row = per_row == 1 ? g : g / per_row, c0 = (g - row * per_row) * p.group;
@@ -121,7 +126,7 @@ __global__ __launch_bounds__(kThreads<TPR>) void residual_norm_kernel(ResidParam
 {
     __shared__ float part[2][kThreads<TPR> / 64];
     const int sub = threadIdx.x / TPR, l = threadIdx.x % TPR;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads<TPR> / TPR) + sub;
+    const int64_t row = block_index() * (kThreads<TPR> / TPR) + sub;
     if (row >= p.rows)
         return;
     // with several vectors a thread, the row is longer than half of them
@@ -229,9 +234,14 @@ hipError_t by_size(int64_t size, F f)
 
 bool grid(int64_t rows, int tpr, dim3 *g)
 {
-    const int64_t per = tpr > 64 ? 1 : 256 / tpr, blocks = (rows + per - 1) / per;
-    *g = dim3(static_cast<uint32_t>(blocks));
-    return blocks <= INT32_MAX;
+    const int64_t per = tpr > 64 ? 1 : 256 / tpr, blocks = (rows + per - 1) / per, line = int64_t(1) << kLineShift;
+    if (blocks <= line) {
+        *g = dim3(static_cast<uint32_t>(blocks));
+        return true;
+    }
+    const int64_t lines = (blocks + line - 1) / line;
+    *g = dim3(static_cast<uint32_t>(line), static_cast<uint32_t>(lines));
+    return lines < 65536;
 }
 
 }  // namespace

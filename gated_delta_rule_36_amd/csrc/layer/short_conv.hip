@@ -149,7 +149,7 @@ hipError_t launch(const ConvParams &p, hipStream_t stream)
     const int64_t cblocks = (p.D + 511) / 512;
     const int64_t len = tile_slots(p.seqs, 32) * cblocks < kFew ? 8 : 16, tasks = tile_slots(p.seqs, len) * cblocks;
     const int64_t blocks = (tasks + kWaves - 1) / kWaves;
-    if (blocks > INT32_MAX / kWaves)
+    if (!grid_fits(blocks, 64 * kWaves))
         return hipErrorInvalidConfiguration;
     conv_kernel<W><<<dim3(static_cast<uint32_t>(blocks)), dim3(64 * kWaves), 0, stream>>>(
         p, static_cast<uint32_t>(tasks), static_cast<uint32_t>(cblocks), static_cast<uint32_t>(len));

@@ -66,7 +66,8 @@ constexpr float kSteep = -80.0f;                 // tiles that decay by more for
 // Log decays from a block to the tile's or segment's end.  Up to kFaint its
 // weighted x enters the state in two parts: their rounding, 2^-16 of the block's
 // own contribution, is below 2^-20 of what the newest tokens bring.  Below
-// kNothing the weights are 0 in fp32 whatever finite x and b they meet.
+// kNothing nothing earlier is left in fp32: what is finite there is 0 times
+// 2^-300, also where negative steps (without softplus) let it grow before.
 constexpr float kFaint = -4.0f, kNothing = -300.0f;
 template <int V>
 struct Int {
@@ -818,7 +819,7 @@ hipError_t launch(const SsmParams &p, hipStream_t stream)
     const int units = static_cast<int>(p.H / p.G * (p.P / 32)), ublocks = (units + NW - 1) / NW;
     const int64_t blocks = tile_slots(p.seqs, p.seg) * p.G * ublocks;
     const int64_t quads = p.P * N / 4, join = p.seqs.N * p.H * ((quads + kJoinThreads - 1) / kJoinThreads);
-    if (blocks > INT32_MAX || join > INT32_MAX)
+    if (!grid_fits(blocks, kThreads) || (p.slabs && !grid_fits(join, kJoinThreads)))
         return hipErrorInvalidConfiguration;
     const dim3 grid(static_cast<uint32_t>(blocks));
     if (p.slabs) {

@@ -120,7 +120,7 @@ template <int N>
 hipError_t launch(const SsmParams &p, hipStream_t stream)
 {
     const int64_t rows = p.P % 64 == 0 ? 64 : 32, blocks = p.seqs.N * p.H * (p.P / rows);
-    if (blocks > INT32_MAX)
+    if (!grid_fits(blocks, kThreads))
         return hipErrorInvalidConfiguration;
     const dim3 grid(static_cast<uint32_t>(blocks));
     if (rows == 64)

@@ -294,6 +294,27 @@ def test_row_and_gate_strides():
         _tokens("x", t(2, 3, 8, 2).transpose(2, 3), cpu, (2, 3, 2, 8))
 
 
+WIDE = [(i + 1) << 44 for i in range(14)]  # addresses with room for any size; nothing is launched with them
+
+
+@pytest.mark.parametrize("entry,struct,base,over", [
+    ("kda_short_conv", _lib.ConvArgs, "CONV", dict(cu_seqlens=WIDE[9], num_seqs=(1 << 31) - 1, T=1, D=1024)),
+    ("kda_short_conv", _lib.ConvArgs, "CONV", dict(B=1 << 27, T=1)),
+    ("kda_ssm_fwd", _lib.SsmArgs, "SSM", dict(B=(1 << 24), T=1, H=1, P=32, N=32)),
+    ("kda_ssm_fwd", _lib.SsmArgs, "SSM", dict(B=1, T=1, cu_seqlens=WIDE[9], num_seqs=1 << 23)),
+    ("kda_ssm_fwd", _lib.SsmArgs, "SSM", dict(B=1, T=2 << 20, cu_seqlens=WIDE[9], num_seqs=1 << 22, seg_tokens=32,
+                                              H=16, workspace=WIDE[13], workspace_bytes=1 << 50)),
+    ("kda_gated_norm", _lib.GatedNormArgs, "GATED", dict(rows=1 << 42, D=1, group=1)),
+    ("kda_residual_norm", _lib.ResidualNormArgs, "RESID", dict(rows=1 << 42, D=1, residual=None, residual_out=None)),
+])
+def test_grids_beyond_the_launch_limit_are_refused(entry, struct, base, over):
+    fields = dict(globals()[base])
+    for i, k in enumerate(k for k, v in fields.items() if v in A):
+        fields[k] = WIDE[i]
+    fields.update({k: 0 for k in fields if "_stride" in k})
+    assert call(entry, struct, fields, over) == _lib.KDA_ERR_SIZE
+
+
 @pytest.mark.parametrize("over,code", [
     (dict(T=9, x_stride_t=(1 << 27) + 1), _lib.KDA_ERR_STRIDE),
     (dict(T=9, b_stride_t=(1 << 27) + 1), _lib.KDA_ERR_STRIDE),

@@ -674,3 +674,165 @@ def test_ssm_largest_token_strides():
         kda.ssm_fwd(a["x"][:, :count], dt, a["b"][:, :count], a["c"][:, :count], out, *rest, a["z"][:, :count])
         kda.ssm_fwd(got["x"], dt, got["b"], got["c"], far_out, *rest, got["z"])
         assert torch.equal(out, far_out)
+
+
+# ---------------------------------------------------------------------------
+# calls at the edges of what is allowed
+# ---------------------------------------------------------------------------
+def scan(a, out, fin, **kw):
+    kda.ssm_fwd(a["x"], a["dt"], a["b"], a["c"], out, a["A_log"], a["D"], a["dt_bias"], a["z"],
+                initial_state=a["initial"], final_state=fin, **kw)
+
+
+def scan_against_formula(a, cu, softplus, **kw):
+    """A chunked scan of CPU inputs `a` against the formula, with the tolerances of ssm_case."""
+    B, T, H, P = a["x"].shape
+    want, final, scale, fscale = ref.ssm(a["x"], a["dt"], a["b"], a["c"], a["A_log"], a["D"], a["dt_bias"], a["z"],
+                                         a["initial"], cu, softplus)
+    d = {k: on_gpu(v) for k, v in a.items()}
+    out, fin = torch.empty(B, T, H, P, dtype=BF16, device="cuda"), torch.empty_like(d["initial"])
+    cug = None if cu is None else torch.tensor(cu, dtype=torch.int64, device="cuda")
+    scan(d, out, fin, cu_seqlens=cug, dt_softplus=softplus, **kw)
+    check("final_state", fin, final, 2.0 ** -15 * fscale)
+    check("out", out, want, 2.0 ** -14 * scale)
+
+
+@pytest.mark.parametrize("segment_tokens", [None, 64, 352])
+@pytest.mark.parametrize("cu", [None, [0, 40, 400, 400, 640]])
+def test_ssm_decays_that_end_a_segment_early(segment_tokens, cu):
+    """Eight heads of one workgroup, from a step that keeps all to one that forgets at once: tiles on both sides of
+    every choice by decay, and segments whose first tiles leave nothing."""
+    g = torch.Generator().manual_seed(21)
+    T, H = 640, 8
+    a = ssm_inputs(g, 1, T, H, 32, 1, 64, 1 if cu is None else len(cu) - 1)
+    per_token = torch.tensor([2.0 ** -14, 0.11, 0.14, 1.2, 1.3, 4.0, 10.0, 100.0])  # halvings, about
+    a["A_log"] = torch.log(per_token * 0.6931)
+    a["dt"] = (1 + 0.1 * torch.randn(1, T, H, generator=g)).abs().to(BF16)
+    a["dt_bias"] = None
+    scan_against_formula(a, cu, False, segment_tokens=segment_tokens)
+    a["A_log"] = torch.full((H,), 2.0)  # all of them forget: workgroups stop early
+    scan_against_formula(a, cu, True, segment_tokens=segment_tokens)
+
+
+def test_ssm_negative_steps_grow_the_state():
+    g = torch.Generator().manual_seed(22)
+    for T, segment_tokens in ((6, None), (200, None), (200, 96)):
+        a = ssm_inputs(g, 2, T, 4, 64, 1, 128, 2)
+        a["dt"] = (torch.randn(2, T, 4, generator=g) * 0.3).to(BF16)
+        a["dt_bias"], a["A_log"] = None, torch.tensor([-2.0, -1.0, 0.0, 0.5])
+        scan_against_formula(a, None, False, segment_tokens=segment_tokens)
+
+
+@pytest.mark.parametrize("P,H,G", [(96, 5, 1), (160, 4, 2), (32, 9, 1), (256, 2, 2)])
+def test_ssm_heads_across_workgroups_in_segments(P, H, G):
+    ssm_case(1, 260, H, P, G, 32, seed=P, segment_tokens=96, cu=[0, 100, 100, 259], in_place=True)
+    ssm_case(2, 200, H, P, G, 128, seed=P + 1, segment_tokens=64)
+
+
+def test_broadcast_inputs():
+    """Inputs expanded over the batch or the tokens (strides of 0) equal their copies."""
+    g = torch.Generator().manual_seed(23)
+    B, T, H, P, N = 2, 70, 3, 64, 64
+    a = {k: on_gpu(v) for k, v in ssm_inputs(g, B, T, H, P, 1, N, B).items()}
+    a["b"], a["c"] = a["b"][:, :1].expand(B, T, 1, N), a["c"][:1].expand(B, T, 1, N)
+    a["x"], a["z"] = a["x"][:, :1].expand(B, T, H, P), a["z"][:1, :1].expand(B, T, H, P)
+    whole = {k: v if v is None else v.clone(memory_format=torch.contiguous_format) for k, v in a.items()}
+    for n in (T, 5):
+        outs = []
+        for v in (a, whole):
+            v = {k: t if t is None or k in ("A_log", "D", "dt_bias", "initial") else t[:, :n] for k, t in v.items()}
+            out, fin = torch.empty(B, n, H, P, dtype=BF16, device="cuda"), torch.empty_like(a["initial"])
+            scan(v, out, fin)
+            outs.append((out, fin))
+        assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    row, w4 = normal(g, 1, 1, 192).cuda(), normal(g, 192, 4).cuda()
+    wide, copy = row.expand(B, T, 192), row.expand(B, T, 192).contiguous()
+    for f in (lambda x, o: kda.short_conv(x, w4, o), lambda x, o: kda.gated_norm(x, x, w4[:, 0].contiguous(), o),
+              lambda x, o: kda.residual_norm(x, None, w4[:, 1].contiguous(), o)):
+        one, two = torch.empty_like(copy), torch.empty_like(copy)
+        f(wide, one)
+        f(copy, two)
+        assert torch.equal(one, two)
+
+
+@pytest.mark.parametrize("cu", [[0, 50, 20, 130], [0, -7, 60, 130], [3, 200, 1 << 40, 130], [130, 90, 40, 0],
+                                [-(1 << 62), 1 << 62, -5, 1 << 33]])
+def test_offsets_out_of_order_write_nothing_else(cu):
+    """cu_seqlens that the caller did not check: the results mean nothing, but no other memory is written."""
+    g = torch.Generator().manual_seed(24)
+    T, H, P, N, n, edge = 130, 2, 64, 64, len(cu) - 1, 1 << 16
+    cug = torch.tensor(cu, dtype=torch.int64, device="cuda")
+    a = {k: on_gpu(v) for k, v in ssm_inputs(g, 1, T, H, P, 1, N, n).items()}
+
+    def guarded(*shape, dtype=BF16):
+        whole = torch.full((2 * edge + torch.Size(shape).numel(),), 7.0, dtype=dtype, device="cuda")
+        return whole, whole[edge:-edge].view(shape)
+
+    made = []
+    for segment_tokens in (None, 32):
+        (ow, out), (fw, fin) = guarded(1, T, H, P), guarded(n, H, P, N, dtype=F32)
+        scan(a, out, fin, cu_seqlens=cug, check_cu_seqlens=False, segment_tokens=segment_tokens)
+        made += [ow, fw]
+    x, w, st = normal(g, 1, T, 13).cuda(), normal(g, 13, 8).cuda(), normal(g, n, 7, 13).cuda()
+    (ow, out), (fw, fin) = guarded(1, T, 13), guarded(n, 7, 13)
+    kda.short_conv(x, w, out, initial_state=st, final_state=fin, cu_seqlens=cug, check_cu_seqlens=False)
+    for whole in made + [ow, fw]:
+        assert bool((whole[:edge] == 7.0).all()) and bool((whole[-edge:] == 7.0).all())
+
+
+@pytest.mark.parametrize("D", [3, 13, 515, 1027])
+def test_conv_in_place_states_of_odd_widths(D):
+    conv_case(1, 60, D, 8, seed=D, cu=[0, 1, 1, 4, 30, 60], in_place=True, state=F32)
+    conv_case(3, 1, D, 4, seed=D + 1, in_place=True, odd_rows=True)
+
+
+def test_norms_of_more_rows_than_one_grid_dimension():
+    """2^29 rows of one channel: as in slices."""
+    rows, piece = (1 << 29) + 5, 1 << 24
+    x = torch.empty(rows, 1, dtype=BF16, device="cuda")
+    for at in range(0, rows, piece):
+        x[at:at + piece].normal_()
+    w, out = torch.full((1,), 1.5, dtype=BF16, device="cuda"), torch.empty_like(x)
+    v = x[-piece:].double()
+    plain = v * (v * v + 1e-6).rsqrt() * 1.5
+    for f, want in ((lambda x, o: kda.gated_norm(x, x, w, o), plain * torch.sigmoid(v)),
+                    (lambda x, o: kda.residual_norm(x, None, w, o), plain)):
+        out.fill_(7.0)
+        f(x, out)
+        for at in (0, rows // 2, rows - piece):
+            part = torch.empty(piece, 1, dtype=BF16, device="cuda")
+            f(x[at:at + piece], part)
+            assert torch.equal(part, out[at:at + piece])
+        # fp32 arithmetic: below 2^-20 of values up to 1.5
+        assert bool(((out[-piece:].double() - want).abs() <= HALF[BF16] * want.abs() + 2.0 ** -19).all())
+
+
+def test_two_graphs_replayed_in_turn():
+    """Two captures of the same calls on inputs of their own, replayed in turn and at once on two streams."""
+    sets = []
+    for seed in (31, 32):
+        found = calls(torch.Generator().manual_seed(seed))
+        for call, _, _ in found.values():
+            call()
+        torch.cuda.synchronize()
+        want = {k: [t.clone() for t in outs] for k, (_, outs, _) in found.items()}
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for call, _, _ in found.values():
+                call()
+        sets.append((found, want, graph))
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(3):
+        for found, _, _ in sets:
+            for _, outs, _ in found.values():
+                for t in outs:
+                    t.fill_(7.0)
+        torch.cuda.synchronize()
+        for stream, (_, _, graph) in zip(streams, sets):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for found, want, _ in sets:
+            for name, (_, outs, _) in found.items():
+                for got, expected in zip(outs, want[name]):
+                    assert torch.equal(got, expected), name
