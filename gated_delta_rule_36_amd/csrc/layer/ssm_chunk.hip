@@ -62,7 +62,7 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 constexpr int CH = static_cast<int>(kSsmChunk);  // tokens a block
 constexpr int TM = 2 * CH;                       // tokens a tile
 constexpr int NW = static_cast<int>(kSsmWaves);  // waves, units a workgroup
-constexpr float kSteep = -80.0f;                 // tiles that decay by more form M
+constexpr float kSteep = -40.0f;                 // tiles that decay by more form M
 // Log decays from a block to the tile's or segment's end.  Up to kFaint its
 // weighted x enters the state in two parts: their rounding, 2^-16 of the block's
 // own contribution, is below 2^-20 of what the newest tokens bring.  Below

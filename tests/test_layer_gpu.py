@@ -705,7 +705,7 @@ def test_ssm_decays_that_end_a_segment_early(segment_tokens, cu):
     g = torch.Generator().manual_seed(21)
     T, H = 640, 8
     a = ssm_inputs(g, 1, T, H, 32, 1, 64, 1 if cu is None else len(cu) - 1)
-    per_token = torch.tensor([2.0 ** -14, 0.11, 0.14, 1.2, 1.3, 4.0, 10.0, 100.0])  # halvings, about
+    per_token = torch.tensor([2.0 ** -14, 0.11, 0.14, 0.6, 0.64, 1.3, 5.0, 100.0])  # halvings, about
     a["A_log"] = torch.log(per_token * 0.6931)
     a["dt"] = (1 + 0.1 * torch.randn(1, T, H, generator=g)).abs().to(BF16)
     a["dt_bias"] = None
