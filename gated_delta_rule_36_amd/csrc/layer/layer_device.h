@@ -195,13 +195,29 @@ __device__ __forceinline__ float softplus_f32(float v, float plain)
     return v > plain ? v : fmaxf(v, 0.0f) + s;
 }
 
+// The sum over the wave's lanes up to and with each lane.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_plus(uint32_t x)
+{
+    return x + static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), CTRL, ROWS, 0xf, true));
+}
+__device__ __forceinline__ uint32_t prefix64(uint32_t x)
+{
+    x = dpp_plus<0x118, 0xf>(dpp_plus<0x114, 0xf>(dpp_plus<0x112, 0xf>(dpp_plus<0x111, 0xf>(x))));
+    return dpp_plus<0x143, 0xc>(dpp_plus<0x142, 0xa>(x));  // lane 15 of rows 0, 2 to 1, 3; lane 31 to rows 2, 3
+}
+
 // Sequences are cut into tiles of `len` tokens that start at the sequence's
-// first token.  In a batch every sequence has ceil(T / len) tiles (one if
-// T = 0).  Packed sequence n owns the slots from cu[n] / len + n on: at least
-// one, and at least as many as it has tiles, since
-// ceil((b - a) / len) <= floor(b / len) - floor(a / len) + 1.  So the host
-// can size the grid (T / len + N slots) without reading cu_seqlens, and a
-// slot finds its sequence by search.
+// first token, at least one a sequence.  In a batch each has ceil(T / len).
+// Of packed ones T / len + N slots hold all tiles, since ceil((b - a) / len)
+// <= floor(b / len) - floor(a / len) + 1, so the host can size the grid
+// without reading cu_seqlens.  Up to 64 sequences, one a lane, take their
+// slots one after the other: the slots that no tile uses are the last ones,
+// and the tiles spread evenly over the chip (unused slots between them cost
+// the scan of 19595 tokens in 8 sequences up to 40 %: some compute units got
+// two of 32 segments).  Of more, sequence n owns the slots from cu[n] / len + n
+// on, and a slot finds its sequence by search.
+constexpr int64_t kLaneSequences = 64;
 struct Tile {
     int64_t n, row;       // sequence, its batch row
     uint32_t begin, end;  // its tokens
@@ -217,6 +233,26 @@ __device__ __forceinline__ uint32_t clamp_offset(const Seqs &s, int64_t n)
     return static_cast<uint32_t>(v < 0 ? 0 : (v > s.T ? s.T : v));
 }
 
+// Sequence `lane` of at most 64 packed ones: its tokens, its first slot and the
+// next one's (lanes past the last sequence: none, after all others).
+struct LaneSequence {
+    uint32_t begin, end, first, next;
+};
+__device__ __forceinline__ LaneSequence lane_sequence(const Seqs &s, uint32_t len, uint32_t lane)
+{
+    LaneSequence q = {0, 0, 0, 0};
+    uint32_t count = 0;
+    if (lane < s.N) {
+        q.begin = clamp_offset(s, lane);
+        const uint32_t end = clamp_offset(s, lane + 1);
+        q.end = end > q.begin ? end : q.begin;
+        count = q.end > q.begin ? (q.end - q.begin + len - 1) / len : 1;
+    }
+    q.next = prefix64(count);
+    q.first = q.next - count;
+    return q;
+}
+
 __device__ __forceinline__ Tile find_tile(const Seqs &s, uint32_t len, uint32_t slot)
 {
     Tile t;
@@ -230,9 +266,21 @@ __device__ __forceinline__ Tile find_tile(const Seqs &s, uint32_t len, uint32_t 
         t.valid = true;
         return t;
     }
+    const uint32_t lane = __lane_id();
+    t.row = 0;
+    if (s.N <= kLaneSequences) {
+        const LaneSequence q = lane_sequence(s, len, lane);
+        const uint64_t past = __ballot(q.next > slot);
+        const int n = past ? __builtin_ctzll(past) : 0;
+        t.n = n;
+        t.begin = __builtin_amdgcn_readlane(q.begin, n);
+        t.end = __builtin_amdgcn_readlane(q.end, n);
+        t.index = slot - __builtin_amdgcn_readlane(q.first, n);
+        t.valid = past != 0;
+        return t;
+    }
     // the last n with cu[n] / len + n <= slot; 64 probes a round.  Offsets
     // out of order still end at some n in [0, N).
-    const uint32_t lane = __lane_id();
     uint32_t lo = 0, hi = static_cast<uint32_t>(s.N);
     while (hi - lo > 1) {
         const uint32_t step = (hi - lo + 63) / 64, n = lo + lane * step;
@@ -244,7 +292,6 @@ __device__ __forceinline__ Tile find_tile(const Seqs &s, uint32_t len, uint32_t 
         hi = hi < lo + step ? hi : lo + step;
     }
     t.n = lo;
-    t.row = 0;
     t.begin = clamp_offset(s, lo);
     t.end = clamp_offset(s, lo + 1);
     if (t.end < t.begin)

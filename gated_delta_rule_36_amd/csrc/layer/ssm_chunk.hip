@@ -761,17 +761,21 @@ __global__ __launch_bounds__(kJoinThreads) void ssm_join_kernel(SsmParams p, int
     const uint32_t q = (blockIdx.x - chain * per) * kJoinThreads + threadIdx.x;  // quad within the head's slab
     const uint32_t heads = static_cast<uint32_t>(p.H), seg = static_cast<uint32_t>(p.seg);
     const int64_t n = chain / heads, h = chain - static_cast<uint32_t>(n) * heads;
-    uint32_t len = static_cast<uint32_t>(p.seqs.T);
-    int64_t slot;
-    if (p.seqs.cu) {
+    uint32_t len = static_cast<uint32_t>(p.seqs.T), first = 0;
+    if (p.seqs.cu && p.seqs.N <= kLaneSequences) {
+        const LaneSequence s = lane_sequence(p.seqs, seg, __lane_id());
+        const int at = __builtin_amdgcn_readfirstlane(static_cast<int>(n));
+        len = __builtin_amdgcn_readlane(s.end, at) - __builtin_amdgcn_readlane(s.begin, at);
+        first = __builtin_amdgcn_readlane(s.first, at);
+    } else if (p.seqs.cu) {
         const uint32_t a = clamp_offset(p.seqs, n), b = clamp_offset(p.seqs, n + 1);
-        slot = a / seg + n;
+        first = a / seg + static_cast<uint32_t>(n);
         len = b > a ? b - a : 0;
     }
     const uint32_t count = len > 0 ? (len + seg - 1) / seg : 1;
-    if (!p.seqs.cu)
-        slot = n * count;
-    if (q >= quads)
+    const int64_t slot = p.seqs.cu ? first : n * count;
+    // offsets out of order may count more slots than there are
+    if (q >= quads || (p.seqs.cu && slot + count > p.seqs.T / seg + p.seqs.N))
         return;
     f32x4_t run = {0, 0, 0, 0};
     if (p.init_kind != kNone) {

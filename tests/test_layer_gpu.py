@@ -836,3 +836,15 @@ def test_two_graphs_replayed_in_turn():
             for name, (_, outs, _) in found.items():
                 for got, expected in zip(outs, want[name]):
                     assert torch.equal(got, expected), name
+
+
+@pytest.mark.parametrize("n", [63, 64, 65, 130])
+@pytest.mark.parametrize("segment_tokens", [None, 32])
+def test_as_many_sequences_as_lanes_and_more(n, segment_tokens):
+    """Random lengths, some of 0, around the number at which tiles are found another way."""
+    g = torch.Generator().manual_seed(n)
+    lengths = torch.randint(0, 12, (n,), generator=g)
+    lengths[[0, 7, n // 2, n - 2]] = torch.tensor([0, 100, 70, 33])
+    cu = [0] + torch.cumsum(lengths, 0).tolist()
+    ssm_case(1, cu[-1] + 3, 2, 32, 1, 32, seed=n, cu=cu, segment_tokens=segment_tokens, in_place=True)
+    conv_case(1, cu[-1] + 3, 24, 4, seed=n, cu=cu, in_place=True)
