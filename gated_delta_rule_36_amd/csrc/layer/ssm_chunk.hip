@@ -10,11 +10,12 @@
 //   S <- 2^(T_1) (2^(T_0) S + sum_0 w_s x_s b_s^T) + sum_1 w_s x_s b_s^T
 // Since 2^(G_t - G_s) dt_s = 2^(G_t - T) w_s, the sum over a block's own tokens
 // takes the same weighted x as the state: 2^(G_t - T) sum (c_t . b_s) w_s x_s,
-// and c b^T, which the heads of a group share, is the other factor.  That
-// holds while 2^-T stays well inside fp32's range; a block that decays by more
-// than 2^-64 forms M[t,s] = (c_t . b_s) 2^(G_t - G_s) dt_s itself (a third more
-// vector work for that block).  No other exponent is positive, so nothing
-// overflows however strong the decay.
+// and c b^T, which the heads of a group share, is the other factor.  A gentle
+// tile, one that decays by less than 2^-40 in all, scales its first block's
+// weights and the state to the tile's end at once, so that 2^(G_t - T) stays
+// well inside fp32's range.  A steep one goes block by block and forms
+// M[t,s] = (c_t . b_s) 2^(G_t - G_s) dt_s itself; no other exponent is positive
+// there, so nothing overflows however strong the decay.
 //
 // A difference of G loses what a strong decay in the same block rounds away,
 // so G is held in fixed point: 32-bit integers in a unit of 2^-29 .. 2^-30 of
@@ -29,6 +30,21 @@
 // share b, c and c b^T (formed once a tile, 16 x 16 tiles spread over the
 // waves).  b, c and x go through registers into LDS, the next tile's loads in
 // flight while this one is computed.  x is read from memory once per pass.
+//
+// What bounds it is the issue of instructions.  A wave's tile (P = 64, N = 128)
+// takes some 95 matrix instructions of 32 cycles and more vector cycles than
+// that, most of them to round S, the weighted x and c b^T into their parts; two
+// waves a SIMD (the state takes 64 registers, a tile in flight 32) overlap them
+// only in part, and all eight wait together while a tile's loads are issued.
+// 8 x 16384 tokens of 32 heads, 3 GB to move: 820 to 900 us, of which the own
+// states take 180 and joining them 10; without loads and stores the output
+// pass would take 430.  19595 tokens in 8 sequences 184 us; one of 8192 tokens
+// with 16 heads of 128 x 64 58 us.  Asking for the next tile before c b^T is
+// formed gained 5 % over asking after it, the priorities below 4 %.  Measured
+// and not better: waves of 16 columns (16 of them), waves of 64, two workgroups
+// of four waves a compute unit, loads spread over the tile, z and out through
+// LDS or exchanged between lanes into whole 64-byte rows, the workgroups of a
+// segment on one L2, non-temporal z (10 % slower) and out (3 %).
 //
 // Operands.  v_mfma_f32_32x32x16_bf16 contracts 16 slots; lane (l32, half)
 // holds slots 8 half .. 8 half + 7 of row / column l32, and accumulator
@@ -62,10 +78,14 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 constexpr int CH = static_cast<int>(kSsmChunk);  // tokens a block
 constexpr int TM = 2 * CH;                       // tokens a tile
 constexpr int NW = static_cast<int>(kSsmWaves);  // waves, units a workgroup
-constexpr float kSteep = -40.0f;                 // tiles that decay by more form M
+// Log decay from which on a tile is steep.  The gentle way is 12 % faster on
+// 4 x 8192 tokens that hardly decay (268 against 300 us); from -80 on it is as fast,
+// with less room for small values of S.
+constexpr float kSteep = -40.0f;
 // Log decays from a block to the tile's or segment's end.  Up to kFaint its
 // weighted x enters the state in two parts: their rounding, 2^-16 of the block's
-// own contribution, is below 2^-20 of what the newest tokens bring.  Below
+// own contribution, is below 2^-20 of what the newest tokens bring (a third
+// part for every block costs 1 to 12 %).  Below
 // kNothing nothing earlier is left in fp32: what is finite there is 0 times
 // 2^-300, also where negative steps (without softplus) let it grow before.
 constexpr float kFaint = -4.0f, kNothing = -300.0f;
@@ -460,6 +480,9 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
                 step_dt(tt + kStep, sh.dt_plain);
             fetch_dt(tt + 2 * kStep);
         }
+        // the tile after it, in flight from here on
+        if (kAhead && more)
+            fetch(tt + kStep);
         if constexpr (OUT) {
             const int ln = here(lane), l16 = ln & 15, g4 = ln >> 4;
             for (int k = 0; k < 2; ++k) {
@@ -490,7 +513,7 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
             }
             lds_barrier();
         }
-        u32x4_t rz[2][2];  // z of the lane's token of either block, asked for before the next tile
+        u32x4_t rz[2][2];  // z of the lane's token of either block
         if (OUT && zp && active) {
             const int ln = here(lane), l32 = ln & 31;
             const uint32_t z_off = 2 * (l32 * static_cast<uint32_t>(p.zt) + 16 * (ln >> 5));
@@ -503,8 +526,6 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
                 zp += 2 * CH * p.zt;
             }
         }
-        if (kAhead && more)
-            fetch(tt + kStep);
         if (active) {
             // Where a SIMD's waves have got to: the one behind goes first, so
             // that neither runs alone at the end.
