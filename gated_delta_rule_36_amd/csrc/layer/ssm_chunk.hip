@@ -36,10 +36,10 @@
 // that, most of them to round S, the weighted x and c b^T into their parts; two
 // waves a SIMD (the state takes 64 registers, a tile in flight 32) overlap them
 // only in part, and all eight wait together while a tile's loads are issued.
-// 8 x 16384 tokens of 32 heads, 3 GB to move: 820 to 900 us, of which the own
-// states take 180 and joining them 10; without loads and stores the output
-// pass would take 430.  19595 tokens in 8 sequences 184 us; one of 8192 tokens
-// with 16 heads of 128 x 64 58 us.  Asking for the next tile before c b^T is
+// 8 x 16384 tokens of 32 heads, 3 GB to move: 820 to 850 us, of which the own
+// states take 180 and joining them 12; without loads and stores the output
+// pass would take 430.  19595 tokens in 8 sequences 171 us; one of 8192 tokens
+// with 16 heads of 128 x 64 55 us.  Asking for the next tile before c b^T is
 // formed gained 5 % over asking after it, the priorities below 4 %.  Measured
 // and not better: waves of 16 columns (16 of them), waves of 64, two workgroups
 // of four waves a compute unit, loads spread over the tile, z and out through
@@ -61,9 +61,9 @@
 // token's output.
 //
 // x, b and c are bf16 and enter as they are.  Of the fp32 factors, S, c b^T and
-// M enter as two bf16 parts (the value rounded, and the rest rounded: good to
-// 2^-16 of itself), which leaves out its one final rounding; the weighted x
-// enters the state as three (2^-24), so the state is as exact as fp32.
+// M enter as two bf16 parts (the value cut, and the rest rounded: good to 2^-17
+// of itself; out is rounded to 2^-9); the weighted x enters the state as three,
+// which hold it whole, so the state is as exact as fp32.
 #include "layer_device.h"
 
 namespace kda {
@@ -83,11 +83,11 @@ constexpr int NW = static_cast<int>(kSsmWaves);  // waves, units a workgroup
 // with less room for small values of S.
 constexpr float kSteep = -40.0f;
 // Log decays from a block to the tile's or segment's end.  Up to kFaint its
-// weighted x enters the state in two parts: their rounding, 2^-16 of the block's
-// own contribution, is below 2^-20 of what the newest tokens bring (a third
-// part for every block costs 1 to 12 %).  Below
-// kNothing nothing earlier is left in fp32: what is finite there is 0 times
-// 2^-300, also where negative steps (without softplus) let it grow before.
+// weighted x enters the state in two parts: their rounding, 2^-17 of the block's
+// own contribution, is below 2^-21 of what the newest tokens bring (a third
+// part for every block costs 1 to 12 %).  Below kNothing nothing earlier is left in
+// fp32: what is finite there is 0 times 2^-300, also where negative steps
+// (without softplus) let it grow before.
 constexpr float kFaint = -4.0f, kNothing = -300.0f;
 template <int V>
 struct Int {
@@ -131,23 +131,49 @@ __device__ __forceinline__ int here(int x)
     return x;
 }
 __device__ __forceinline__ const char *bytes(const uint16_t *p) { return reinterpret_cast<const char *>(p); }
-// v as the sum of parts[0..PARTS-1], each the rest rounded to bf16.
-template <int PARTS>
-__device__ __forceinline__ void split8(float v[8], bf16x8_t parts[PARTS])
+// v cut after its first 8 and 16 significant bits.
+__device__ __forceinline__ float cut8(float v) { return __uint_as_float(__float_as_uint(v) & 0xffff0000u); }
+__device__ __forceinline__ float cut16(float v) { return __uint_as_float(__float_as_uint(v) & 0xffffff00u); }
+// Two numbers of 8 significant bits as bf16.
+__device__ __forceinline__ uint32_t pack_exact(float a, float b)
 {
+    return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+// v as a sum of bf16 numbers: two, the value cut and the rest rounded (to 2^-17
+// of v); or three, the 24 bits of v in eights, which is exact.  Cutting takes
+// fewer and cheaper instructions than rounding and unpacking.
+template <int PARTS>
+__device__ __forceinline__ void split8(const float v[8], bf16x8_t parts[PARTS])
+{
+    static_assert(PARTS == 2 || PARTS == 3, "two parts or three");
+    u32x4_t h[3];
 #pragma unroll
-    for (int k = 0; k < PARTS; ++k) {
-        u32x4_t h;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            h[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-            if (k + 1 < PARTS) {
-                v[2 * i] -= lo_f32(h[i]);
-                v[2 * i + 1] -= hi_f32(h[i]);
-            }
+    for (int i = 0; i < 4; ++i) {
+        const float a = v[2 * i], b = v[2 * i + 1];
+        h[0][i] = pack_exact(a, b);
+        if constexpr (PARTS == 2) {
+            h[1][i] = pack_bf16x2(a - cut8(a), b - cut8(b));
+        } else {
+            // (the middle eight as a difference of the others: fewer registers at once)
+            const float ra = a - cut8(a), rb = b - cut8(b), la = a - cut16(a), lb = b - cut16(b);
+            h[1][i] = pack_exact(ra - la, rb - lb);
+            h[2][i] = pack_exact(la, lb);
         }
-        parts[k] = __builtin_bit_cast(bf16x8_t, h);
     }
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) parts[k] = __builtin_bit_cast(bf16x8_t, h[k]);
+}
+// What the two parts leave of v, rounded.
+__device__ __forceinline__ bf16x8_t rest8(const float v[8])
+{
+    u32x4_t h;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = v[2 * i] - cut8(v[2 * i]), b = v[2 * i + 1] - cut8(v[2 * i + 1]);
+        const uint32_t second = pack_bf16x2(a, b);
+        h[i] = pack_bf16x2(a - lo_f32(second), b - hi_f32(second));
+    }
+    return __builtin_bit_cast(bf16x8_t, h);
 }
 
 template <int CTRL, int ROWS>
@@ -504,10 +530,9 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float v = si == ti && 4 * g4 + r > l16 ? 0.0f : acc[r];
-                    const uint32_t hi = pack_bf16x2(v, v);
-                    const uint32_t lo = pack_bf16x2(v - lo_f32(hi), 0.0f);
+                    const uint32_t lo = pack_bf16x2(v - cut8(v), 0.0f);
                     const int e = 2 * (si & 1) + (g4 >> 1) + 4 * (r & 1);
-                    sh.cb[blk][0][r >> 1][g4 & 1][16 * (ti & 1) + l16][e] = static_cast<uint16_t>(hi);
+                    sh.cb[blk][0][r >> 1][g4 & 1][16 * (ti & 1) + l16][e] = static_cast<uint16_t>(__float_as_uint(v) >> 16);
                     sh.cb[blk][1][r >> 1][g4 & 1][16 * (ti & 1) + l16][e] = static_cast<uint16_t>(lo);
                 }
             }
@@ -540,7 +565,7 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
                 const uint32_t a = x_tr + 2 * kXPitch * (CH * q + 2 * j);
                 return cat8(lds_tr(a), lds_tr(a + 2 * kXPitch));
             };
-            // w_s x_s in parts
+            // w_s x_s in two or three parts, or (1) the third that two leave out
             const auto weighted = [&](auto parts, int q, bf16x8_t(&wx)[2][3]) {
                 float w[4][4];
 #pragma unroll
@@ -555,7 +580,10 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
                     unpack8(__builtin_bit_cast(u32x4_t, load_x(q, j)), v);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[e] *= w[e & 3][2 * j + (e >> 2)];
-                    split8<parts()>(v, wx[j]);
+                    if constexpr (parts() == 1)
+                        wx[j][2] = rest8(v);
+                    else
+                        split8<parts()>(v, wx[j]);
                 }
             };
             // S += parts k0 .. k1 - 1 of sum_s w_s x_s b_s^T over block q
@@ -570,10 +598,10 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
                 if constexpr (!kAhead)
                     fence();  // registers are short: no operand is read early
             };
-            // The last part, where the block is near enough to need it.
+            // The third part, where the block is near enough to need it.
             const auto refine = [&](int q) {
                 bf16x8_t wx[2][3];
-                weighted(Int<3>(), q, wx);
+                weighted(Int<1>(), q, wx);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) update(q, Int<2>(), Int<3>(), nt, wx);
             };
@@ -584,11 +612,15 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
                     if (rest < kNothing)
                         break;
                     bf16x8_t wx[2][3];
-                    weighted(Int<2>(), q, wx);
+                    if (rest > kFaint) {
+                        weighted(Int<3>(), q, wx);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) update(q, Int<0>(), Int<2>(), nt, wx);
-                    if (rest > kFaint)
-                        refine(q);
+                        for (int nt = 0; nt < NT; ++nt) update(q, Int<0>(), Int<3>(), nt, wx);
+                    } else {
+                        weighted(Int<2>(), q, wx);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) update(q, Int<0>(), Int<2>(), nt, wx);
+                    }
                 }
             } else {
                 const bool updates = more || final_at;
