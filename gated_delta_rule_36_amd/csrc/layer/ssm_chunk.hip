@@ -36,10 +36,10 @@
 // that, most of them to round S, the weighted x and c b^T into their parts; two
 // waves a SIMD (the state takes 64 registers, a tile in flight 32) overlap them
 // only in part, and all eight wait together while a tile's loads are issued.
-// 8 x 16384 tokens of 32 heads, 3 GB to move: 820 to 850 us, of which the own
+// 8 x 16384 tokens of 32 heads, 3 GB to move: 820 to 880 us, of which the own
 // states take 180 and joining them 12; without loads and stores the output
-// pass would take 430.  19595 tokens in 8 sequences 171 us; one of 8192 tokens
-// with 16 heads of 128 x 64 55 us.  Asking for the next tile before c b^T is
+// pass would take 430.  19595 tokens in 8 sequences 175 us; one of 8192 tokens
+// with 16 heads of 128 x 64 56 us.  Asking for the next tile before c b^T is
 // formed gained 5 % over asking after it, the priorities below 4 %.  Measured
 // and not better: waves of 16 columns (16 of them), waves of 64, two workgroups
 // of four waves a compute unit, loads spread over the tile, z and out through
@@ -612,7 +612,8 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
                     if (rest < kNothing)
                         break;
                     bf16x8_t wx[2][3];
-                    if (rest > kFaint) {
+                    const bool near = rest > kFaint;
+                    if (N <= 128 && near) {
                         weighted(Int<3>(), q, wx);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) update(q, Int<0>(), Int<3>(), nt, wx);
@@ -620,6 +621,8 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
                         weighted(Int<2>(), q, wx);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) update(q, Int<0>(), Int<2>(), nt, wx);
+                        if (near)  // with 256 state columns the registers hold no three parts
+                            refine(q);
                     }
                 }
             } else {
