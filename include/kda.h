@@ -316,7 +316,8 @@ const char *kda_fwd_kernel(int64_t T, int varlen, const kda_options *options);
  * may be slices of wider rows, given by element strides of the batch row and
  * of the token (>= 0) with the channels of a token adjacent.  Token tensors
  * need no alignment beyond their element's; out and the states 16 bytes.
- * Outputs must not overlap inputs, except where it is said.
+ * Outputs must not overlap inputs, except where it is said.  Sizes whose grid
+ * would pass 2^32 threads are KDA_ERR_SIZE (the norms take any number of rows).
  * ---------------------------------------------------------------------- */
 
 typedef enum kda_activation {
@@ -407,8 +408,10 @@ kda_status kda_short_conv(const kda_conv_args *args, void *stream);
  *                  kda_ssm_workspace_bytes(args) bytes (which may be 0), as
  *                  for kda_fwd_scan (KDA_ERR_WORKSPACE otherwise).
  *
- * A non-finite x, b or c reaches the outputs of its whole 32-token chunk and
- * of every later token of its sequence; it never reaches another sequence.
+ * A non-finite x, dt, b or c may reach every output of its head from the start
+ * of its tile of 64 tokens to the end of its sequence (of the group's heads, for
+ * b and c; x: of its 32 columns), or no later one where the state has decayed by
+ * more than 2^-300 in between.  It never reaches another sequence.
  */
 typedef struct kda_ssm_args {
     const void *x;
