@@ -36,16 +36,17 @@
 // that, most of them to round S, the weighted x and c b^T into their parts; two
 // waves a SIMD (the state takes 64 registers, a tile in flight 32) overlap them
 // only in part, and all eight wait together while a tile's loads are issued.
-// 8 x 16384 tokens of 32 heads, 1.7 GB to move: 820 to 880 us, of which the own
+// 8 x 16384 tokens of 32 heads, 1.7 GB to move: 790 to 880 us, of which the own
 // states take 180 and joining them 12; without loads and stores the output
-// pass would take 430.  19595 tokens in 8 sequences 175 us; one of 8192 tokens
+// pass would take 430.  19595 tokens in 8 sequences 155 to 175 us; one of 8192 tokens
 // with 16 heads of 128 x 64 56 us.  Asking for the next tile before c b^T is
 // formed gained 5 % over asking after it, the priorities below 4 %.  Measured
 // and not better: waves of 16 columns (16 of them), waves of 64, two workgroups
 // of four waves a compute unit, loads spread over the tile, z and out through
 // LDS or exchanged between lanes into whole 64-byte rows, more and shorter
 // segments for the own states (220 us in twice as many), the workgroups of a
-// segment on one L2, non-temporal z (10 % slower) and out (3 %).
+// segment on one L2, stores held back until the next tile has arrived (3 to 5 %
+// slower), non-temporal z (10 % slower) and out (3 %).
 //
 // Operands.  v_mfma_f32_32x32x16_bf16 contracts 16 slots; lane (l32, half)
 // holds slots 8 half .. 8 half + 7 of row / column l32, and accumulator

@@ -10,7 +10,7 @@ be adjacent, the tokens may lie anywhere.
 """
 from __future__ import annotations
 
-import ctypes
+import struct
 from typing import Optional
 
 import torch
@@ -46,9 +46,9 @@ def _device(x):
 
 
 def _dense(name, t, device, shape, *dtypes):
-    """The pointer of a contiguous tensor of exactly `shape`, or None."""
+    """The pointer of a contiguous tensor of exactly `shape`, or 0 for None."""
     if t is None:
-        return None
+        return 0
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.device != device:
         _tensor(name, t, device, *dtypes)
     if t.shape != shape:
@@ -61,7 +61,7 @@ def _dense(name, t, device, shape, *dtypes):
 def _tokens(name, t, device, shape):
     """(pointer, batch stride, token stride) of bf16 [B, T, ...] whose trailing dimensions are adjacent."""
     if t is None:
-        return None, 0, 0
+        return 0, 0, 0
     _tensor(name, t, device, _BF16)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
@@ -94,7 +94,7 @@ def _row_stride(name, t):
 def _sequences(cu_seqlens, device, B, T, check):
     """(pointer, number of sequences, states) of a call."""
     if cu_seqlens is None:
-        return None, 0, B
+        return 0, 0, B
     _tensor("cu_seqlens", cu_seqlens, device, torch.int64)
     if cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must be contiguous [N+1] with N+1 >= 1 entries")
@@ -109,13 +109,32 @@ def _sequences(cu_seqlens, device, B, T, check):
 def _typed(name, t, device, shape):
     """(pointer, dtype code) of a contiguous bf16 or fp32 tensor of exactly `shape`, or of None."""
     if t is None:
-        return None, _lib.KDA_DTYPE_NONE
+        return 0, _lib.KDA_DTYPE_NONE
     return _dense(name, t, device, shape, _BF16, torch.float32), _CODES[t.dtype]
 
 
-def _call(entry, args, device):
-    """Enqueue on the current stream of `device` (its handle straight from torch's C layer: the Stream object
-    that torch.cuda.current_stream builds costs as much as the launch)."""
+def _pack(pack, values):
+    """The bytes of an argument struct; a field of the wrong type is a TypeError."""
+    try:
+        return pack(*values)
+    except struct.error as e:
+        raise TypeError(f"an argument has the wrong type: {e}") from None
+
+
+def _entry(name):
+    found = _lib.LAYER.get(name)
+    if found is None:
+        _lib.load()
+        found = _lib.LAYER[name]
+    return found
+
+
+def _call(name, values, device, args=None):
+    """Enqueue `values` (or what they were packed to) on the current stream of `device` (its handle straight from
+    torch's C layer: the Stream object that torch.cuda.current_stream builds costs as much as the launch)."""
+    entry, pack = _entry(name)
+    if args is None:
+        args = _pack(pack, values)
     index = device.index
     if torch._C._cuda_getDevice() == index:
         status = entry(args, torch._C._cuda_getCurrentRawStream(index))
@@ -166,9 +185,8 @@ def short_conv(x: torch.Tensor, weight: torch.Tensor, out: torch.Tensor,
     pc, num, N = _sequences(cu_seqlens, device, B, T, check_cu_seqlens)
     pi, icode = _typed("initial_state", initial_state, device, (N, W - 1, D))
     pf, fcode = _typed("final_state", final_state, device, (N, W - 1, D))
-    _call(_lib.load().kda_short_conv,
-          _lib.ConvArgs(px, sb, st, pw, pb, po, pi, pf, pc, num, B, T, D, W, wcode, icode, fcode,
-                        _ACTIVATIONS[activation], l2norm or 0, l2norm_eps, 0), device)
+    _call("kda_short_conv", (px, sb, st, pw, pb, po, pi, pf, pc, num, B, T, D, W, wcode, icode, fcode,
+                             _ACTIVATIONS[activation], l2norm or 0, l2norm_eps, 0), device)
     return out
 
 
@@ -216,17 +234,17 @@ def ssm_fwd(x: torch.Tensor, dt: torch.Tensor, b: torch.Tensor, c: torch.Tensor,
     if segment_tokens is not None and (not isinstance(segment_tokens, int) or isinstance(segment_tokens, bool)
                                        or segment_tokens < 1):
         raise ValueError(f"segment_tokens must be a positive int or None, got {segment_tokens!r}")
-    args = _lib.SsmArgs(px, pd, pb, pc, pz, po, xb, xt, db, dtt, bb, bt, cb, ct, zb, zt, pA, pD, pt, pi, pf, pu,
-                        num, B, T, H, P, G, N, icode, fcode, 1 if dt_softplus else 0, 0, segment_tokens or 0,
-                        None, 0)
-    lib = _lib.load()
-    nbytes = lib.kda_ssm_workspace_bytes(args)
+    values = (px, pd, pb, pc, pz, po, xb, xt, db, dtt, bb, bt, cb, ct, zb, zt, pA, pD, pt, pi, pf, pu,
+              num, B, T, H, P, G, N, icode, fcode, 1 if dt_softplus else 0, 0, segment_tokens or 0)
+    workspace_bytes, pack = _entry("kda_ssm_workspace_bytes")
+    args = _pack(pack, values + (0, 0))
+    nbytes = workspace_bytes(args)
     if nbytes > 0:
         # freed right after the call: the caching allocator hands it out
         # again only to work ordered after this call on the same stream
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        args.workspace, args.workspace_bytes = workspace.data_ptr(), nbytes
-    _call(lib.kda_ssm_fwd, args, device)
+        args = _pack(pack, values + (workspace.data_ptr(), nbytes))
+    _call("kda_ssm_fwd", values, device, args)
     return out
 
 
@@ -263,8 +281,7 @@ def gated_norm(x: torch.Tensor, gate: Optional[torch.Tensor], weight: torch.Tens
         raise ValueError(f"activation must be 'sigmoid' or 'silu', got {activation!r}")
     if D == 0:
         return out
-    _call(_lib.load().kda_gated_norm,
-          _lib.GatedNormArgs(x.data_ptr(), None if gate is None else gate.data_ptr(), pw, po, xs, gs,
+    _call("kda_gated_norm", (x.data_ptr(), 0 if gate is None else gate.data_ptr(), pw, po, xs, gs,
                              x.numel() // D, D, D if group_size is None else group_size, wcode,
                              _ACTIVATIONS[activation], 1 if gate_first else 0, 0, eps), device)
     return out
@@ -329,7 +346,7 @@ def residual_norm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: Opt
     pp, pcode = _typed("post_weight", post_weight, device, (D,))
     pw, wcode = _typed("weight", weight, device, (D,))
     po = _dense("out", out, device, shape, _BF16)
-    pg, gcode, period, gs = None, _lib.KDA_DTYPE_NONE, 0, 0
+    pg, gcode, period, gs = 0, _lib.KDA_DTYPE_NONE, 0, 0
     if gate is not None:
         _tensor("gate", gate, device, _BF16, torch.float32)
         if gate.dim() < 1:
@@ -338,7 +355,6 @@ def residual_norm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: Opt
         pg, gcode = gate.data_ptr(), _CODES[gate.dtype]
     if D == 0:
         return out
-    _call(_lib.load().kda_residual_norm,
-          _lib.ResidualNormArgs(x.data_ptr(), pr, pq, pp, pg, pw, po, xs, gs, period, x.numel() // D, D,
+    _call("kda_residual_norm", (x.data_ptr(), pr, pq, pp, pg, pw, po, xs, gs, period, x.numel() // D, D,
                                 rcode, qcode, pcode, gcode, wcode, 0, residual_scale, block_scale, eps), device)
     return out

@@ -848,3 +848,36 @@ def test_as_many_sequences_as_lanes_and_more(n, segment_tokens):
     cu = [0] + torch.cumsum(lengths, 0).tolist()
     ssm_case(1, cu[-1] + 3, 2, 32, 1, 32, seed=n, cu=cu, segment_tokens=segment_tokens, in_place=True)
     conv_case(1, cu[-1] + 3, 24, 4, seed=n, cu=cu, in_place=True)
+
+
+@pytest.mark.parametrize("call", [
+    lambda x, w, o: kda.gated_norm(x, None, w, o, group_size=2.5),
+    lambda x, w, o: kda.gated_norm(x, None, w, o, eps="small"),
+    lambda x, w, o: kda.residual_norm(x, None, w, o, block_scale=None),
+    lambda x, w, o: kda.short_conv(x[None], w[:, None], o[None], l2norm="all"),
+])
+def test_arguments_of_the_wrong_type(call):
+    x, w, o = torch.zeros(2, 64, dtype=BF16, device="cuda"), torch.ones(64, dtype=BF16, device="cuda"), \
+        torch.full((2, 64), 7.0, dtype=BF16, device="cuda")
+    with pytest.raises(TypeError):
+        call(x, w, o)
+    assert bool((o == 7.0).all())
+
+
+def test_host_refusals_on_the_gpu():
+    """What the library refuses raises before anything is enqueued: the outputs stay as they were."""
+    x = torch.zeros(1, 9, 2, 32, dtype=BF16, device="cuda")
+    bc, dt, a = torch.zeros(1, 9, 1, 32, dtype=BF16, device="cuda"), torch.zeros(1, 9, 2, dtype=BF16, device="cuda"), torch.zeros(2, device="cuda")
+    out = torch.full_like(x, 7.0)
+    for segment_tokens in (16, 33):
+        with pytest.raises(kda.KdaArgumentError):
+            kda.ssm_fwd(x, dt, bc, bc, out, a, segment_tokens=segment_tokens)
+    with pytest.raises(kda.KdaArgumentError):
+        kda.ssm_fwd(x, dt, bc, bc, x, a)  # out is an input
+    with pytest.raises(kda.KdaArgumentError):
+        kda.short_conv(x.flatten(-2), torch.zeros(64, 9, dtype=BF16, device="cuda"), out.flatten(-2))  # nine taps
+    with pytest.raises(kda.KdaArgumentError):
+        kda.gated_norm(x, None, torch.ones(32, dtype=BF16, device="cuda"), out, group_size=5)
+    with pytest.raises(kda.KdaArgumentError):
+        kda.residual_norm(x, None, torch.ones(32, dtype=BF16, device="cuda"), out, eps=-1.0)
+    assert bool((out == 7.0).all())
