@@ -12,13 +12,15 @@
 // stays in the registers of the threads that share it (TPR threads, K vectors
 // of eight elements each), so every tensor is touched once.  Rows of up to
 // 512 elements are shared by 8 to 64 lanes of one wave, and their sums never
-// leave it; longer ones by a workgroup of 128 to 512 threads, one vector each
-// up to 4096 elements, whose waves meet in LDS.  Sums and the values between
+// leave it; longer ones by a workgroup of two to eight waves, one vector a
+// thread up to 4096 elements, which meet in LDS: as many waves as the row fills
+// (8192 rows of 5120: 62 us with five waves, 78 with eight; 4096 rows of 2560:
+// 15.6 with five, 18.2 with eight).  Sums and the values between
 // the two norms are fp32; the second norm takes the unrounded r.
 //
 // Measured: gated_norm over 4,194,304 rows of 128, 525 us, 6.1 TB/s;
 // residual_norm over 32768 rows of 4096 with an fp32 stream, post norm and
-// gate, 277 us, 5.8 TB/s (512 threads a row; 294 us with 256 of two vectors
+// gate, 278 us, 5.8 TB/s (512 threads a row; 294 us with 256 of two vectors
 // each), where a 1 GiB copy reaches 5.1 TB/s.  Asking for more waves a SIMD (8,
 // by a register limit) lost 2 to 3 %.
 #include "layer_device.h"
@@ -27,32 +29,49 @@ namespace kda {
 namespace layer {
 namespace {
 
-// Threads of a workgroup: one row where its threads are several waves, else
-// as many rows as four waves hold.
+// TPR of rows shared by a workgroup: 2 to 8 waves, as many as the row fills.
+constexpr int kWaves = 0, kMaxThreads = 512;
+// Threads of a workgroup: one row where its threads are several waves (at
+// most), else as many rows as four waves hold.
 template <int TPR>
-constexpr int kThreads = TPR > 64 ? TPR : 256;
+constexpr int kThreads = TPR == kWaves ? kMaxThreads : 256;
 
 // Workgroups come in lines of 2^kLineShift: the rows of a large batch are more
 // than one dimension of a grid takes (2^32 threads).
 constexpr int kLineShift = 20;
 __device__ __forceinline__ int64_t block_index() { return static_cast<int64_t>(blockIdx.y) << kLineShift | blockIdx.x; }
 
-// Sum over the TPR threads of a row.  `part` is LDS for TPR > 64; a second
+// The row of a thread, and its place among the row's threads.
+struct Place {
+    int64_t row;
+    int lane;
+};
+template <int TPR>
+__device__ __forceinline__ Place place()
+{
+    const int t = threadIdx.x;
+    if constexpr (TPR == kWaves)
+        return {block_index(), t};
+    else
+        return {block_index() * (256 / TPR) + t / TPR, t % TPR};
+}
+
+// Sum over the threads of a row.  `part` is LDS for a workgroup's row; a second
 // sum in the same kernel takes another one, so one barrier serves each.
 template <int TPR>
-__device__ __forceinline__ float row_sum(float x, float *part)
+__device__ __forceinline__ float row_sum(float x, float *part, int threads)
 {
-    if constexpr (TPR <= 64) {
+    if constexpr (TPR != kWaves) {
         return lane_sum<TPR>(x);
     } else {
         x = lane_sum<64>(x);
         if ((threadIdx.x & 63) == 0)
             part[threadIdx.x >> 6] = x;
         __syncthreads();
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < TPR / 64; ++i) s += part[i];
-        return s;
+        static_assert(kMaxThreads / 64 == 8, "a sum over groups of eight lanes");
+        const int wave = threadIdx.x & 7;
+        const float s = part[wave];
+        return lane_sum<8>(64 * wave < threads ? s : 0.0f);
     }
 }
 
@@ -63,13 +82,14 @@ __device__ __forceinline__ float inv_rms(float ss, float n, float eps)
 
 // FULL: the row fills its lanes' vectors.
 template <int TPR, int K, bool FULL>
-__global__ __launch_bounds__(kThreads<TPR>) void gated_norm_kernel(GatedParams p, int64_t groups, uint32_t per_row)
+__global__ __launch_bounds__(kThreads<TPR>) void gated_norm_kernel(GatedParams p, int64_t groups, uint32_t per_row, int threads)
 {
     __shared__ float part[kThreads<TPR> / 64];
-    const int r = threadIdx.x / TPR, l = threadIdx.x % TPR;
-    const int64_t g = block_index() * (kThreads<TPR> / TPR) + r;
+    const Place at_row = place<TPR>();
+    const int l = at_row.lane, tpr = TPR == kWaves ? threads : TPR;
+    const int64_t g = at_row.row;
     if (g >= groups)
-        return;  // whole rows: TPR threads leave together
+        return;  // whole rows: their threads leave together
     const int64_t row = per_row == 1 ? g : g / per_row, c0 = (g - row * per_row) * p.group;
     const uint16_t *x = p.x + row * p.xr + c0, *gate = p.gate ? p.gate + row * p.gr + c0 : nullptr;
 
@@ -78,7 +98,7 @@ __global__ __launch_bounds__(kThreads<TPR>) void gated_norm_kernel(GatedParams p
     // with several vectors a thread, the row is longer than half of them
     const auto whole = [](int k) { return FULL || 2 * k + 2 <= K; };
     const auto part_of = [&](int k) {
-        const int64_t at = (k * TPR + l) * 8;
+        const int64_t at = (k * tpr + l) * 8;
         return whole(k) ? Eight{at, 0, 8} : eight_of(at, p.group);
     };
 #pragma unroll
@@ -103,7 +123,7 @@ __global__ __launch_bounds__(kThreads<TPR>) void gated_norm_kernel(GatedParams p
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss = fmaf(v[k][e], v[k][e], ss);
     }
-    const float s = inv_rms(row_sum<TPR>(ss, part), static_cast<float>(p.group), p.eps);
+    const float s = inv_rms(row_sum<TPR>(ss, part, threads), static_cast<float>(p.group), p.eps);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const Eight ch = part_of(k);
@@ -122,17 +142,18 @@ __global__ __launch_bounds__(kThreads<TPR>) void gated_norm_kernel(GatedParams p
 }
 
 template <int TPR, int K, bool FULL>
-__global__ __launch_bounds__(kThreads<TPR>) void residual_norm_kernel(ResidParams p)
+__global__ __launch_bounds__(kThreads<TPR>) void residual_norm_kernel(ResidParams p, int threads)
 {
     __shared__ float part[2][kThreads<TPR> / 64];
-    const int sub = threadIdx.x / TPR, l = threadIdx.x % TPR;
-    const int64_t row = block_index() * (kThreads<TPR> / TPR) + sub;
+    const Place at_row = place<TPR>();
+    const int l = at_row.lane, tpr = TPR == kWaves ? threads : TPR;
+    const int64_t row = at_row.row;
     if (row >= p.rows)
         return;
     // with several vectors a thread, the row is longer than half of them
     const auto whole = [](int k) { return FULL || 2 * k + 2 <= K; };
     const auto part_of = [&](int k) {
-        const int64_t at = (k * TPR + l) * 8;
+        const int64_t at = (k * tpr + l) * 8;
         return whole(k) ? Eight{at, 0, 8} : eight_of(at, p.D);
     };
 
@@ -156,7 +177,7 @@ __global__ __launch_bounds__(kThreads<TPR>) void residual_norm_kernel(ResidParam
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int e = 0; e < 8; ++e) ss = fmaf(v[k][e], v[k][e], ss);
-        const float s = inv_rms(row_sum<TPR>(ss, part[0]), static_cast<float>(p.D), p.eps);
+        const float s = inv_rms(row_sum<TPR>(ss, part[0], threads), static_cast<float>(p.D), p.eps);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             float w[8];
@@ -189,7 +210,7 @@ __global__ __launch_bounds__(kThreads<TPR>) void residual_norm_kernel(ResidParam
     }
     if (!p.out)
         return;
-    const float s = inv_rms(row_sum<TPR>(ss, part[1]), static_cast<float>(p.D), p.eps);
+    const float s = inv_rms(row_sum<TPR>(ss, part[1], threads), static_cast<float>(p.D), p.eps);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const Eight ch = part_of(k);
@@ -204,18 +225,20 @@ __global__ __launch_bounds__(kThreads<TPR>) void residual_norm_kernel(ResidParam
 }
 
 // Calls f(threads per row, vectors per thread) for rows of `size` elements:
-// the fewest lanes that hold the row at eight elements each, then workgroups
-// (16384 elements at most).  With several vectors a thread the row is longer
-// than half of them hold.
+// the fewest lanes that hold the row at eight elements each, then workgroups of
+// as many waves as hold it (16384 elements at most).  With several vectors a
+// thread the row is longer than half of them hold.
 template <int A, int B, bool C>
 struct Shape {
     static constexpr int tpr = A, k = B;
     static constexpr bool full = C;
+    int threads;  // of a row
 };
 template <int A, int B, class F>
 hipError_t with_shape(int64_t size, F f)
 {
-    return size == A * B * 8 ? f(Shape<A, B, true>()) : f(Shape<A, B, false>());
+    const int threads = A != kWaves ? A : static_cast<int>((size + 512 * B - 1) / (512 * B) * 64);
+    return size == threads * B * 8 ? f(Shape<A, B, true>{threads}) : f(Shape<A, B, false>{threads});
 }
 template <class F>
 hipError_t by_size(int64_t size, F f)
@@ -224,11 +247,9 @@ hipError_t by_size(int64_t size, F f)
     if (size <= 128) return with_shape<16, 1>(size, f);
     if (size <= 256) return with_shape<32, 1>(size, f);
     if (size <= 512) return with_shape<64, 1>(size, f);
-    if (size <= 1024) return with_shape<128, 1>(size, f);
-    if (size <= 2048) return with_shape<256, 1>(size, f);
-    if (size <= 4096) return with_shape<512, 1>(size, f);
-    if (size <= 8192) return with_shape<512, 2>(size, f);
-    if (size <= kMaxNormSize) return with_shape<512, 4>(size, f);
+    if (size <= 4096) return with_shape<kWaves, 1>(size, f);
+    if (size <= 8192) return with_shape<kWaves, 2>(size, f);
+    if (size <= kMaxNormSize) return with_shape<kWaves, 4>(size, f);
     return hipErrorInvalidValue;
 }
 
@@ -251,9 +272,10 @@ hipError_t launch_gated_norm(const GatedParams &p, hipStream_t stream)
     const int64_t per_row = p.D / p.group, groups = p.rows * per_row;
     return by_size(p.group, [&](auto c) {
         dim3 g;
-        if (!grid(groups, c.tpr, &g))
+        if (!grid(groups, c.threads, &g))
             return hipErrorInvalidConfiguration;
-        gated_norm_kernel<c.tpr, c.k, c.full><<<g, dim3(kThreads<c.tpr>), 0, stream>>>(p, groups, static_cast<uint32_t>(per_row));
+        gated_norm_kernel<c.tpr, c.k, c.full><<<g, dim3(c.tpr == kWaves ? c.threads : 256), 0, stream>>>(
+            p, groups, static_cast<uint32_t>(per_row), c.threads);
         return hipGetLastError();
     });
 }
@@ -262,9 +284,9 @@ hipError_t launch_residual_norm(const ResidParams &p, hipStream_t stream)
 {
     return by_size(p.D, [&](auto c) {
         dim3 g;
-        if (!grid(p.rows, c.tpr, &g))
+        if (!grid(p.rows, c.threads, &g))
             return hipErrorInvalidConfiguration;
-        residual_norm_kernel<c.tpr, c.k, c.full><<<g, dim3(kThreads<c.tpr>), 0, stream>>>(p);
+        residual_norm_kernel<c.tpr, c.k, c.full><<<g, dim3(c.tpr == kWaves ? c.threads : 256), 0, stream>>>(p, c.threads);
         return hipGetLastError();
     });
 }

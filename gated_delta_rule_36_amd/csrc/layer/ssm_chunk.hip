@@ -75,7 +75,6 @@ namespace {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
-typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int CH = static_cast<int>(kSsmChunk);  // tokens a block
 constexpr int TM = 2 * CH;                       // tokens a tile

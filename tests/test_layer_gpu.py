@@ -881,3 +881,10 @@ def test_host_refusals_on_the_gpu():
     with pytest.raises(kda.KdaArgumentError):
         kda.residual_norm(x, None, torch.ones(32, dtype=BF16, device="cuda"), out, eps=-1.0)
     assert bool((out == 7.0).all())
+
+
+@pytest.mark.parametrize("D", [513, 640, 1025, 1536, 1999, 2560, 2561, 3590, 4095, 4097, 5120, 5121, 7168, 8191, 8193, 10240, 12289, 16383])
+def test_norms_of_rows_of_every_number_of_waves(D):
+    test_gated_norm_sizes(D, "silu", D % 2 == 0)
+    test_residual_norm_sizes(D, "channel", True, F32)
+    test_residual_norm_sizes(D, "none", False, BF16)
