@@ -888,3 +888,22 @@ def test_norms_of_rows_of_every_number_of_waves(D):
     test_gated_norm_sizes(D, "silu", D % 2 == 0)
     test_residual_norm_sizes(D, "channel", True, F32)
     test_residual_norm_sizes(D, "none", False, BF16)
+
+
+@pytest.mark.parametrize("P,N,G", [(64, 128, 1), (128, 64, 2), (64, 256, 1)])
+@pytest.mark.parametrize("segment_tokens", [None, 4096])
+def test_ssm_state_is_as_exact_as_fp32(P, N, G, segment_tokens):
+    """The fp32 state of a chunked scan from decays that forget in a token to ones that keep all.  Some thirty
+    roundings of 2^-24 reach an element (steps 4, weights 6, products 1, sums over 300 tokens in sixteens); they are
+    independent, so their sum is sqrt(30) 2^-24 or 2^-21.5 of it."""
+    g = torch.Generator().manual_seed(N)
+    for per_token in (0.003, 0.1, 2.0):
+        a = ssm_inputs(g, 1, 300, 8, P, G, N, 1, gate=False)
+        a["A_log"] = torch.log(torch.linspace(1, 16, 8) * per_token)
+        want, final, _, _ = ref.ssm(a["x"], a["dt"], a["b"], a["c"], a["A_log"], a["D"], a["dt_bias"], None, a["initial"])
+        d = {k: on_gpu(v) for k, v in a.items()}
+        out, fin = torch.empty(1, 300, 8, P, dtype=BF16, device="cuda"), torch.empty_like(d["initial"])
+        scan(d, out, fin, segment_tokens=segment_tokens)
+        for h in range(8):
+            error = (fin[:, h].double().cpu() - final[:, h]).norm() / final[:, h].norm()
+            assert float(error) <= 2.0 ** -20, (per_token, h, float(error))
