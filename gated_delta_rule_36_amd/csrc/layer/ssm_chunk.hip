@@ -63,9 +63,9 @@
 // token's output.
 //
 // x, b and c are bf16 and enter as they are.  Of the fp32 factors, S, c b^T and
-// M enter as two bf16 parts (the value cut, and the rest rounded: good to 2^-17
-// of itself; out is rounded to 2^-9); the weighted x enters the state as three,
-// which hold it whole, so the state is as exact as fp32.
+// M enter as two bf16 parts (the value rounded, and the rest rounded: good to
+// 2^-17 of itself; out is rounded to 2^-8); the weighted x enters the state as
+// three, which hold it whole.
 #include "layer_device.h"
 
 namespace kda {
@@ -132,45 +132,35 @@ __device__ __forceinline__ int here(int x)
     return x;
 }
 __device__ __forceinline__ const char *bytes(const uint16_t *p) { return reinterpret_cast<const char *>(p); }
-// v cut after its first 8 and 16 significant bits.
-__device__ __forceinline__ float cut8(float v) { return __uint_as_float(__float_as_uint(v) & 0xffff0000u); }
-__device__ __forceinline__ float cut16(float v) { return __uint_as_float(__float_as_uint(v) & 0xffffff00u); }
-// Two numbers of 8 significant bits as bf16.
-__device__ __forceinline__ uint32_t pack_exact(float a, float b)
-{
-    return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
-}
-// v as a sum of bf16 numbers: two, the value cut and the rest rounded (to 2^-17
-// of v); or three, the 24 bits of v in eights, which is exact.  Cutting takes
-// fewer and cheaper instructions than rounding and unpacking.
+// v as a sum of bf16 numbers, each what is left rounded to nearest: two leave
+// 2^-17 of v at most (half a step of 2^-8 v, which is half a step of v), three
+// hold its 24 bits.
 template <int PARTS>
 __device__ __forceinline__ void split8(const float v[8], bf16x8_t parts[PARTS])
 {
     static_assert(PARTS == 2 || PARTS == 3, "two parts or three");
-    u32x4_t h[3];
+    u32x4_t h[PARTS];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float a = v[2 * i], b = v[2 * i + 1];
-        h[0][i] = pack_exact(a, b);
-        if constexpr (PARTS == 2) {
-            h[1][i] = pack_bf16x2(a - cut8(a), b - cut8(b));
-        } else {
-            // (the middle eight as a difference of the others: fewer registers at once)
-            const float ra = a - cut8(a), rb = b - cut8(b), la = a - cut16(a), lb = b - cut16(b);
-            h[1][i] = pack_exact(ra - la, rb - lb);
-            h[2][i] = pack_exact(la, lb);
+        float a = v[2 * i], b = v[2 * i + 1];
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) {
+            h[k][i] = pack_bf16x2(a, b);
+            a -= lo_f32(h[k][i]);
+            b -= hi_f32(h[k][i]);
         }
     }
 #pragma unroll
     for (int k = 0; k < PARTS; ++k) parts[k] = __builtin_bit_cast(bf16x8_t, h[k]);
 }
-// What the two parts leave of v, rounded.
+// The third part of v, which two leave out.
 __device__ __forceinline__ bf16x8_t rest8(const float v[8])
 {
     u32x4_t h;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float a = v[2 * i] - cut8(v[2 * i]), b = v[2 * i + 1] - cut8(v[2 * i + 1]);
+        const uint32_t first = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+        const float a = v[2 * i] - lo_f32(first), b = v[2 * i + 1] - hi_f32(first);
         const uint32_t second = pack_bf16x2(a, b);
         h[i] = pack_bf16x2(a - lo_f32(second), b - hi_f32(second));
     }
@@ -531,9 +521,9 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float v = si == ti && 4 * g4 + r > l16 ? 0.0f : acc[r];
-                    const uint32_t lo = pack_bf16x2(v - cut8(v), 0.0f);
+                    const uint32_t hi = pack_bf16x2(v, 0.0f), lo = pack_bf16x2(v - lo_f32(hi), 0.0f);
                     const int e = 2 * (si & 1) + (g4 >> 1) + 4 * (r & 1);
-                    sh.cb[blk][0][r >> 1][g4 & 1][16 * (ti & 1) + l16][e] = static_cast<uint16_t>(__float_as_uint(v) >> 16);
+                    sh.cb[blk][0][r >> 1][g4 & 1][16 * (ti & 1) + l16][e] = static_cast<uint16_t>(hi);
                     sh.cb[blk][1][r >> 1][g4 & 1][16 * (ti & 1) + l16][e] = static_cast<uint16_t>(lo);
                 }
             }

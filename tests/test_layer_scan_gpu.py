@@ -1,0 +1,89 @@
+"""The chunked scan where its arithmetic and its masks can go wrong: operand
+splits under cancellation, quiet tails, non-finite inputs, workspaces."""
+import pytest
+import torch
+
+import gated_delta_rule_36_amd as kda
+import layer_ref as ref
+from test_layer_gpu import BF16, F32, check, normal, on_gpu, scan, ssm_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+def still(T, H, P, N):
+    """Inputs of a scan whose state never decays (exp(A_log) = 0) and whose x, dt, b and c are 0."""
+    z = lambda *s: torch.zeros(*s, dtype=BF16)  # noqa: E731
+    return dict(x=z(1, T, H, P), dt=z(1, T, H), b=z(1, T, 1, N), c=z(1, T, 1, N), A_log=torch.full((H,), -200.0), D=None,
+                dt_bias=None, z=None, initial=torch.zeros(1, H, P, N))
+
+
+def mantissas(n, g):
+    """n numbers in [1, 2) of 24 bits, and the nearest bf16 numbers."""
+    v = 1 + torch.randint(0, 1 << 23, (n,), generator=g).float() * 2.0 ** -23
+    return v, v.to(BF16).float()
+
+
+# A value v of 24 bits less its nearest bf16 number r, an operand that is exact: two parts of v, each rounded to
+# nearest, leave 2^-8 2^-9 v at most (|v - r| <= 2^-8 in [1, 2), half a step of which is 2^-17); the sums are exact up
+# to 2^-24 of |v|, a handful of times.
+def check_rest(name, got, v, r):
+    want = v.double() - r.double()
+    check(name, got, want, (2.0 ** -17 + 2.0 ** -20) * torch.ones_like(want))
+
+
+@pytest.mark.parametrize("N", [64, 128, 256])
+def test_scan_state_operand_is_good_to_two_rounded_parts(N):
+    T, H, P = 70, 2, 64
+    a, g = still(T, H, P, N), torch.Generator().manual_seed(N)
+    v, r = mantissas(H * P, g)
+    a["initial"][0, :, :, 3], a["initial"][0, :, :, 9] = v.view(H, P), r.view(H, P)
+    a["c"][..., 3], a["c"][..., 9] = 1.0, -1.0
+    d = {k: on_gpu(t) for k, t in a.items()}
+    out, fin = torch.empty(1, T, H, P, dtype=BF16, device="cuda"), torch.empty(1, H, P, N, device="cuda")
+    scan(d, out, fin, dt_softplus=False)
+    assert torch.equal(fin.cpu(), a["initial"])
+    for t in range(T):
+        check_rest(f"token {t}", out[0, t].flatten(), v, r)
+
+
+@pytest.mark.parametrize("N", [64, 128, 256])
+@pytest.mark.parametrize("s,t", [(0, 0), (3, 20), (3, 40), (35, 60), (35, 35), (5, 69)])
+def test_scan_weighted_operand_is_good_to_two_rounded_parts(N, s, t):
+    """Token s writes v = dt x, and token t reads it beside -r from the initial state."""
+    T, H, P = 70, 64, 32
+    a, g = still(T, H, P, N), torch.Generator().manual_seed(N + s)
+    v, r = mantissas(H, g)
+    a["dt_bias"] = v                   # dt = v at every token; x is 0 but at s
+    a["x"][0, s] = 1.0
+    a["b"][0, s, 0, 3] = 1.0
+    a["initial"][0, :, :, 9] = r[:, None]
+    a["c"][0, t, 0, 3], a["c"][0, t, 0, 9] = 1.0, -1.0
+    d = {k: on_gpu(u) for k, u in a.items()}
+    out, fin = torch.empty(1, T, H, P, dtype=BF16, device="cuda"), torch.empty(1, H, P, N, device="cuda")
+    scan(d, out, fin, dt_softplus=False)
+    check_rest(f"token {t}", out[0, t].flatten(), v[:, None].expand(H, P).flatten(), r[:, None].expand(H, P).flatten())
+    assert torch.equal(fin[0, :, :, 3].cpu(), v[:, None].expand(H, P))
+
+
+@pytest.mark.parametrize("N", [64, 128, 256])
+@pytest.mark.parametrize("s,t", [(2, 2), (3, 30), (3, 50), (40, 63)])
+def test_scan_product_operand_is_good_to_two_rounded_parts(N, s, t):
+    """c_t . b_s is a number of 24 bits; the token's x takes it as it is, beside the nearest bf16 number less."""
+    T, H, P = 70, 2, 32
+    g = torch.Generator().manual_seed(s + t)
+    for _ in range(24):
+        a = still(T, H, P, N)
+        v, r = mantissas(1, g)
+        a["dt_bias"] = torch.ones(H)
+        a["x"][0, s] = 1.0
+        rest = v.double()
+        for n in range(3):             # v in three bf16 numbers
+            a["b"][0, s, 0, n] = rest.to(BF16).item()
+            rest = rest - rest.to(BF16).double()
+            a["c"][0, t, 0, n] = 1.0
+        a["initial"][..., 9] = r.item()
+        a["c"][0, t, 0, 9] = -1.0
+        d = {k: on_gpu(u) for k, u in a.items()}
+        out, fin = torch.empty(1, T, H, P, dtype=BF16, device="cuda"), torch.empty(1, H, P, N, device="cuda")
+        scan(d, out, fin, dt_softplus=False)
+        check_rest(f"token {t}", out[0, t].flatten(), v.expand(H * P), r.expand(H * P))
