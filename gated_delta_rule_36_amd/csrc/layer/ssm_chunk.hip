@@ -65,7 +65,8 @@
 // x, b and c are bf16 and enter as they are.  Of the fp32 factors, S, c b^T and
 // M enter as two bf16 parts (the value rounded, and the rest rounded: good to
 // 2^-17 of itself; out is rounded to 2^-8); the weighted x enters the state as
-// three, which hold it whole.
+// three, which hold it whole, at any decay: what a decay leaves of a block is
+// all there is of the state where later tokens bring nothing.
 #include "layer_device.h"
 
 namespace kda {
@@ -83,13 +84,10 @@ constexpr int NW = static_cast<int>(kSsmWaves);  // waves, units a workgroup
 // 4 x 8192 tokens that hardly decay (268 against 300 us); from -80 on it is as fast,
 // with less room for small values of S.
 constexpr float kSteep = -40.0f;
-// Log decays from a block to the tile's or segment's end.  Up to kFaint its
-// weighted x enters the state in two parts: their rounding, 2^-17 of the block's
-// own contribution, is below 2^-21 of what the newest tokens bring (a third
-// part for every block costs 1 to 12 %).  Below kNothing nothing earlier is left in
-// fp32: what is finite there is 0 times 2^-300, also where negative steps
-// (without softplus) let it grow before.
-constexpr float kFaint = -4.0f, kNothing = -300.0f;
+// Log decay from a block to the segment's end below which nothing earlier is
+// left in fp32: what is finite there is 0 times 2^-300, also where negative
+// steps (without softplus) let it grow before.
+constexpr float kNothing = -300.0f;
 template <int V>
 struct Int {
     constexpr int operator()() const { return V; }
@@ -586,10 +584,10 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
 #pragma unroll
                     for (int k = k0(); k < k1(); ++k) s[nt] = mfma(vb, wx[j][k], s[nt]);
                 }
-                if constexpr (!kAhead)
+                if constexpr (N > 128)
                     fence();  // registers are short: no operand is read early
             };
-            // The third part, where the block is near enough to need it.
+            // The third part by itself: y's sums hold registers that it would need.
             const auto refine = [&](int q) {
                 bf16x8_t wx[2][3];
                 weighted(Int<1>(), q, wx);
@@ -603,18 +601,9 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
                     if (rest < kNothing)
                         break;
                     bf16x8_t wx[2][3];
-                    const bool near = rest > kFaint;
-                    if (N <= 128 && near) {
-                        weighted(Int<3>(), q, wx);
+                    weighted(Int<3>(), q, wx);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) update(q, Int<0>(), Int<3>(), nt, wx);
-                    } else {
-                        weighted(Int<2>(), q, wx);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) update(q, Int<0>(), Int<2>(), nt, wx);
-                        if (near)  // with 256 state columns the registers hold no three parts
-                            refine(q);
-                    }
+                    for (int nt = 0; nt < NT; ++nt) update(q, Int<0>(), Int<3>(), nt, wx);
                 }
             } else {
                 const bool updates = more || final_at;
@@ -712,8 +701,7 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
                     if (updates) {
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) update(1, Int<0>(), Int<3>(), nt, wx);
-                        if (total1 > kFaint)
-                            refine(0);
+                        refine(0);
                     }
                     finish(1, exp2_f32(log_to(1) - total1));
                 } else {
@@ -733,8 +721,7 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
                             decay_state(exp2_f32(total));
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) update(q, Int<0>(), Int<2>(), nt, wx);
-                            if (q == 1 || total1 > kFaint)
-                                refine(q);
+                            refine(q);
                         }
                         // M[t, s] = (c_t . b_s) dt_s 2^(G_t - G_s) over the block's own tokens
                         const float f = exp2_f32(log_t);

@@ -87,3 +87,29 @@ def test_scan_product_operand_is_good_to_two_rounded_parts(N, s, t):
         out, fin = torch.empty(1, T, H, P, dtype=BF16, device="cuda"), torch.empty(1, H, P, N, device="cuda")
         scan(d, out, fin, dt_softplus=False)
         check_rest(f"token {t}", out[0, t].flatten(), v.expand(H * P), r.expand(H * P))
+
+
+@pytest.mark.parametrize("P,N", [(64, 128), (64, 64), (32, 256)])
+@pytest.mark.parametrize("segment_tokens", [None, 4096])
+@pytest.mark.parametrize("T,tail", [(320, 32), (320, 64), (300, 32), (300, 64)])
+def test_scan_state_of_a_quiet_tail_is_as_exact_as_fp32(P, N, segment_tokens, T, tail):
+    """Tokens whose x is zero or small at a prompt's end (padding, masked ones): the state is what earlier ones left,
+    and as exact.  Independent roundings leave 2^-20 (as where no token is quiet); the log decay d from the tail's start
+    carries up to six relative roundings common to all tokens (e^A_log, log2 e, their product, the steps, their product
+    and sums), which are 6 d ln 2 2^-24 of the state."""
+    g = torch.Generator().manual_seed(N + T + tail)
+    H = 8
+    per_block = torch.linspace(4.2, 12.0, H)
+    for scale in (0.0, 0.01):
+        a = ssm_inputs(g, 1, T, H, P, 1, N, 1, gate=False)
+        a["x"][:, T - tail:] *= scale
+        a["dt"], a["dt_bias"] = torch.full((1, T, H), 0.125, dtype=BF16), None
+        a["A_log"] = torch.log(per_block / 32 / 0.125 * 0.693147181)
+        want, final, _, _ = ref.ssm(a["x"], a["dt"], a["b"], a["c"], a["A_log"], a["D"], None, None, a["initial"], None, False)
+        d = {k: on_gpu(v) for k, v in a.items()}
+        out, fin = torch.empty(1, T, H, P, dtype=BF16, device="cuda"), torch.empty_like(d["initial"])
+        scan(d, out, fin, segment_tokens=segment_tokens, dt_softplus=False)
+        for h in range(H):
+            error = float((fin[:, h].double().cpu() - final[:, h]).norm() / final[:, h].norm())
+            bound = 2.0 ** -20 + 6 * 0.6931 * 2.0 ** -24 * float(per_block[h]) * tail / 32
+            assert error <= bound, (scale, h, error, bound)
