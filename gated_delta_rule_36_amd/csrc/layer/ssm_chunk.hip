@@ -410,8 +410,11 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
     const auto step_dt = [&](int tt, float plain) {
         const int ln = here(lane), buf = (tt / TM) & 1;
         const float raw = bf16_to_f32(static_cast<uint16_t>(rdt)) + dt_bias;
-        const float dt = tt + ln < tokens ? softplus_f32(raw, plain) : 0.0f;
-        const float a = fmaxf(rate * dt, -160.0f);
+        const bool inside = tt + ln < tokens;  // behind the end nothing decays, however strong the rate
+        const float step = inside ? softplus_f32(raw, plain) : 0.0f, log_keep = inside ? rate * step : 0.0f;
+        // a decay that is not a number makes its step NaN, which reaches y and S,
+        // and counts as the strongest one in the sums
+        const float dt = log_keep == log_keep ? step : log_keep, a = fmaxf(log_keep, -160.0f);
         float r = after32(a, ln);
         if constexpr (OUT) {
             const float abs_sum = prefix32(fabsf(a));

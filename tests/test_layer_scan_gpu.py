@@ -113,3 +113,32 @@ def test_scan_state_of_a_quiet_tail_is_as_exact_as_fp32(P, N, segment_tokens, T,
             error = float((fin[:, h].double().cpu() - final[:, h]).norm() / final[:, h].norm())
             bound = 2.0 ** -20 + 6 * 0.6931 * 2.0 ** -24 * float(per_block[h]) * tail / 32
             assert error <= bound, (scale, h, error, bound)
+
+
+@pytest.mark.parametrize("T,segment_tokens", [(4, None), (70, None), (300, 64), (300, None)])
+@pytest.mark.parametrize("N", [64, 256])
+def test_scan_decay_parameters_that_are_not_finite(T, segment_tokens, N):
+    """A_log = NaN makes its head's outputs and state NaN, at any length; A_log = inf forgets everything before a
+    token (exp(-inf dt) = 0), so its state is the last token's, also where the last tile is not full."""
+    g = torch.Generator().manual_seed(T + N)
+    H, P = 3, 32
+    a = ssm_inputs(g, 1, T, H, P, 1, N, 1)
+    d = {k: on_gpu(v) for k, v in a.items()}
+
+    def run():
+        out, fin = torch.empty(1, T, H, P, dtype=BF16, device="cuda"), torch.empty_like(d["initial"])
+        scan(d, out, fin, segment_tokens=segment_tokens)
+        return out, fin
+
+    clean, cf = run()
+    d["A_log"][1] = a["A_log"][1] = float("nan")
+    out, fin = run()
+    assert bool(out[:, :, 1].isnan().all()) and bool(fin[:, 1].isnan().all())
+    assert torch.equal(out[:, :, [0, 2]], clean[:, :, [0, 2]]) and torch.equal(fin[:, [0, 2]], cf[:, [0, 2]])
+    d["A_log"][1] = a["A_log"][1] = float("inf")
+    out, fin = run()
+    want, final, scale, fscale = ref.ssm(a["x"], a["dt"], a["b"], a["c"], a["A_log"], a["D"], a["dt_bias"], a["z"],
+                                         a["initial"])
+    # the tolerances of the parity tests
+    check("final_state", fin, final, 2.0 ** -15 * fscale)
+    check("out", out, want, 2.0 ** -14 * scale)
