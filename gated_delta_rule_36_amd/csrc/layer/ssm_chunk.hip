@@ -88,6 +88,9 @@ constexpr float kSteep = -40.0f;
 // left in fp32: what is finite there is 0 times 2^-300, also where negative
 // steps (without softplus) let it grow before.
 constexpr float kNothing = -300.0f;
+// Weights from 2^32 on and x from 2^96 on are looked at one by one (see scrub):
+// below, their product is finite.
+constexpr float kLargeWeight = 0x1p32f;
 template <int V>
 struct Int {
     constexpr int operator()() const { return V; }
@@ -130,6 +133,11 @@ __device__ __forceinline__ int here(int x)
     return x;
 }
 __device__ __forceinline__ const char *bytes(const uint16_t *p) { return reinterpret_cast<const char *>(p); }
+// a b + c over the two bf16 numbers of a and b.
+__device__ __forceinline__ float dot2_bf16(uint32_t a, uint32_t b, float c)
+{
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, a), __builtin_bit_cast(bf16x2_t, b), c, false);
+}
 // v as a sum of bf16 numbers, each what is left rounded to nearest: two leave
 // 2^-17 of v at most (half a step of 2^-8 v, which is half a step of v), three
 // hold its 24 bits.
@@ -179,6 +187,12 @@ __device__ __forceinline__ float read_lane(float x, int lane)
 {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
 }
+// x, the same in all lanes, as worked out up to here.
+__device__ __forceinline__ float of_wave(float x)
+{
+    asm volatile("" : "+v"(x));
+    return read_lane(x, 0);
+}
 // Sums over the 32 lanes of each wave half up to and with each lane.
 template <typename V>
 __device__ __forceinline__ V prefix32(V x)
@@ -218,7 +232,14 @@ struct Shared {
     alignas(16) float w[2][NW][TM];
     float total[2][NW][2], unit[2][NW][2];
     float dt_plain;  // dt + bias above this is taken as it is
+    // What earlier tokens' outputs have to be kept from (see scrub): per head the
+    // tile's first step that is not finite (kNoToken: none, kLarge: none, but a
+    // large weight), per loading wave whether it loaded an x that is large or not
+    // finite, and per column of a wave the first token taken out.
+    int odd_dt[2][NW], odd_x[NW];
+    alignas(16) uint8_t taken[NW][OUT ? 32 : 1];
 };
+constexpr int kNoToken = TM, kLarge = TM + 1;  // both behind every token
 
 // Column of a unit that row / column l32 of its matrices stands for.
 __device__ __forceinline__ int unit_column(int l32) { return 16 * ((l32 >> 2) & 1) + 4 * (l32 >> 3) + (l32 & 3); }
@@ -317,9 +338,10 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
     const int64_t state_at = ((tile.n * p.H + h) * p.P + colblk * 32) * N;
     float *const slab = p.slabs + ((static_cast<int64_t>(slot) * p.H + h) * p.P + colblk * 32) * N;
 
-    const float rate = -expf(p.A_log[dh]) * kLog2eF;
-    const float dt_bias = p.dt_bias ? p.dt_bias[dh] : 0.0f;
-    const float skip = OUT && p.D ? p.D[h] : 0.0f;
+    // One value a wave each, kept in scalar registers.
+    const float rate = of_wave(-expf(p.A_log[dh]) * kLog2eF);
+    const float dt_bias = of_wave(p.dt_bias ? p.dt_bias[dh] : 0.0f);
+    const float skip = of_wave(OUT && p.D ? p.D[h] : 0.0f);
 
     f32x16_t s[NT];
     if (OUT && active && p.slabs) {
@@ -349,7 +371,7 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
                 sh.cb[blk][part][j][hf][tid & 15][e] = 0;
     }
 
-    u32x4_t rb[kLoadB], rc[OUT ? kLoadB : 1], rx[kLoadX];
+    u32x4_t rb[kLoadB], rc[OUT ? kLoadB : 1], rx[kLoadX] = {};
     uint32_t rdt = 0;
     float after = 0.0f;  // sum of a over the tiles after this one (!OUT; this wave's dt head)
     // Loads the tile from token tt on and moves on to the next.
@@ -411,12 +433,19 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
         const int ln = here(lane), buf = (tt / TM) & 1;
         const float raw = bf16_to_f32(static_cast<uint16_t>(rdt)) + dt_bias;
         const bool inside = tt + ln < tokens;  // behind the end nothing decays, however strong the rate
-        const float step = inside ? softplus_f32(raw, plain) : 0.0f, log_keep = inside ? rate * step : 0.0f;
-        // a decay that is not a number makes its step NaN, which reaches y and S,
-        // and counts as the strongest one in the sums
-        const float dt = log_keep == log_keep ? step : log_keep, a = fmaxf(log_keep, -160.0f);
+        float dt = inside ? softplus_f32(raw, plain) : 0.0f;
+        const float log_keep = inside ? rate * dt : 0.0f;
+        // Not a number, or a growth beyond fp32: as a step that is not finite, and
+        // in the sums as the strongest decay.
+        const bool keeps = log_keep < 128.0f;
+        const float a = keeps ? fmaxf(log_keep, -160.0f) : -160.0f;
+        dt = keeps ? dt : __builtin_nanf("");
         float r = after32(a, ln);
+        uint64_t odd = 0;
         if constexpr (OUT) {
+            const bool finite = fabsf(dt) < __builtin_inff();
+            odd = __ballot(!finite);
+            dt = finite ? dt : 0.0f;
             const float abs_sum = prefix32(fabsf(a));
             const float s0 = read_lane(abs_sum, 31), s1 = read_lane(abs_sum, 63);
             // 2^e <= sum < 2^(e + 1): a unit of 2^(e - 29)
@@ -443,7 +472,13 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
             r += ln < 32 ? b1 + after : after;
             after += b0 + b1;
         }
-        sh.w[buf][wave][ln] = dt * exp2_f32(r);
+        const float w = dt * exp2_f32(r);
+        sh.w[buf][wave][ln] = w;
+        if constexpr (OUT) {
+            const bool large = __any(!(fabsf(w) < kLargeWeight));
+            if (ln == 0)
+                sh.odd_dt[buf][wave] = odd ? __builtin_ctzll(odd) : large ? kLarge : kNoToken;
+        }
     };
     const auto put = [](uint16_t *dst, u32x4_t v) {  // rows are 8-byte aligned
         *reinterpret_cast<u32x2_t *>(dst) = u32x2_t{v[0], v[1]};
@@ -488,6 +523,17 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
             }
 #pragma unroll
             for (int k = 0; k < kLoadX; ++k) put(&sh.x[wx0 + ln / PX + k * SX][ln % PX * 8], rx[k]);
+            if constexpr (OUT) {
+                // not finite once an x is not, or is 2^96 or more
+                float sum = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kLoadX; ++k)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sum = dot2_bf16(rx[k][i], 0x4f804f80u, sum);  // times 2^32
+                const bool odd = __any(!(fabsf(sum) < __builtin_inff()));
+                if (ln == 0)
+                    sh.odd_x[wave] = odd;
+            }
         }
         lds_barrier();
         const int buf = (tt / TM) & 1;
@@ -597,6 +643,41 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) update(q, Int<2>(), Int<3>(), nt, wx);
             };
+            const int odd_dt = OUT ? __builtin_amdgcn_readfirstlane(sh.odd_dt[buf][hs]) : kNoToken;
+            const bool suspect = OUT && (odd_dt != kNoToken || __any(sh.odd_x[ln & (NW - 1)]));
+            // A product of 0 (in c b^T, M) and what is not finite is NaN, and would
+            // take a token into the outputs before it.  So an x whose product with
+            // its weight is not finite leaves its column (0 in its place), as a step
+            // that is not finite has left the weights, and the outputs from its token
+            // on and the state are made NaN (spoil, finish).
+            const auto scrub = [&]() {
+                const int t = here(ln);
+                int mine = kNoToken;  // of column t & 31
+                const float w = sh.w[buf][hs][t];
+#pragma unroll 1
+                for (int c = 0; c < 32; ++c) {
+                    uint16_t *x = &sh.x[t][wave * 32 + c];
+                    const bool out = !(fabsf(w * bf16_to_f32(*x)) < __builtin_inff());
+                    if (out)
+                        *x = 0;
+                    const uint64_t tokens_out = __ballot(out);
+                    mine = tokens_out && (t & 31) == c ? __builtin_ctzll(tokens_out) : mine;
+                }
+                if (t < 32)
+                    sh.taken[wave][t] = static_cast<uint8_t>(mine < odd_dt ? mine : odd_dt);
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            };
+            const auto spoil = [&]() {
+                const bool gone = sh.taken[wave][unit_column(here(l32))] < kNoToken;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) s[nt][r] = gone ? __builtin_nanf("") : s[nt][r];
+            };
+            if constexpr (OUT) {
+                if (suspect)
+                    scrub();
+            }
             if constexpr (!OUT) {
 #pragma unroll 1
                 for (int q = 1; q >= 0; --q) {
@@ -679,6 +760,13 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
 #pragma unroll
                             for (int r = 0; r < 16; ++r) o[r] *= silu_f32(z[r]);
                         }
+                        if (suspect) {
+                            const u32x4_t from = *reinterpret_cast<const u32x4_t *>(&sh.taken[wave][here(16 * half)]);
+                            const uint32_t at = here(l32) + CH * q;
+#pragma unroll
+                            for (int r = 0; r < 16; ++r)
+                                o[r] = (from[r / 4] >> (8 * (r & 3)) & 0xff) <= at ? __builtin_nanf("") : o[r];
+                        }
                         const uint32_t o_off = 2 * (l32 * static_cast<uint32_t>(width) + 16 * half);
                         *reinterpret_cast<u32x4_t *>(op + o_off) = pack8(o);
                         *reinterpret_cast<u32x4_t *>(op + 16 + o_off) = pack8(o + 8);
@@ -754,6 +842,8 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
                         finish(q, 1.0f);
                     }
                 }
+                if (suspect)
+                    spoil();
             }
             __builtin_amdgcn_s_setprio(3);
         }

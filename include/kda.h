@@ -408,10 +408,12 @@ kda_status kda_short_conv(const kda_conv_args *args, void *stream);
  *                  kda_ssm_workspace_bytes(args) bytes (which may be 0), as
  *                  for kda_fwd_scan (KDA_ERR_WORKSPACE otherwise).
  *
- * A non-finite x, dt, b or c may reach every output of its head from the start
- * of its tile of 64 tokens to the end of its sequence (of the group's heads, for
- * b and c; x: of its 32 columns), or no later one where the state has decayed by
- * more than 2^-300 in between.  It never reaches another sequence.
+ * A non-finite x, dt, b or c reaches outputs from its own token on, never
+ * earlier ones: those of its column (x), head (dt) or group's heads (b; c: at
+ * its token alone), to the end of its sequence, or none after the state has
+ * decayed by more than 2^-300.  It never reaches another sequence.  A step that
+ * grows the state by 2^128 or more counts as non-finite, and so does an A_log
+ * that is NaN.
  */
 typedef struct kda_ssm_args {
     const void *x;

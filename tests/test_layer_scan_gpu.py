@@ -142,3 +142,61 @@ def test_scan_decay_parameters_that_are_not_finite(T, segment_tokens, N):
     # the tolerances of the parity tests
     check("final_state", fin, final, 2.0 ** -15 * fscale)
     check("out", out, want, 2.0 ** -14 * scale)
+
+
+NAN, INF, LOWEST = float("nan"), float("inf"), torch.finfo(BF16).min
+
+
+@pytest.mark.parametrize("T,segment_tokens", [(6, None), (150, None), (150, 64), (150, 96)])
+@pytest.mark.parametrize("N", [64, 128, 256])
+@pytest.mark.parametrize("kind,value", [("x", NAN), ("x", INF), ("x", -INF), ("x", LOWEST), ("dt", NAN), ("dt", INF),
+                                        ("dt", LOWEST), ("b", NAN), ("b", -INF), ("c", NAN), ("c", INF)])
+def test_scan_inputs_that_are_not_finite_never_reach_earlier_tokens(T, segment_tokens, N, kind, value):
+    """One value of a padded or masked token: the outputs before it are those without it, its own and later ones of its
+    column (x), head (dt) or group (b; c: its own token) are not finite, and everything else stays as it was.  The
+    first head decays little, the second by some 2^-60 in 64 tokens.  LOWEST: with dt a growth by 2^(10^38) (a step
+    without softplus); x times its step is beyond fp32, but not what the decay leaves of it, which need not be infinite."""
+    g = torch.Generator().manual_seed(T + N)
+    H, P = 2, 64
+    a = ssm_inputs(g, 1, T, H, P, 1, N, 1)
+    a["dt"], a["dt_bias"] = (1 + 0.2 * torch.randn(1, T, H, generator=g)).abs().to(BF16), None
+    a["A_log"] = torch.log(torch.tensor([0.1, 0.95]) * 0.6931)
+    for s in [0, 3, 5] if T == 6 else [0, 7, 31, 32, 45, 63, 64, 100, 149]:
+        a["dt"][0, s] = 2.0
+        d = {k: on_gpu(v) for k, v in a.items()}
+
+        def run():
+            out, fin = torch.empty(1, T, H, P, dtype=BF16, device="cuda"), torch.empty_like(d["initial"])
+            scan(d, out, fin, segment_tokens=segment_tokens, dt_softplus=False)
+            return out.cpu(), fin.cpu()
+
+        clean, cf = run()
+        where = {"x": (0, s, 1, 9), "dt": (0, s, 1), "b": (0, s, 0, 3), "c": (0, s, 0, 3)}[kind]
+        for h in range(H if kind in ("x", "dt") else 1):
+            at = (*where[:2], h, *where[3:]) if kind in ("x", "dt") else where
+            kept = d[kind][at].clone()
+            d[kind][at] = value
+            out, fin = run()
+            d[kind][at] = kept
+            touched = torch.zeros(out.shape, dtype=torch.bool)
+            if kind == "x":
+                touched[:, s:, h, 9] = True
+            elif kind == "dt":
+                touched[:, s:, h] = True
+            else:
+                touched[:, s:s + 1 if kind == "c" else T] = True
+            if kind == "dt":   # the other tokens' decays are rounded in other units: the parity tests' tolerance
+                want, _, scale, _ = ref.ssm(a["x"], a["dt"], a["b"], a["c"], a["A_log"], a["D"], None, a["z"],
+                                            a["initial"], None, False)
+                check("out", out[:, :s, h], want[:, :s, h], 2.0 ** -14 * scale[:, :s, h])
+                touched[:, :s, h] = True
+            assert torch.equal(out[~touched], clean[~touched]), (s, h)
+            assert (kind, value) == ("x", LOWEST) or not bool(out[:, s:][touched[:, s:]].isfinite().any()), (s, h)
+            if kind == "x":
+                assert value == LOWEST or not bool(fin[0, h, 9].isfinite().any())
+                fin[0, h, 9] = cf[0, h, 9]
+            if kind == "dt":
+                assert not bool(fin[0, h].isfinite().any())
+                fin[0, h] = cf[0, h]
+            if kind != "b":
+                assert torch.equal(fin, cf), (s, h)
