@@ -11,11 +11,12 @@
 // Since 2^(G_t - G_s) dt_s = 2^(G_t - T) w_s, the sum over a block's own tokens
 // takes the same weighted x as the state: 2^(G_t - T) sum (c_t . b_s) w_s x_s,
 // and c b^T, which the heads of a group share, is the other factor.  A gentle
-// tile, one that decays by less than 2^-40 in all, scales its first block's
-// weights and the state to the tile's end at once, so that 2^(G_t - T) stays
-// well inside fp32's range.  A steep one goes block by block and forms
-// M[t,s] = (c_t . b_s) 2^(G_t - G_s) dt_s itself; no other exponent is positive
-// there, so nothing overflows however strong the decay.
+// tile, one that decays by less than 2^-40 in all (and, where steps may be
+// negative, neither decays nor grows by more from any token to its end), scales
+// its first block's weights and the state to the tile's end at once, so that
+// 2^(G_t - T) stays well inside fp32's range.  A steep one goes block by block
+// and forms M[t,s] = (c_t . b_s) 2^(G_t - G_s) dt_s itself; no other exponent is
+// positive there after softplus, so nothing overflows however strong the decay.
 //
 // A difference of G loses what a strong decay in the same block rounds away,
 // so G is held in fixed point: 32-bit integers in a unit of 2^-29 .. 2^-30 of
@@ -235,8 +236,9 @@ struct Shared {
     // What earlier tokens' outputs have to be kept from (see scrub): per head the
     // tile's first step that is not finite (kNoToken: none, kLarge: none, but a
     // large weight), per loading wave whether it loaded an x that is large or not
-    // finite, and per column of a wave the first token taken out.
-    int odd_dt[2][NW], odd_x[NW];
+    // finite, and per column of a wave the first token taken out.  And whether the
+    // tile is a gentle one for the head.
+    int odd_dt[2][NW], odd_x[NW], gentle[2][NW];
     alignas(16) uint8_t taken[NW][OUT ? 32 : 1];
 };
 constexpr int kNoToken = TM, kLarge = TM + 1;  // both behind every token
@@ -461,7 +463,11 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
             }
             // a gentle tile weighs its first block up to the tile's end
             const float b1 = read_lane(r + a, 32), both = read_lane(total, 31) + read_lane(total, 63);
-            r += ln < 32 && kAhead && both >= kSteep ? b1 : 0.0f;
+            const float to_end = r + (ln < 32 ? b1 : 0.0f);
+            const bool gentle = kAhead && !__any(fabsf(to_end) > -kSteep || both < kSteep);
+            r = gentle ? to_end : r;
+            if (ln == 0)
+                sh.gentle[buf][wave] = gentle;
         } else {
             // from the block's end to the segment's
             const float b0 = read_lane(r + a, 0), b1 = read_lane(r + a, 32);
@@ -692,7 +698,7 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
             } else {
                 const bool updates = more || final_at;
                 const float total0 = read_lane(sh.total[buf][hs][0], 0), total1 = read_lane(sh.total[buf][hs][1], 0);
-                const bool gentle = kAhead && total0 + total1 >= kSteep;  // never with 256 state columns
+                const bool gentle = kAhead && __builtin_amdgcn_readfirstlane(sh.gentle[buf][hs]);  // never with 256 state columns
                 f32x16_t y[2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q)

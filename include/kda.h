@@ -391,7 +391,9 @@ kda_status kda_short_conv(const kda_conv_args *args, void *stream);
  *   b, c           bf16 [B,T,G,N]; heads h with the same h / (H / G) share a
  *                  group's b and c (G divides H).
  *   A_log, D, dt_bias  fp32 [H]; D and dt_bias may be NULL (0).
- *   softplus       1 or 0.  Without it a negative dt grows the state.
+ *   softplus       1 or 0.  Without it a negative dt grows the state: by up to
+ *                  2^100 from any token to a later one, beyond which results
+ *                  may be infinite or NaN.
  *   initial_state, final_state  [N_seq,H,P,N] of their dtypes, as for
  *                  kda_fwd (they may be one buffer).
  *   cu_seqlens, num_seqs, B, T, H   as for kda_fwd.

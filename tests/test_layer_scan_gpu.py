@@ -200,3 +200,24 @@ def test_scan_inputs_that_are_not_finite_never_reach_earlier_tokens(T, segment_t
                 fin[0, h] = cf[0, h]
             if kind != "b":
                 assert torch.equal(fin, cf), (s, h)
+
+
+@pytest.mark.parametrize("N", [64, 128, 256])
+@pytest.mark.parametrize("up,down", [((0, 16), (32, 48)), ((2, 30), (31, 60)), ((32, 40), (48, 64)), ((0, 30), (64, 90))])
+def test_scan_growth_that_a_decay_takes_back(N, up, down):
+    """Negative steps (without softplus) grow the state by 2^100 and positive ones take 2^138 of it, within a block, a
+    tile or from one to the next: the tolerances of the parity tests hold, relative to the sums' absolute values."""
+    g = torch.Generator().manual_seed(N)
+    T, H, P = 100, 2, 32
+    a = ssm_inputs(g, 1, T, H, P, 1, N, 1, gate=False)
+    a["dt"], a["dt_bias"] = torch.full((1, T, H), 2.0 ** -7, dtype=BF16), None
+    a["A_log"] = torch.log(torch.tensor([0.6931, 0.6931]))
+    a["dt"][:, up[0]:up[1]] = -100.0 / (up[1] - up[0])
+    a["dt"][:, down[0]:down[1]] = 138.0 / (down[1] - down[0])
+    want, final, scale, fscale = ref.ssm(a["x"], a["dt"], a["b"], a["c"], a["A_log"], a["D"], None, None, a["initial"], None,
+                                         False)
+    d = {k: on_gpu(v) for k, v in a.items()}
+    out, fin = torch.empty(1, T, H, P, dtype=BF16, device="cuda"), torch.empty_like(d["initial"])
+    scan(d, out, fin, dt_softplus=False)
+    check("final_state", fin, final, 2.0 ** -15 * fscale)
+    check("out", out, want, 2.0 ** -14 * scale)
