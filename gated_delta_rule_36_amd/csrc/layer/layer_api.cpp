@@ -180,8 +180,9 @@ namespace {
 struct SsmPlan {
     bool recurrent = false;
     int64_t seg = 0;              // tokens a segment (chunked kernel)
-    int64_t slots = 0, slab = 0;  // slots and floats a slot, slab = 0 without segments
-    int64_t bytes = 0;            // workspace
+    kda::layer::SlabMap map = {};  // no slabs without segments
+    int64_t slab = 0;              // floats a slab
+    int64_t bytes = 0;             // workspace
 };
 
 // Calls without cu_seqlens of up to kSsmRecurrentMaxTokens tokens: the token
@@ -219,12 +220,12 @@ bool ssm_plan(const kda_ssm_args &a, const Seqs &s, SsmPlan *plan)
             seg = kTile;
     }
     plan->seg = seg < longest ? seg : longest;
-    plan->slots = kda::layer::tile_slots(s, plan->seg);
     if (plan->seg >= longest)
         return true;
+    plan->map = kda::layer::slab_map(s, plan->seg);
     plan->slab = a.H * a.P * a.N;
     int64_t n;
-    return mul_ok(plan->slots, 4 * (plan->slab + a.H), &n) && add_ok(n, 15, &plan->bytes) && (plan->bytes &= ~int64_t(15)) >= 0;
+    return mul_ok(plan->map.slabs, 4 * (plan->slab + a.H), &n) && add_ok(n, 15, &plan->bytes) && (plan->bytes &= ~int64_t(15)) >= 0;
 }
 
 }  // namespace
@@ -319,9 +320,10 @@ extern "C" kda_status kda_ssm_fwd(const kda_ssm_args *args, void *stream)
     if (plan.recurrent)
         return launched(kda::layer::launch_ssm_recurrent(p, static_cast<hipStream_t>(stream)));
     p.seg = plan.seg;
-    if (plan.slab > 0) {
+    p.map = plan.map;
+    if (plan.map.slabs > 0) {
         p.slabs = static_cast<float *>(a.workspace);
-        p.logs = p.slabs + plan.slots * plan.slab;
+        p.logs = p.slabs + plan.map.slabs * plan.slab;
     }
     return launched(kda::layer::launch_ssm_chunk(p, static_cast<hipStream_t>(stream)));
 }

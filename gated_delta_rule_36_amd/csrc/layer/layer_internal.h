@@ -30,6 +30,27 @@ inline int64_t tile_slots(const Seqs &s, int64_t len)
     return s.N * (s.T > 0 ? (s.T + len - 1) / len : 1);
 }
 
+// State slabs for sequences of more than one segment of len tokens, one a
+// segment; a sequence of one segment takes its state where it lies, so that many
+// short ones need no more than T / len allow.  The slabs of sequence n, over
+// tokens [a, b), start at mul floor(a / len) + add n.  In a batch each has as
+// many as segments.  Of packed ones, count = ceil((b - a) / len) is at most
+// floor(b / len) - floor(a / len) + 1, which leaves room with (1, 1); and from two
+// segments on count <= 2 (count - 1), which leaves room with (2, 0).  All slabs
+// are below the total for any offsets 0 <= a <= b <= T, in order or not.
+struct SlabMap {
+    int64_t mul, add, slabs;
+};
+inline SlabMap slab_map(const Seqs &s, int64_t len)
+{
+    if (!s.cu) {
+        const int64_t per = (s.T + len - 1) / len;
+        return {0, per, per > 1 ? s.N * per : 0};
+    }
+    const int64_t whole = s.T / len;
+    return s.N < whole ? SlabMap{1, 1, whole + s.N} : SlabMap{2, 0, 2 * whole};
+}
+
 // Whether a grid of one dimension takes this many workgroups: a launch counts
 // its threads in 32 bits.  Launches that do not fit return
 // hipErrorInvalidConfiguration.
@@ -91,9 +112,10 @@ struct SsmParams {
     Seqs seqs;
     int64_t H, P, G, N;
     int softplus;
-    // chunked kernel: tokens a segment; with more than one segment a sequence,
-    // a state [H,P,N] and log decays [H] per work slot (else nullptr)
+    // chunked kernel: tokens a segment; if a sequence can have more than one, the
+    // slabs (see slab_map): a state [H,P,N] and log decays [H] each (else nullptr)
     int64_t seg;
+    SlabMap map;
     float *slabs, *logs;
 };
 // Tokens per chunk of the chunked kernel; segments are multiples of it.

@@ -336,9 +336,10 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
     const int wcol = h * static_cast<int>(p.P) + colblk * 32;  // the unit's first output column
     const char *zp = OUT && p.z ? bytes(p.z + tile.row * p.zb + first * p.zt + wcol) : nullptr;
     char *op = reinterpret_cast<char *>(p.out + (tile.row * p.seqs.T + first) * width + wcol);
-    // The unit in the states, and in the slabs [H][P / 32][4 N / 32][lane][4].
+    // The unit in the states, and in its segment's slab [H][P / 32][4 N / 32][lane][4].
     const int64_t state_at = ((tile.n * p.H + h) * p.P + colblk * 32) * N;
-    float *const slab = p.slabs + ((static_cast<int64_t>(slot) * p.H + h) * p.P + colblk * 32) * N;
+    const int64_t slab_no = p.map.mul * (tile.begin / seg) + p.map.add * tile.n + tile.index;
+    float *const slab = p.slabs + ((slab_no * p.H + h) * p.P + colblk * 32) * N;
 
     // One value a wave each, kept in scalar registers.
     const float rate = of_wave(-expf(p.A_log[dh]) * kLog2eF);
@@ -346,7 +347,7 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
     const float skip = of_wave(OUT && p.D ? p.D[h] : 0.0f);
 
     f32x16_t s[NT];
-    if (OUT && active && p.slabs) {
+    if (OUT && active && !(last && tile.index == 0)) {  // one of several segments
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -880,13 +881,15 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
         }
         // several workgroups may hold columns of one head: they write the same value
         if (keeps_dt && lane == 0)
-            p.logs[static_cast<int64_t>(slot) * p.H + dh] = after;
+            p.logs[slab_no * p.H + dh] = after;
     }
 }
 
 // The states in front of the segments, in order: start_0 = the initial state,
 // start_(k+1) = 2^(log decay of k) start_k + own state of k, each over its
-// segment's slab.  A thread carries four elements of one (sequence, head).
+// segment's slab.  (The first one too: the output pass may write the final
+// state over the initial one.)  Sequences of one segment are left to the output
+// pass.  A thread carries four elements of one (sequence, head).
 constexpr int kJoinThreads = 256;
 __global__ __launch_bounds__(kJoinThreads) void ssm_join_kernel(SsmParams p, int64_t quads)
 {
@@ -894,21 +897,13 @@ __global__ __launch_bounds__(kJoinThreads) void ssm_join_kernel(SsmParams p, int
     const uint32_t q = (blockIdx.x - chain * per) * kJoinThreads + threadIdx.x;  // quad within the head's slab
     const uint32_t heads = static_cast<uint32_t>(p.H), seg = static_cast<uint32_t>(p.seg);
     const int64_t n = chain / heads, h = chain - static_cast<uint32_t>(n) * heads;
-    uint32_t len = static_cast<uint32_t>(p.seqs.T), first = 0;
-    if (p.seqs.cu && p.seqs.N <= kLaneSequences) {
-        const LaneSequence s = lane_sequence(p.seqs, seg, __lane_id());
-        const int at = __builtin_amdgcn_readfirstlane(static_cast<int>(n));
-        len = __builtin_amdgcn_readlane(s.end, at) - __builtin_amdgcn_readlane(s.begin, at);
-        first = __builtin_amdgcn_readlane(s.first, at);
-    } else if (p.seqs.cu) {
-        const uint32_t a = clamp_offset(p.seqs, n), b = clamp_offset(p.seqs, n + 1);
-        first = a / seg + static_cast<uint32_t>(n);
-        len = b > a ? b - a : 0;
+    uint32_t begin = 0, end = static_cast<uint32_t>(p.seqs.T);
+    if (p.seqs.cu) {
+        begin = clamp_offset(p.seqs, n);
+        end = clamp_offset(p.seqs, n + 1);
     }
-    const uint32_t count = len > 0 ? (len + seg - 1) / seg : 1;
-    const int64_t slot = p.seqs.cu ? first : n * count;
-    // offsets out of order may count more slots than there are
-    if (q >= quads || (p.seqs.cu && slot + count > p.seqs.T / seg + p.seqs.N))
+    const uint32_t count = end > begin ? (end - begin - 1) / seg + 1 : 1;
+    if (q >= quads || count == 1)
         return;
     f32x4_t run = {0, 0, 0, 0};
     if (p.init_kind != kNone) {
@@ -924,8 +919,9 @@ __global__ __launch_bounds__(kJoinThreads) void ssm_join_kernel(SsmParams p, int
         }
     }
     const int64_t step = p.H * p.P * p.N;
-    float *slab = p.slabs + (slot * p.H + h) * p.P * p.N + 4 * q;
-    const float *logs = p.logs + slot * p.H + h;
+    const int64_t slab_no = p.map.mul * (begin / seg) + p.map.add * n;
+    float *slab = p.slabs + (slab_no * p.H + h) * p.P * p.N + 4 * q;
+    const float *logs = p.logs + slab_no * p.H + h;
     // eight segments' loads at once: a store of this loop could be what the
     // next load reads, as far as the compiler knows
     constexpr uint32_t kAhead = 8;

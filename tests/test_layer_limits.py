@@ -1,0 +1,35 @@
+"""Limits and messages of the layer operators that no launch is needed for."""
+import pytest
+
+from gated_delta_rule_36_amd import _lib
+
+
+def workspace(**over):
+    fields = dict(B=1, T=0, H=32, P=64, G=1, N=128, softplus=1)
+    fields.update(over)
+    return _lib.load().kda_ssm_workspace_bytes(_lib.SsmArgs(**fields))
+
+
+STATE = 4 * (32 * 64 * 128 + 32)  # of the heads above, with their log decays
+
+
+@pytest.mark.parametrize("n,T", [(512, 512), (1000, 1000), (4096, 4096), (1000, 5000), (300, 40), (65, 64)])
+def test_many_short_sequences_need_little_workspace(n, T):
+    """Segments have 64 tokens at least and a sequence of one needs no slab, so T / 64 sequences at most have any, of
+    twice as many segments as 64-token steps they cross: never one for every sequence."""
+    assert 0 <= workspace(cu_seqlens=16, num_seqs=n, T=T) <= 2 * (T // 64) * STATE + 16
+
+
+@pytest.mark.parametrize("n,T,seg", [(1, 4096, 64), (8, 19595, 704), (3, 1000, 32), (100, 1000, 32), (7, 33, 32), (2, 31, 32)])
+def test_workspace_of_packed_segments(n, T, seg):
+    whole = T // seg if T > seg else 0
+    assert workspace(cu_seqlens=16, num_seqs=n, T=T, seg_tokens=seg) <= min(2 * whole, whole + n) * STATE + 16
+    assert (workspace(cu_seqlens=16, num_seqs=n, T=T, seg_tokens=seg) > 0) == (T > seg)
+
+
+def test_workspace_of_a_batch():
+    """As many slabs as segments where there are several, none where there is one."""
+    assert workspace(B=4, T=4096, seg_tokens=512) == 4 * 8 * STATE
+    assert workspace(B=4, T=4090, seg_tokens=512) == 4 * 8 * STATE
+    assert workspace(B=4, T=512, seg_tokens=512) == 0
+    assert workspace(B=4, T=8) == 0

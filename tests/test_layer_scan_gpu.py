@@ -3,9 +3,9 @@ splits under cancellation, quiet tails, non-finite inputs, workspaces."""
 import pytest
 import torch
 
-import gated_delta_rule_36_amd as kda
 import layer_ref as ref
-from test_layer_gpu import BF16, F32, check, normal, on_gpu, scan, ssm_inputs
+from gated_delta_rule_36_amd import _lib
+from test_layer_gpu import BF16, F32, check, on_gpu, scan, ssm_case, ssm_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -221,3 +221,48 @@ def test_scan_growth_that_a_decay_takes_back(N, up, down):
     scan(d, out, fin, dt_softplus=False)
     check("final_state", fin, final, 2.0 ** -15 * fscale)
     check("out", out, want, 2.0 ** -14 * scale)
+
+
+@pytest.mark.parametrize("cu", [[0, 130], list(range(131)), [0, 1, 2, 3, 100, 130], [0] + [2 * i for i in range(1, 66)], [0, 0, 64, 64, 130],
+                                [130, 90, 40, 0], [0, 130, 0, 130, 0, 130], [5, 127, 3, 130, 64, 64, -9, 1 << 40]])
+@pytest.mark.parametrize("segment_tokens", [32, 64, 96])
+def test_scan_stays_in_its_workspace(cu, segment_tokens):
+    """The workspace of exactly the bytes asked for lies between two guards, for offsets in order and not; the same
+    results as with the library's own, in place too."""
+    g = torch.Generator().manual_seed(len(cu))
+    T, H, P, N, n, edge = 130, 3, 32, 32, len(cu) - 1, 1 << 16
+    a = {k: on_gpu(v) for k, v in ssm_inputs(g, 1, T, H, P, 1, N, n).items()}
+    cug = torch.tensor(cu, dtype=torch.int64, device="cuda")
+    out, fin = torch.zeros(1, T, H, P, dtype=BF16, device="cuda"), torch.empty_like(a["initial"])
+    scan(a, out, fin, cu_seqlens=cug, check_cu_seqlens=False, segment_tokens=segment_tokens)
+    state, again = a["initial"].clone(), torch.zeros_like(out)
+    s = {k: t.stride() for k, t in a.items() if k in "xbcz" or k == "dt"}
+    args = _lib.SsmArgs(x=a["x"].data_ptr(), dt=a["dt"].data_ptr(), b=a["b"].data_ptr(), c=a["c"].data_ptr(),
+                        z=a["z"].data_ptr(), out=again.data_ptr(), x_stride_t=s["x"][1], dt_stride_t=s["dt"][1],
+                        b_stride_t=s["b"][1], c_stride_t=s["c"][1], z_stride_t=s["z"][1], A_log=a["A_log"].data_ptr(),
+                        D=a["D"].data_ptr(), dt_bias=a["dt_bias"].data_ptr(), initial_state=state.data_ptr(),
+                        final_state=state.data_ptr(), cu_seqlens=cug.data_ptr(), num_seqs=n, B=1, T=T, H=H, P=P, G=1,
+                        N=N, initial_state_dtype=_lib.KDA_DTYPE_FP32, final_state_dtype=_lib.KDA_DTYPE_FP32, softplus=1,
+                        seg_tokens=segment_tokens)
+    lib = _lib.load()
+    nbytes = lib.kda_ssm_workspace_bytes(args)
+    assert nbytes > 0
+    whole = torch.full((2 * edge + nbytes,), 7, dtype=torch.uint8, device="cuda")
+    args.workspace, args.workspace_bytes = whole.data_ptr() + edge, nbytes
+    assert lib.kda_ssm_fwd(args, torch.cuda.current_stream().cuda_stream) == _lib.KDA_OK
+    torch.cuda.synchronize()
+    assert bool((whole[:edge] == 7).all()) and bool((whole[edge + nbytes:] == 7).all())
+    if cu == sorted(cu):
+        assert torch.equal(out, again) and torch.equal(fin, state)
+
+
+@pytest.mark.parametrize("n,longest", [(200, 1), (300, 5), (60, 1), (150, 90)])
+@pytest.mark.parametrize("state", [BF16, F32])
+def test_scan_of_many_short_sequences(n, longest, state):
+    """Packed single tokens and short prompts, with a longer one among them, states in place."""
+    g = torch.Generator().manual_seed(n)
+    lengths = torch.randint(0, longest + 1, (n,), generator=g)
+    lengths[n // 3], lengths[n - 1] = 150, 1
+    cu = [0] + torch.cumsum(lengths, 0).tolist()
+    for segment_tokens in (None, 32):
+        ssm_case(1, cu[-1], 2, 32, 1, 64, seed=n, cu=cu, state=state, in_place=True, segment_tokens=segment_tokens)
