@@ -879,8 +879,9 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
                     *reinterpret_cast<f32x4_t *>(slab + (4 * nt + i) * 256 + 4 * lane) =
                         f32x4_t{s[nt][4 * i], s[nt][4 * i + 1], s[nt][4 * i + 2], s[nt][4 * i + 3]};
         }
-        // several workgroups may hold columns of one head: they write the same value
-        if (keeps_dt && lane == 0)
+        // Several workgroups may hold columns of one head, and their sums may differ
+        // below kNothing, where each stops: the one with the first column writes.
+        if (keeps_dt && lane == 0 && (wave > 0 || head0 * per_head == u0))
             p.logs[slab_no * p.H + dh] = after;
     }
 }

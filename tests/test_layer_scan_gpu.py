@@ -223,6 +223,22 @@ def test_scan_growth_that_a_decay_takes_back(N, up, down):
     check("out", out, want, 2.0 ** -14 * scale)
 
 
+def ssm_args(a, out, initial, final, segment_tokens, cu=None):
+    """The C arguments of a scan of GPU tensors `a`, without a workspace."""
+    (B, T, H, P), N = a["x"].shape, a["b"].shape[3]
+    args = _lib.SsmArgs(out=out.data_ptr(), A_log=a["A_log"].data_ptr(), D=a["D"].data_ptr(), dt_bias=a["dt_bias"].data_ptr(),
+                        initial_state=initial.data_ptr(), final_state=final.data_ptr(), B=B, T=T, H=H, P=P, G=1, N=N,
+                        initial_state_dtype=_lib.KDA_DTYPE_FP32, final_state_dtype=_lib.KDA_DTYPE_FP32, softplus=1,
+                        seg_tokens=segment_tokens)
+    if cu is not None:
+        args.cu_seqlens, args.num_seqs = cu.data_ptr(), cu.numel() - 1
+    for k in ("x", "dt", "b", "c", "z"):
+        setattr(args, k, a[k].data_ptr())
+        setattr(args, f"{k}_stride_b", a[k].stride(0))
+        setattr(args, f"{k}_stride_t", a[k].stride(1))
+    return args
+
+
 @pytest.mark.parametrize("cu", [[0, 130], list(range(131)), [0, 1, 2, 3, 100, 130], [0] + [2 * i for i in range(1, 66)], [0, 0, 64, 64, 130],
                                 [130, 90, 40, 0], [0, 130, 0, 130, 0, 130], [5, 127, 3, 130, 64, 64, -9, 1 << 40]])
 @pytest.mark.parametrize("segment_tokens", [32, 64, 96])
@@ -236,14 +252,7 @@ def test_scan_stays_in_its_workspace(cu, segment_tokens):
     out, fin = torch.zeros(1, T, H, P, dtype=BF16, device="cuda"), torch.empty_like(a["initial"])
     scan(a, out, fin, cu_seqlens=cug, check_cu_seqlens=False, segment_tokens=segment_tokens)
     state, again = a["initial"].clone(), torch.zeros_like(out)
-    s = {k: t.stride() for k, t in a.items() if k in "xbcz" or k == "dt"}
-    args = _lib.SsmArgs(x=a["x"].data_ptr(), dt=a["dt"].data_ptr(), b=a["b"].data_ptr(), c=a["c"].data_ptr(),
-                        z=a["z"].data_ptr(), out=again.data_ptr(), x_stride_t=s["x"][1], dt_stride_t=s["dt"][1],
-                        b_stride_t=s["b"][1], c_stride_t=s["c"][1], z_stride_t=s["z"][1], A_log=a["A_log"].data_ptr(),
-                        D=a["D"].data_ptr(), dt_bias=a["dt_bias"].data_ptr(), initial_state=state.data_ptr(),
-                        final_state=state.data_ptr(), cu_seqlens=cug.data_ptr(), num_seqs=n, B=1, T=T, H=H, P=P, G=1,
-                        N=N, initial_state_dtype=_lib.KDA_DTYPE_FP32, final_state_dtype=_lib.KDA_DTYPE_FP32, softplus=1,
-                        seg_tokens=segment_tokens)
+    args = ssm_args(a, again, state, state, segment_tokens, cug)
     lib = _lib.load()
     nbytes = lib.kda_ssm_workspace_bytes(args)
     assert nbytes > 0
@@ -266,3 +275,26 @@ def test_scan_of_many_short_sequences(n, longest, state):
     cu = [0] + torch.cumsum(lengths, 0).tolist()
     for segment_tokens in (None, 32):
         ssm_case(1, cu[-1], 2, 32, 1, 64, seed=n, cu=cu, state=state, in_place=True, segment_tokens=segment_tokens)
+
+
+def test_scan_decay_of_a_head_over_two_workgroups_has_one_writer():
+    """Heads of 96 columns, 8 units of 32 a workgroup: head 2 lies in two.  The first stops where all its heads have
+    forgotten, the second has one that keeps all and goes on.  The head's sum of logarithms in the workspace is the
+    first's, whichever ends last."""
+    g = torch.Generator().manual_seed(1)
+    T, H, P, N, seg = 1920, 6, 96, 32, 960
+    a = ssm_inputs(g, 1, T, H, P, 1, N, 1)
+    a["dt"], a["dt_bias"] = torch.full((1, T, H), 20.5, dtype=BF16), torch.zeros(H)
+    a["A_log"] = torch.log(torch.tensor([40.0, 40.0, 40.0, 1e-3, 40.0, 40.0]) / 64 / 20.5 * 0.6931)  # 2^-40 a tile
+    d = {k: on_gpu(v) for k, v in a.items()}
+    out, fin = torch.empty(1, T, H, P, dtype=BF16, device="cuda"), torch.empty_like(d["initial"])
+    args = ssm_args(d, out, d["initial"], fin, seg)
+    nbytes = _lib.load().kda_ssm_workspace_bytes(args)
+    work = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
+    args.workspace, args.workspace_bytes = work.data_ptr(), nbytes
+    for _ in range(4):
+        assert _lib.load().kda_ssm_fwd(args, torch.cuda.current_stream().cuda_stream) == _lib.KDA_OK
+        slabs = nbytes // (4 * (H * P * N + H))
+        logs = work[4 * slabs * H * P * N:][:4 * H].view(torch.float32).cpu()
+        assert bool((logs[:3] < -300).all()) and bool((logs[:3] > -420).all()), logs   # of 600 in all
+        assert -1.0 < float(logs[3]) < 0.0
