@@ -160,7 +160,7 @@ kda_status check_ssm_sizes(const kda_ssm_args &a, Seqs *s)
     if (a.P < 32 || a.P > 256 || a.P % 32 != 0 || (a.N != 32 && a.N != 64 && a.N != 128 && a.N != 256) ||
         a.seg_tokens < 0 || a.seg_tokens % kda::layer::kSsmChunk != 0)
         return KDA_ERR_SHAPE;
-    if (a.H < 1 || a.H > 65536)
+    if (a.H < 1 || a.H > 65536 || a.T > kda::layer::kSsmMaxTokens)
         return KDA_ERR_SIZE;
     if (a.G < 1 || a.H % a.G != 0)
         return KDA_ERR_SHAPE;

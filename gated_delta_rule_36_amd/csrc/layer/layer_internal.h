@@ -130,6 +130,9 @@ hipError_t launch_ssm_recurrent(const SsmParams &p, hipStream_t stream);
 hipError_t launch_ssm_chunk(const SsmParams &p, hipStream_t stream);
 // Waves of a workgroup of the chunked kernel, and columns a wave takes.
 constexpr int64_t kSsmWaves = 8, kSsmColumns = 32;
+// Tokens a call: the chunked kernel counts a segment's in 32 bits with sign, up to
+// two tiles (of two chunks) past its end.
+constexpr int64_t kSsmMaxTokens = INT32_MAX - 4 * kSsmChunk;
 // Token strides (elements) whose lane offsets stay within 32 bits of bytes: a
 // wave loads up to 16 rows of x, b or c from one base, and 32 of z.
 constexpr int64_t kSsmMaxStride = int64_t(1) << 27, kSsmMaxZStride = int64_t(1) << 26;

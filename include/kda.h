@@ -396,7 +396,8 @@ kda_status kda_short_conv(const kda_conv_args *args, void *stream);
  *                  may be infinite or NaN.
  *   initial_state, final_state  [N_seq,H,P,N] of their dtypes, as for
  *                  kda_fwd (they may be one buffer).
- *   cu_seqlens, num_seqs, B, T, H   as for kda_fwd.
+ *   cu_seqlens, num_seqs, B, T, H   as for kda_fwd, with T < 2^31 - 128
+ *                  (KDA_ERR_SIZE otherwise).
  *   P              a multiple of 32, at most 256; N is 32, 64, 128 or 256
  *                  (KDA_ERR_SHAPE otherwise).
  *   seg_tokens     tokens a segment: sequences longer than that are cut into

@@ -33,3 +33,17 @@ def test_workspace_of_a_batch():
     assert workspace(B=4, T=4090, seg_tokens=512) == 4 * 8 * STATE
     assert workspace(B=4, T=512, seg_tokens=512) == 0
     assert workspace(B=4, T=8) == 0
+
+
+@pytest.mark.parametrize("over", [dict(), dict(seg_tokens=32), dict(seg_tokens=1 << 31), dict(cu_seqlens=1 << 44, num_seqs=1)])
+def test_scan_token_counts_that_would_leave_32_bits_are_refused(over):
+    """Inputs may be broadcast over tokens (strides of 0), so such a call can fit the memory.  Nothing is launched: the
+    largest length allowed gets as far as the next check, here that of a pointer."""
+    fields = dict(B=1, H=1, P=32, G=1, N=32, softplus=1)
+    fields.update(over)
+    lib = _lib.load()
+    for T, code in (((1 << 31) - 129, _lib.KDA_ERR_NULL_POINTER), ((1 << 31) - 128, _lib.KDA_ERR_SIZE),
+                    ((1 << 31) - 64, _lib.KDA_ERR_SIZE), ((1 << 31) - 1, _lib.KDA_ERR_SIZE)):
+        args = _lib.SsmArgs(T=T, **fields)
+        assert lib.kda_ssm_fwd(args, None) == code, T
+        assert (lib.kda_ssm_workspace_bytes(args) < 0) == (code == _lib.KDA_ERR_SIZE), T
