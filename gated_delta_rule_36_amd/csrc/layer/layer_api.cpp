@@ -21,6 +21,8 @@ bool bf16_or_fp32(int32_t d) { return d == KDA_DTYPE_BF16 || d == KDA_DTYPE_FP32
 int64_t bytes_of(int32_t d) { return d == KDA_DTYPE_BF16 ? 2 : 4; }
 bool flag(int32_t v) { return v == 0 || v == 1; }
 bool norm_eps(double e) { return std::isfinite(e) && e >= 0.0; }
+// The kernels multiply in fp32: a scale has to be 0 or normal there.
+bool fp32_scale(double s) { return s == 0.0 || std::isnormal(static_cast<float>(s)); }
 
 // Byte range of a buffer.
 struct Span {
@@ -382,7 +384,7 @@ extern "C" kda_status kda_residual_norm(const kda_residual_norm_args *args, void
         return KDA_ERR_OPTION;
     if (a.D < 1 || a.D > kda::layer::kMaxNormSize)
         return KDA_ERR_SHAPE;
-    if (!norm_eps(a.eps) || !std::isfinite(a.residual_scale) || !std::isfinite(a.block_scale))
+    if (!norm_eps(a.eps) || !fp32_scale(a.residual_scale) || !fp32_scale(a.block_scale))
         return KDA_ERR_SCALE;
     if ((a.residual && !bf16_or_fp32(a.residual_dtype)) || (a.residual_out && !bf16_or_fp32(a.residual_out_dtype)) ||
         (a.post_weight && !bf16_or_fp32(a.post_weight_dtype)) || (a.gate && !bf16_or_fp32(a.gate_dtype)) ||

@@ -330,6 +330,7 @@ def residual_norm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: Opt
     in its last leading dimensions (``[B, 1, D]``: one a sequence).  Without
     ``residual`` (None) the stream starts here; ``weight`` and ``out`` are
     both None where no norm follows, and one of the outputs may be left out.
+    The scales are 0 or normal numbers of fp32.
     """
     device = _device(x)
     if x.dim() < 1:

@@ -503,7 +503,8 @@ kda_status kda_gated_norm(const kda_gated_norm_args *args, void *stream);
  *   weight, out    [D] of weight_dtype and bf16 [rows, D], contiguous; both
  *                  NULL: no norm before the next block.
  *   D              1 <= D <= 16384 (KDA_ERR_SHAPE otherwise).
- *   residual_scale, block_scale  finite; eps finite, >= 0 (KDA_ERR_SCALE).
+ *   residual_scale, block_scale  0, or normal numbers as fp32; eps finite, >= 0
+ *                  (KDA_ERR_SCALE).
  * rows = 0 does nothing.
  */
 typedef struct kda_residual_norm_args {

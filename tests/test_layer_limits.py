@@ -47,3 +47,14 @@ def test_scan_token_counts_that_would_leave_32_bits_are_refused(over):
         args = _lib.SsmArgs(T=T, **fields)
         assert lib.kda_ssm_fwd(args, None) == code, T
         assert (lib.kda_ssm_workspace_bytes(args) < 0) == (code == _lib.KDA_ERR_SIZE), T
+
+
+@pytest.mark.parametrize("scale,ok", [(0.0, True), (-0.0, True), (1.0, True), (-2.0 ** -126, True), (2.0 ** 127, True),
+                                      (2.0 ** 128, False), (-1e39, False), (1e300, False), (2.0 ** -127, False), (1e-300, False)])
+def test_residual_scales_are_numbers_of_fp32(scale, ok):
+    """Beyond fp32 a scale would be infinite (and times 0 NaN) or lose its digits."""
+    for name in ("residual_scale", "block_scale"):
+        fields = dict(rows=0, D=64, gate_period=1, x_stride=64, eps=1e-6, residual_scale=1.0, block_scale=1.0)
+        fields[name] = scale
+        status = _lib.load().kda_residual_norm(_lib.ResidualNormArgs(**fields), None)
+        assert status == (_lib.KDA_OK if ok else _lib.KDA_ERR_SCALE), name
