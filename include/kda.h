@@ -60,18 +60,26 @@ typedef enum kda_status {
                                   final_state partly overlaps initial_state */
     KDA_ERR_SIZE = 7,          /* B < 1, H < 1, H > 65536, T < 0 or
                                   T > 2^31-1, sizes overflow int64, or more
-                                  than 2^31-1 (sequence, head) chains */
-    KDA_ERR_SCALE = 8,         /* scale is not finite */
+                                  than 2^31-1 (sequence, head) chains; the
+                                  layer operators: also rows < 0, gate_period
+                                  < 1, a grid beyond 2^32 threads, or
+                                  kda_ssm_fwd's T >= 2^31 - 128 */
+    KDA_ERR_SCALE = 8,         /* scale is not finite; the layer operators: eps is
+                                  not finite or negative, or a scale is not 0
+                                  or a normal number of fp32 */
     KDA_ERR_LAUNCH = 9,        /* the HIP runtime rejected the launch */
-    KDA_ERR_WORKSPACE = 10,    /* kda_fwd_scan: workspace NULL, not 16-byte
-                                  aligned, smaller than
-                                  kda_fwd_scan_workspace_bytes(), or
+    KDA_ERR_WORKSPACE = 10,    /* kda_fwd_scan, kda_ssm_fwd: workspace NULL,
+                                  not 16-byte aligned, smaller than
+                                  kda_fwd_scan_workspace_bytes() or
+                                  kda_ssm_workspace_bytes(), or
                                   overlapping a tensor argument */
     KDA_ERR_ALIGNMENT = 11,    /* a non-NULL pointer is misaligned: q, k, v,
                                   g, out, initial_state and final_state need
                                   16 bytes, beta 2, A_log and dt_bias 4,
                                   cu_seqlens 8 (allocator memory and whole
-                                  token rows of it always are) */
+                                  token rows of it always are); the layer
+                                  operators' other inputs: their element's
+                                  size, residual_out 16 */
     KDA_ERR_OPTION = 12,       /* kda_options: an unknown value, a non-zero
                                   reserved field, or a kernel / inverse /
                                   sigmoid combination that no kernel of the

@@ -58,3 +58,15 @@ def test_residual_scales_are_numbers_of_fp32(scale, ok):
         fields[name] = scale
         status = _lib.load().kda_residual_norm(_lib.ResidualNormArgs(**fields), None)
         assert status == (_lib.KDA_OK if ok else _lib.KDA_ERR_SCALE), name
+
+
+@pytest.mark.parametrize("code,words", [
+    (_lib.KDA_ERR_STRIDE, ("negative", "int64", "2^27", "2^26")),
+    (_lib.KDA_ERR_SCALE, ("finite", "eps", ">= 0", "residual_scale", "block_scale")),
+    (_lib.KDA_ERR_SIZE, ("2^31", "2^31 - 128", "2^32 threads", "gate_period", "rows")),
+    (_lib.KDA_ERR_ALIGNMENT, ("16 bytes", "inputs 2", "inputs 4", "cu_seqlens 8", "residual_out")),
+])
+def test_messages_name_what_the_layer_operators_refuse(code, words):
+    """The text that a KdaArgumentError shows."""
+    text = _lib.status_string(code)
+    assert all(w in text for w in words), text
