@@ -20,7 +20,7 @@ bool add_ok(int64_t a, int64_t b, int64_t *r) { return !__builtin_add_overflow(a
 bool bf16_or_fp32(int32_t d) { return d == KDA_DTYPE_BF16 || d == KDA_DTYPE_FP32; }
 int64_t bytes_of(int32_t d) { return d == KDA_DTYPE_BF16 ? 2 : 4; }
 bool flag(int32_t v) { return v == 0 || v == 1; }
-bool norm_eps(double e) { return std::isfinite(e) && e >= 0.0; }
+bool valid_eps(double e) { return std::isfinite(e) && e >= 0.0; }
 // The kernels multiply in fp32: a scale has to be 0 or normal there.
 bool fp32_scale(double s) { return s == 0.0 || std::isnormal(static_cast<float>(s)); }
 
@@ -105,7 +105,7 @@ extern "C" kda_status kda_short_conv(const kda_conv_args *args, void *stream)
         (a.l2norm != 0 && a.l2norm != 64 && a.l2norm != 128 && a.l2norm != 256) ||
         (a.l2norm != 0 && a.D % a.l2norm != 0))
         return KDA_ERR_SHAPE;
-    if (a.l2norm != 0 && !norm_eps(a.l2norm_eps))
+    if (a.l2norm != 0 && !valid_eps(a.l2norm_eps))
         return KDA_ERR_SCALE;
     if (!bf16_or_fp32(a.weight_dtype))
         return KDA_ERR_DTYPE;
@@ -148,7 +148,7 @@ extern "C" kda_status kda_short_conv(const kda_conv_args *args, void *stream)
     p.D = a.D;
     p.act = a.activation;
     p.l2norm = static_cast<int>(a.l2norm);
-    p.l2eps = static_cast<float>(a.l2norm_eps);
+    p.l2eps = kda::layer::norm_eps(a.l2norm_eps);
     if (p.seqs.N == 0 || (tokens == 0 && !a.final_state))
         return KDA_OK;
     return launched(kda::layer::launch_conv(p, static_cast<int>(a.W), static_cast<hipStream_t>(stream)));
@@ -340,7 +340,7 @@ extern "C" kda_status kda_gated_norm(const kda_gated_norm_args *args, void *stre
         return KDA_ERR_OPTION;
     if (a.D < 1 || a.D > kMaxChannels || a.group < 1 || a.group > kda::layer::kMaxNormSize || a.D % a.group != 0)
         return KDA_ERR_SHAPE;
-    if (!norm_eps(a.eps))
+    if (!valid_eps(a.eps))
         return KDA_ERR_SCALE;
     if (!bf16_or_fp32(a.weight_dtype))
         return KDA_ERR_DTYPE;
@@ -371,7 +371,7 @@ extern "C" kda_status kda_gated_norm(const kda_gated_norm_args *args, void *stre
     p.group = a.group;
     p.act = a.activation;
     p.gate_first = a.gate_first;
-    p.eps = static_cast<float>(a.eps);
+    p.eps = kda::layer::norm_eps(a.eps);
     return launched(kda::layer::launch_gated_norm(p, static_cast<hipStream_t>(stream)));
 }
 
@@ -384,7 +384,7 @@ extern "C" kda_status kda_residual_norm(const kda_residual_norm_args *args, void
         return KDA_ERR_OPTION;
     if (a.D < 1 || a.D > kda::layer::kMaxNormSize)
         return KDA_ERR_SHAPE;
-    if (!norm_eps(a.eps) || !fp32_scale(a.residual_scale) || !fp32_scale(a.block_scale))
+    if (!valid_eps(a.eps) || !fp32_scale(a.residual_scale) || !fp32_scale(a.block_scale))
         return KDA_ERR_SCALE;
     if ((a.residual && !bf16_or_fp32(a.residual_dtype)) || (a.residual_out && !bf16_or_fp32(a.residual_out_dtype)) ||
         (a.post_weight && !bf16_or_fp32(a.post_weight_dtype)) || (a.gate && !bf16_or_fp32(a.gate_dtype)) ||
@@ -436,6 +436,6 @@ extern "C" kda_status kda_residual_norm(const kda_residual_norm_args *args, void
     p.D = a.D;
     p.residual_scale = static_cast<float>(a.residual_scale);
     p.block_scale = static_cast<float>(a.block_scale);
-    p.eps = static_cast<float>(a.eps);
+    p.eps = kda::layer::norm_eps(a.eps);
     return launched(kda::layer::launch_residual_norm(p, static_cast<hipStream_t>(stream)));
 }

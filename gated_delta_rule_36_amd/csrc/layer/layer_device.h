@@ -173,6 +173,15 @@ __device__ __forceinline__ float lane_sum(float x)
 
 __device__ __forceinline__ float silu_f32(float x) { return x * sigmoid_f32(x); }
 
+// Norms divide by the root of m, a sum or mean of squares and eps.  Where fp32
+// does not hold the squares (m infinite, or so small that some may be denormal,
+// which the reciprocal root takes for 0) the numbers are scaled by a power of two
+// and squared again: by 2^94 below m = 2^-80, so that 16384 squares stay under
+// 2^122 and that of the least number above 2^-124, else by 2^-80.
+__device__ __forceinline__ bool norm_in_range(float m) { return m >= 0x1p-80f && m < __builtin_inff(); }
+__device__ __forceinline__ float norm_shift(float m) { return m < 0x1p-80f ? 0x1p94f : 0x1p-80f; }
+__device__ __forceinline__ float shifted_eps(const NormEps &e, float m) { return m < 0x1p-80f ? e.up : e.down; }
+
 // log(1 + e^v) = max(v, 0) + log1p(u), u = e^-|v|, or v itself above `plain`:
 // 20, where the two agree in fp32, or below everything for steps that are not
 // to be transformed.  Most steps are far below 1, so u and its log1p have to be

@@ -56,6 +56,16 @@ inline SlabMap slab_map(const Seqs &s, int64_t len)
 // hipErrorInvalidConfiguration.
 inline bool grid_fits(int64_t blocks, int threads) { return blocks <= UINT32_MAX / threads; }
 
+// A norm's eps, and times 2^188 and 2^-160 for rows whose squares fp32 does not
+// hold (see norm_shift in layer_device.h).
+struct NormEps {
+    float plain, up, down;
+};
+inline NormEps norm_eps(double eps)
+{
+    return {static_cast<float>(eps), static_cast<float>(eps * 0x1p188), static_cast<float>(eps * 0x1p-160)};
+}
+
 struct ConvParams {
     const uint16_t *x;
     int64_t xb, xt;  // element strides of batch row and token
@@ -68,7 +78,7 @@ struct ConvParams {
     Seqs seqs;
     int64_t D;
     int act, l2norm;
-    float l2eps;
+    NormEps l2eps;
 };
 hipError_t launch_conv(const ConvParams &p, int W, hipStream_t stream);
 
@@ -80,7 +90,7 @@ struct GatedParams {
     uint16_t *out;
     int64_t rows, D, group;
     int act, gate_first;
-    float eps;
+    NormEps eps;
 };
 hipError_t launch_gated_norm(const GatedParams &p, hipStream_t stream);
 
@@ -97,7 +107,8 @@ struct ResidParams {
     int64_t gr, gate_period;
     uint16_t *out;  // or nullptr
     int64_t rows, D;
-    float residual_scale, block_scale, eps;
+    float residual_scale, block_scale;
+    NormEps eps;
 };
 hipError_t launch_residual_norm(const ResidParams &p, hipStream_t stream);
 

@@ -75,9 +75,30 @@ __device__ __forceinline__ float row_sum(float x, float *part, int threads)
     }
 }
 
-__device__ __forceinline__ float inv_rms(float ss, float n, float eps)
+// 1 / sqrt(mean v^2 + eps) over a row of n elements, of which ss is the thread's
+// sum of squares; for a row whose squares fp32 does not hold v comes back scaled
+// and what is returned with it.
+template <int TPR, int K>
+__device__ __forceinline__ float inv_rms(float (&v)[K][8], float ss, float *part, int threads, float n, const NormEps &eps)
 {
-    return __builtin_amdgcn_rsqf(ss / n + eps);
+    float m = row_sum<TPR>(ss, part, threads) / n + eps.plain;
+    const bool held = norm_in_range(m);
+    // a wave's rows together, or the workgroup's one, whose threads all have m
+    if (TPR != kWaves ? __any(!held) : !held) {
+        const float f = held ? 1.0f : norm_shift(m), e = held ? eps.plain : shifted_eps(eps, m);
+        ss = 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[k][i] *= f;
+                ss = fmaf(v[k][i], v[k][i], ss);
+            }
+        if constexpr (TPR == kWaves)
+            __syncthreads();  // the first sum has been read
+        m = row_sum<TPR>(ss, part, threads) / n + e;
+    }
+    return __builtin_amdgcn_rsqf(m);
 }
 
 // FULL: the row fills its lanes' vectors.
@@ -123,7 +144,7 @@ __global__ __launch_bounds__(kThreads<TPR>) void gated_norm_kernel(GatedParams p
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss = fmaf(v[k][e], v[k][e], ss);
     }
-    const float s = inv_rms(row_sum<TPR>(ss, part, threads), static_cast<float>(p.group), p.eps);
+    const float s = inv_rms<TPR>(v, ss, part, threads, static_cast<float>(p.group), p.eps);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const Eight ch = part_of(k);
@@ -177,7 +198,7 @@ __global__ __launch_bounds__(kThreads<TPR>) void residual_norm_kernel(ResidParam
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int e = 0; e < 8; ++e) ss = fmaf(v[k][e], v[k][e], ss);
-        const float s = inv_rms(row_sum<TPR>(ss, part[0], threads), static_cast<float>(p.D), p.eps);
+        const float s = inv_rms<TPR>(v, ss, part[0], threads, static_cast<float>(p.D), p.eps);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             float w[8];
@@ -210,7 +231,7 @@ __global__ __launch_bounds__(kThreads<TPR>) void residual_norm_kernel(ResidParam
     }
     if (!p.out)
         return;
-    const float s = inv_rms(row_sum<TPR>(ss, part[1], threads), static_cast<float>(p.D), p.eps);
+    const float s = inv_rms<TPR>(r, ss, part[1], threads, static_cast<float>(p.D), p.eps);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const Eight ch = part_of(k);

@@ -128,8 +128,22 @@ __global__ __launch_bounds__(64 * kWaves) void conv_kernel(ConvParams p, uint32_
                 float ss = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-                ss = p.l2norm == 64 ? lane_sum<8>(ss) : p.l2norm == 128 ? lane_sum<16>(ss) : lane_sum<32>(ss);
-                const float r = __builtin_amdgcn_rsqf(ss + p.l2eps);
+                const auto group_sum = [&](float v) {
+                    return p.l2norm == 64 ? lane_sum<8>(v) : p.l2norm == 128 ? lane_sum<16>(v) : lane_sum<32>(v);
+                };
+                ss = group_sum(ss);
+                float m = ss + p.l2eps.plain;
+                if (__any(!norm_in_range(m))) {  // the wave together: the sum below is over lanes
+                    const float f = norm_in_range(m) ? 1.0f : norm_shift(m), eps = norm_in_range(m) ? p.l2eps.plain : shifted_eps(p.l2eps, m);
+                    ss = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        y[e] *= f;
+                        ss = fmaf(y[e], y[e], ss);
+                    }
+                    m = group_sum(ss) + eps;
+                }
+                const float r = __builtin_amdgcn_rsqf(m);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[e] *= r;
             }

@@ -324,7 +324,9 @@ const char *kda_fwd_kernel(int64_t T, int varlen, const kda_options *options);
  * may be slices of wider rows, given by element strides of the batch row and
  * of the token (>= 0) with the channels of a token adjacent.  Token tensors
  * need no alignment beyond their element's; out and the states 16 bytes.
- * Outputs must not overlap inputs, except where it is said.  Sizes whose grid
+ * Outputs must not overlap inputs, except where it is said.  Norms hold for
+ * rows of any size, also where fp32 does not hold their squares, and for any eps
+ * >= 0 (with 0, a row of zeros is NaN).  Sizes whose grid
  * would pass 2^32 threads are KDA_ERR_SIZE (the norms take any number of rows).
  * ---------------------------------------------------------------------- */
 
