@@ -664,7 +664,7 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
 #pragma unroll 1
                 for (int c = 0; c < 32; ++c) {
                     uint16_t *x = &sh.x[t][wave * 32 + c];
-                    const bool out = !(fabsf(w * bf16_to_f32(*x)) < __builtin_inff());
+                    const bool out = !(fabsf(w * bf16_to_f32(*x)) < 0x1.ffp127f);  // as bf16 infinite from there on
                     if (out)
                         *x = 0;
                     const uint64_t tokens_out = __ballot(out);

@@ -5,7 +5,7 @@ import torch
 
 import layer_ref as ref
 from gated_delta_rule_36_amd import _lib
-from test_layer_gpu import BF16, F32, check, on_gpu, scan, ssm_case, ssm_inputs
+from test_layer_gpu import BF16, F32, check, normal, on_gpu, scan, ssm_case, ssm_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -298,3 +298,26 @@ def test_scan_decay_of_a_head_over_two_workgroups_has_one_writer():
         logs = work[4 * slabs * H * P * N:][:4 * H].view(torch.float32).cpu()
         assert bool((logs[:3] < -300).all()) and bool((logs[:3] > -420).all()), logs   # of 600 in all
         assert -1.0 < float(logs[3]) < 0.0
+
+
+@pytest.mark.parametrize("N", [64, 128, 256])
+@pytest.mark.parametrize("step", [1.0015, 1.0025, 1.0039, 1.5])
+def test_scan_products_next_to_fp32s_largest_never_reach_earlier_tokens(N, step):
+    """x = bf16's lowest number times a step just above 1: between bf16's largest number and fp32's, or beyond."""
+    T, H, P = 90, 1, 32
+    a, g = still(T, H, P, N), torch.Generator().manual_seed(N)
+    a["b"], a["c"] = normal(g, 1, T, 1, N), normal(g, 1, T, 1, N)
+    a["x"], a["initial"] = normal(g, 1, T, H, P), torch.randn(1, H, P, N, generator=g)
+    a["dt_bias"] = torch.full((H,), step)
+    for s in (1, 31, 40, 63, 64, 85):
+        outs = []
+        for value in (1.0, LOWEST):
+            a["x"][0, s, 0, 5] = value
+            d = {k: on_gpu(u) for k, u in a.items()}
+            out, fin = torch.empty(1, T, H, P, dtype=BF16, device="cuda"), torch.empty(1, H, P, N, device="cuda")
+            scan(d, out, fin, dt_softplus=False)
+            outs.append(out.cpu())
+        a["x"][0, s, 0, 5] = 1.0
+        touched = torch.zeros(out.shape, dtype=torch.bool)
+        touched[:, s:, 0, 5] = True
+        assert torch.equal(outs[0][~touched], outs[1][~touched]), s
