@@ -190,13 +190,20 @@ struct SsmPlan {
 // Calls without cu_seqlens of up to kSsmRecurrentMaxTokens tokens: the token
 // recurrence.  The others: as many segments as give every compute unit of 256
 // one workgroup and no more (one fits a unit, and a second round costs as much
-// as the first: 4 rows of 4096 tokens, 32 heads of 64 x 128, take 138 us in 8
-// segments a row, 169 in 16, 208 in 4 and 594 whole), of whole tiles of the
-// kernel (2048 tokens of 8 heads take 37 us in segments of one tile, 43 of two,
-// 63 of four).  A batch is cut into equal parts; of packed sequences, whose
-// lengths are not known here, each is taken to end half a segment early (a
-// segment more than there is room for starts when a short one ends: 8 sequences
-// of 19595 tokens in 31 to 33 segments of 704 take 184 us, in fewer of 768 190).
+// as the first: 4 rows of 4096 tokens, 32 heads of 64 x 128, take 139 us in 8
+// segments a row, 170 in 16, 210 in 4 and 585 whole), of whole tiles of the
+// kernel (2048 tokens of 8 heads take 37 us in segments of one tile, 45 of two,
+// 63 of four).  A batch is cut into equal parts.
+// The lengths of packed sequences are not known here: each is taken to end half a
+// segment early, and half the segments are kept however many sequences there
+// are, for one of them may be long.  Of five random sets of lengths each, 32
+// heads of 64 x 128, us by this rule (in segments of 256 / 768 / 2048 tokens):
+//   2 sequences of 8192 tokens in all   95 - 98 (100 - 129 / 159 - 162 / 368 - 390)
+//   8 of 19595                          175 - 184 (220 - 230 / 182 - 187 / 388 - 405)
+//   32 of 16384                         145 - 166 (194 - 205 / 178 - 222 / 137 - 166)
+//   128 of 16384                        207 - 224 (223 - 231 / 209 - 220 / 210 - 220)
+// It loses where short ends add up to a segment more than there is room for: 8 of
+// 19595 tokens in 33 segments take 271 us, and would 182 in those of 768.
 // False if the workspace overflows.
 bool ssm_plan(const kda_ssm_args &a, const Seqs &s, SsmPlan *plan)
 {

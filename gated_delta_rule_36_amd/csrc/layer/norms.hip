@@ -18,9 +18,9 @@
 // 15.6 with five, 18.2 with eight).  Sums and the values between
 // the two norms are fp32; the second norm takes the unrounded r.
 //
-// Measured: gated_norm over 4,194,304 rows of 128, 525 us, 6.1 TB/s;
+// Measured: gated_norm over 4,194,304 rows of 128, 516 us, 6.2 TB/s;
 // residual_norm over 32768 rows of 4096 with an fp32 stream, post norm and
-// gate, 278 us, 5.8 TB/s (512 threads a row; 294 us with 256 of two vectors
+// gate, 280 us, 5.8 TB/s (512 threads a row; 294 us with 256 of two vectors
 // each), where a 1 GiB copy reaches 5.1 TB/s.  Asking for more waves a SIMD (8,
 // by a register limit) lost 2 to 3 %.
 #include "layer_device.h"

@@ -16,9 +16,13 @@
 // may be one buffer.
 //
 // Tiles are 16 tokens long (one row in six read twice, from the caches), or 8
-// where longer ones would leave fewer than kFew waves: measured against 32 on
-// packed prompts of 19595 tokens and 4096 channels, 70 us with 16, 71 with 8, 73
-// with 32; on 4097 tokens of 1283 channels 14 us with 8 and 33 with 32.
+// where longer ones would leave fewer than kFew waves: packed prompts of 19595
+// tokens and 4096 channels take 70.5 us with 16, 72.6 with 8 and 80 with 32; 4097
+// tokens of 1283 channels 9.0 us with 8, 11.3 with 16 and 18.3 with 32.
+//
+// One token of 64 rows of 12288 channels takes 8.1 us where memory would take 2.5:
+// state, input and weights are asked for one after the other, and four rows are
+// computed for the one.
 #include "layer_device.h"
 
 namespace kda {

@@ -32,20 +32,18 @@
 // waves).  b, c and x go through registers into LDS, the next tile's loads in
 // flight while this one is computed.  x is read from memory once per pass.
 //
-// What bounds it is the issue of instructions.  A wave's tile (P = 64, N = 128)
-// takes some 95 matrix instructions of 32 cycles and more vector cycles than
-// that, most of them to round S, the weighted x and c b^T into their parts; two
-// waves a SIMD (the state takes 64 registers, a tile in flight 32) overlap them
-// only in part, and all eight wait together while a tile's loads are issued.
-// 8 x 16384 tokens of 32 heads, 1.7 GB to move: 790 to 880 us, of which the own
-// states take 180 and joining them 12; without loads and stores the output
-// pass would take 430.  19595 tokens in 8 sequences 155 to 175 us; one of 8192 tokens
-// with 16 heads of 128 x 64 56 us.  Asking for the next tile before c b^T is
-// formed gained 5 % over asking after it, the priorities below 4 %.  Measured
-// and not better: waves of 16 columns (16 of them), waves of 64, two workgroups
+// What bounds it is vector instructions, and what two waves a SIMD leave
+// uncovered (the state takes 64 registers, a tile in flight 32).  A wave's tile
+// (P = 64, N = 128) takes 102 matrix instructions and 1519 vector ones, most of
+// them to round S, the weighted x and c b^T into their parts; they fill 26 and 53 %
+// of a SIMD's cycles.  8 x 16384 tokens of 32 heads, 1.7 GB to move: 900 to 960 us,
+// of which the own states take 204 to 225 and joining them 12.  19595 tokens in 8
+// sequences 176 to 198 us; one of 8192 tokens with 16 heads of 128 x 64 60 us.
+// Asking for the next tile before c b^T is formed gained 5 % over asking after
+// it, the priorities below 4 %.  Measured and not better: waves of 16 columns (16 of them), waves of 64, two workgroups
 // of four waves a compute unit, loads spread over the tile, z and out through
 // LDS or exchanged between lanes into whole 64-byte rows, more and shorter
-// segments for the own states (220 us in twice as many), the workgroups of a
+// segments for the own states (13 % slower in twice as many), the workgroups of a
 // segment on one L2, stores held back until the next tile has arrived (3 to 5 %
 // slower), non-temporal z (10 % slower) and out (3 %).
 //
@@ -67,7 +65,10 @@
 // M enter as two bf16 parts (the value rounded, and the rest rounded: good to
 // 2^-17 of itself; out is rounded to 2^-8); the weighted x enters the state as
 // three, which hold it whole, at any decay: what a decay leaves of a block is
-// all there is of the state where later tokens bring nothing.
+// all there is of the state where later tokens bring nothing.  (Two for blocks
+// that decay by more than 2^-4 were 4 to 8 % faster and left 2^-17.)  Of the
+// parts' products with c b^T the last times the last, 2^-18 of the whole, is
+// left out.
 #include "layer_device.h"
 
 namespace kda {
@@ -82,7 +83,7 @@ constexpr int CH = static_cast<int>(kSsmChunk);  // tokens a block
 constexpr int TM = 2 * CH;                       // tokens a tile
 constexpr int NW = static_cast<int>(kSsmWaves);  // waves, units a workgroup
 // Log decay from which on a tile is steep.  The gentle way is 12 % faster on
-// 4 x 8192 tokens that hardly decay (268 against 300 us); from -80 on it is as fast,
+// 4 x 8192 tokens that hardly decay (250 against 283 us); from -80 on it is as fast,
 // with less room for small values of S.
 constexpr float kSteep = -40.0f;
 // Log decay from a block to the segment's end below which nothing earlier is

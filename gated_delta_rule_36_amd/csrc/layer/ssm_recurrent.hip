@@ -13,7 +13,7 @@
 // With several tokens it is the latency of their inputs that counts, not their
 // bytes: a token's are asked for while the one before is computed, and each
 // lane finishes one row.  64 rows, 32 heads of 64 x 128, fp32 states: one token
-// 23 us (5.9 TB/s), 8 tokens 40 us; with inputs loaded where they are used, one
+// 22 us (5.9 TB/s), 8 tokens 41 us; with inputs loaded where they are used, one
 // element at a time, and one lane finishing all rows, 25 and 56 us.
 #include "layer_device.h"
 

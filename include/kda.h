@@ -314,8 +314,8 @@ const char *kda_status_string(kda_status status);
 const char *kda_fwd_kernel(int64_t T, int varlen, const kda_options *options);
 
 /* -------------------------------------------------------------------------
- * The layer operators: what surrounds a recurrent mixer in a model, and the
- * scalar-decay recurrence that hybrid models alternate with KDA.  The rules
+ * The layer operators: what surrounds a recurrent mixer in a layer, and KDA's
+ * sibling with one decay per head, which takes the same states.  The rules
  * above hold for them too: device pointers on the current device, nothing
  * allocated, every check on the host before anything is enqueued, no state
  * between calls, asynchronous on `stream`.  Activations are bf16 with
