@@ -133,12 +133,12 @@ struct SsmParams {
 constexpr int64_t kSsmChunk = 32;
 // Calls without cu_seqlens of at most this many tokens take the token
 // recurrence.  32 heads of 64 x 128, in us, by it (by the chunked kernel): 64 rows
-// of 8 tokens 41 (47), of 12 52 (47), of 16 63 (47); 8 rows of 8 11 (20), of 16 16
-// (20); one row of 8 9 (18), of 16 14 (19).  64 heads of 64 x 64: 64 rows of 8 43
-// (57), of 12 58 (57); 8 rows of 12 13 (15), of 16 17 (15).  So up to 8 it is the
-// faster one for every batch, and above that for small ones only, by 9 us at most;
-// the limit goes by tokens alone, so that a row's roundings do not depend on how
-// many others the call has.
+// of 8 tokens 41 (47), of 9 43 (47), of 12 52 (47), of 16 63 (47); 8 rows of 8 11
+// (20), of 16 16 (20); one row of 8 9 (18), of 16 14 (19).  64 heads of 64 x 64: 64
+// rows of 8 43 (57), of 9 47 (58), of 12 58 (57); 8 rows of 12 13 (15), of 16 17
+// (15).  So at 8 it is the faster one for every batch measured; between 9 and 16
+// that depends on the batch, and the limit goes by tokens alone, so that a row's
+// roundings do not depend on how many others the call has.
 constexpr int64_t kSsmRecurrentMaxTokens = 8;
 
 hipError_t launch_ssm_recurrent(const SsmParams &p, hipStream_t stream);
