@@ -40,12 +40,12 @@
 // of which the own states take 204 to 225 and joining them 12.  19595 tokens in 8
 // sequences 176 to 198 us; one of 8192 tokens with 16 heads of 128 x 64 60 us.
 // Asking for the next tile before c b^T is formed gained 5 % over asking after
-// it, the priorities below 4 %.  Measured and not better: waves of 16 columns (16 of them), waves of 64, two workgroups
-// of four waves a compute unit, loads spread over the tile, z and out through
-// LDS or exchanged between lanes into whole 64-byte rows, more and shorter
-// segments for the own states (13 % slower in twice as many), the workgroups of a
-// segment on one L2, stores held back until the next tile has arrived (3 to 5 %
-// slower), non-temporal z (10 % slower) and out (3 %).
+// it, the priorities below 4 %.  Measured and not better: waves of 16 columns (16
+// of them), waves of 64, two workgroups of four waves a compute unit, loads spread
+// over the tile, z and out through LDS or exchanged between lanes into whole
+// 64-byte rows, more and shorter segments for the own states (13 % slower in twice
+// as many), the workgroups of a segment on one L2, stores held back until the next
+// tile has arrived (3 to 5 % slower), non-temporal z (10 % slower) and out (3 %).
 //
 // Operands.  v_mfma_f32_32x32x16_bf16 contracts 16 slots; lane (l32, half)
 // holds slots 8 half .. 8 half + 7 of row / column l32, and accumulator
@@ -90,7 +90,7 @@ constexpr float kSteep = -40.0f;
 // left in fp32: what is finite there is 0 times 2^-300, also where negative
 // steps (without softplus) let it grow before.
 constexpr float kNothing = -300.0f;
-// Weights from 2^32 on and x from 2^96 on are looked at one by one (see scrub):
+// Weights from 2^32 on and x from 2^64 on are looked at one by one (see scrub):
 // below, their product is finite.
 constexpr float kLargeWeight = 0x1p32f;
 template <int V>
@@ -532,12 +532,12 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_chunk_kernel(SsmParams p, int
 #pragma unroll
             for (int k = 0; k < kLoadX; ++k) put(&sh.x[wx0 + ln / PX + k * SX][ln % PX * 8], rx[k]);
             if constexpr (OUT) {
-                // not finite once an x is not, or is 2^96 or more
+                // squares: not finite once an x is not, or is 2^64 or more
                 float sum = 0.0f;
 #pragma unroll
                 for (int k = 0; k < kLoadX; ++k)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sum = dot2_bf16(rx[k][i], 0x4f804f80u, sum);  // times 2^32
+                    for (int i = 0; i < 4; ++i) sum = dot2_bf16(rx[k][i], rx[k][i], sum);
                 const bool odd = __any(!(fabsf(sum) < __builtin_inff()));
                 if (ln == 0)
                     sh.odd_x[wave] = odd;

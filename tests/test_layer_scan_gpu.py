@@ -321,3 +321,25 @@ def test_scan_products_next_to_fp32s_largest_never_reach_earlier_tokens(N, step)
         touched = torch.zeros(out.shape, dtype=torch.bool)
         touched[:, s:, 0, 5] = True
         assert torch.equal(outs[0][~touched], outs[1][~touched]), s
+
+
+@pytest.mark.parametrize("N", [64, 128, 256])
+def test_scan_large_numbers_of_both_signs_never_reach_earlier_tokens(N):
+    """Neighbours of opposite sign in one load: what is looked for must not cancel."""
+    T, H, P = 90, 2, 32
+    a, g = still(T, H, P, N), torch.Generator().manual_seed(N)
+    a["b"], a["c"], a["x"] = normal(g, 1, T, 1, N), normal(g, 1, T, 1, N), normal(g, 1, T, H, P)
+    a["dt_bias"] = torch.full((H,), 1.5)
+    for s, pairs in ((31, [(4, 5)]), (40, [(4, 5), (6, 7)]), (63, [(4, 6)]), (85, [(5, 6), (9, 24)])):
+        outs, kept = [], a["x"].clone()
+        for sign in (None, 1.0, -1.0):
+            a["x"] = kept.clone()
+            for i, j in pairs if sign else ():
+                a["x"][0, s, 0, i], a["x"][0, s, 0, j] = sign * LOWEST, -sign * LOWEST
+            d = {k: on_gpu(u) for k, u in a.items()}
+            out, fin = torch.empty(1, T, H, P, dtype=BF16, device="cuda"), torch.empty(1, H, P, N, device="cuda")
+            scan(d, out, fin, dt_softplus=False)
+            outs.append(out.cpu())
+        a["x"] = kept
+        for out in outs[1:]:
+            assert torch.equal(outs[0][:, :s], out[:, :s]) and torch.equal(outs[0][:, :, 1], out[:, :, 1]), s
