@@ -11,9 +11,10 @@ LIBRARY = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
 EXPORTS = ("kda_fwd", "kda_fwd_ex", "kda_fwd_scan", "kda_fwd_scan_static",
            "kda_fwd_scan_workspace_bytes", "kda_status_string", "kda_fwd_kernel",
            "kda_abi_version", "kda_short_conv", "kda_ssm_fwd", "kda_ssm_workspace_bytes",
-           "kda_gated_norm", "kda_residual_norm")
+           "kda_gated_norm", "kda_residual_norm", "kda_delta_fwd", "kda_qk_norm_rotary", "kda_append_kv",
+           "kda_paged_attention", "kda_paged_attention_workspace_bytes")
 SCAN_STATIC_BYTES = 32 << 20  # KDA_SCAN_STATIC_BYTES
-ABI_VERSION = 5
+ABI_VERSION = 6
 
 # kda_status codes (include/kda.h)
 KDA_OK = 0
@@ -95,6 +96,44 @@ class ResidualNormArgs(ctypes.Structure):
                 + _fields(_F64, "residual_scale block_scale eps"))
 
 
+class DeltaArgs(ctypes.Structure):
+    """struct kda_delta_args"""
+    _fields_ = (_fields(_P, "q k v g beta out")
+                + _fields(_I64, "q_stride_b q_stride_t k_stride_b k_stride_t v_stride_b v_stride_t "
+                                "g_stride_b g_stride_t beta_stride_b beta_stride_t")
+                + _fields(_P, "A_log dt_bias initial_state final_state cu_seqlens")
+                + _fields(_I64, "num_seqs B T H G K V")
+                + _fields(_I32, "initial_state_dtype final_state_dtype") + _fields(_I64, "reserved")
+                + _fields(_F64, "scale"))
+
+
+class RotaryArgs(ctypes.Structure):
+    """struct kda_rotary_args"""
+    _fields_ = (_fields(_P, "q k q_out k_out") + _fields(_I64, "q_stride_b q_stride_t k_stride_b k_stride_t")
+                + _fields(_P, "positions inv_freq q_weight k_weight") + _fields(_I64, "B T Hq Hk D R")
+                + _fields(_I32, "q_weight_dtype k_weight_dtype interleaved reserved")
+                + _fields(_F64, "eps rotary_scale"))
+
+
+class AppendArgs(ctypes.Structure):
+    """struct kda_append_args"""
+    _fields_ = (_fields(_P, "k v k_cache v_cache") + _fields(_I64, "k_stride_b k_stride_t v_stride_b v_stride_t "
+                "k_cache_stride_page k_cache_stride_token k_cache_stride_head "
+                "v_cache_stride_page v_cache_stride_token v_cache_stride_head")
+                + _fields(_P, "slots positions inv_freq weight") + _fields(_I64, "B T Hk D R pages page_size")
+                + _fields(_I32, "weight_dtype interleaved") + _fields(_I64, "reserved")
+                + _fields(_F64, "eps rotary_scale"))
+
+
+class AttentionArgs(ctypes.Structure):
+    """struct kda_attention_args"""
+    _fields_ = (_fields(_P, "q k_cache v_cache block_table lengths out lse")
+                + _fields(_I64, "q_stride table_stride k_cache_stride_page k_cache_stride_token k_cache_stride_head "
+                                "v_cache_stride_page v_cache_stride_token v_cache_stride_head "
+                                "N Hq Hk D pages page_size table_width window reserved")
+                + _fields(_F64, "scale") + _fields(_P, "workspace") + _fields(_I64, "workspace_bytes"))
+
+
 class KdaLibraryMissing(RuntimeError):
     """libkda.so has not been built (there is no other implementation)."""
 
@@ -147,13 +186,16 @@ def load() -> ctypes.CDLL:
     lib.kda_fwd_kernel.argtypes = [i64, ctypes.c_int, opt]
     lib.kda_fwd_kernel.restype = ctypes.c_char_p
     for name, args in (("kda_short_conv", ConvArgs), ("kda_ssm_fwd", SsmArgs),
-                       ("kda_gated_norm", GatedNormArgs), ("kda_residual_norm", ResidualNormArgs)):
+                       ("kda_gated_norm", GatedNormArgs), ("kda_residual_norm", ResidualNormArgs),
+                       ("kda_delta_fwd", DeltaArgs), ("kda_qk_norm_rotary", RotaryArgs),
+                       ("kda_append_kv", AppendArgs), ("kda_paged_attention", AttentionArgs)):
         getattr(lib, name).argtypes = [ctypes.POINTER(args), p]
         getattr(lib, name).restype = ctypes.c_int
         LAYER[name] = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p, p)((name, lib)), packer(args)
-    lib.kda_ssm_workspace_bytes.argtypes = [ctypes.POINTER(SsmArgs)]
-    lib.kda_ssm_workspace_bytes.restype = i64
-    LAYER["kda_ssm_workspace_bytes"] = ctypes.CFUNCTYPE(i64, ctypes.c_char_p)(("kda_ssm_workspace_bytes", lib)), packer(SsmArgs)
+    for name, args in (("kda_ssm_workspace_bytes", SsmArgs), ("kda_paged_attention_workspace_bytes", AttentionArgs)):
+        getattr(lib, name).argtypes = [ctypes.POINTER(args)]
+        getattr(lib, name).restype = i64
+        LAYER[name] = ctypes.CFUNCTYPE(i64, ctypes.c_char_p)((name, lib)), packer(args)
     _lib = lib
     return lib
 

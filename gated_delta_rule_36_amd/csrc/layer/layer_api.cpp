@@ -1,96 +1,15 @@
 // C-ABI front end of the layer operators: argument checks on the host, then
 // the hand-off to the kernels.  Nothing here touches device memory.
 #include <algorithm>
-#include <cmath>
 #include <cstdint>
-#include <initializer_list>
 
-#include "kda.h"
-#include "layer_internal.h"
+#include "layer_checks.h"
 
 namespace {
 
-using kda::layer::Seqs;
+using namespace kda::layer;
 
 constexpr int64_t kMaxChannels = int64_t(1) << 24;
-
-bool mul_ok(int64_t a, int64_t b, int64_t *r) { return !__builtin_mul_overflow(a, b, r); }
-bool add_ok(int64_t a, int64_t b, int64_t *r) { return !__builtin_add_overflow(a, b, r); }
-
-bool bf16_or_fp32(int32_t d) { return d == KDA_DTYPE_BF16 || d == KDA_DTYPE_FP32; }
-int64_t bytes_of(int32_t d) { return d == KDA_DTYPE_BF16 ? 2 : 4; }
-bool flag(int32_t v) { return v == 0 || v == 1; }
-bool valid_eps(double e) { return std::isfinite(e) && e >= 0.0; }
-// The kernels multiply in fp32: a scale has to be 0 or normal there.
-bool fp32_scale(double s) { return s == 0.0 || std::isnormal(static_cast<float>(s)); }
-
-// Byte range of a buffer.
-struct Span {
-    uintptr_t lo = 0, hi = 0;
-    bool overlaps(const Span &o) const { return lo < o.hi && o.lo < hi; }
-};
-Span span(const void *p, int64_t bytes)
-{
-    Span s;
-    if (p && bytes > 0) {
-        s.lo = reinterpret_cast<uintptr_t>(p);
-        s.hi = s.lo + static_cast<uintptr_t>(bytes);
-    }
-    return s;
-}
-bool any_overlap(const Span &out, std::initializer_list<Span> inputs)
-{
-    for (const Span &s : inputs)
-        if (out.overlaps(s))
-            return true;
-    return false;
-}
-
-bool misaligned(const void *p, uintptr_t a) { return p != nullptr && reinterpret_cast<uintptr_t>(p) % a != 0; }
-
-// Bytes from the first to past the last element of `outer` x `inner` rows of
-// `width` adjacent elements with the given strides; false on a negative
-// stride or overflow.
-bool extent(int64_t outer, int64_t stride_o, int64_t inner, int64_t stride_i, int64_t width, int64_t elem,
-            int64_t *bytes)
-{
-    int64_t a = 0, b = 0, n = 0;
-    if (stride_o < 0 || stride_i < 0)
-        return false;
-    if (outer == 0 || inner == 0 || width == 0) {
-        *bytes = 0;
-        return true;
-    }
-    return mul_ok(outer - 1, stride_o, &a) && mul_ok(inner - 1, stride_i, &b) && add_ok(a, b, &n) &&
-           add_ok(n, width, &n) && mul_ok(n, elem, bytes);
-}
-
-// The batch of sequences a call names: KDA_OK, or what is wrong with it.
-kda_status check_seqs(const int64_t *cu, int64_t num_seqs, int64_t B, int64_t T, Seqs *s)
-{
-    if (B < 1 || T < 0 || T > INT32_MAX)
-        return KDA_ERR_SIZE;
-    if (cu && (B != 1 || num_seqs < 0))
-        return KDA_ERR_VARLEN_BATCH;
-    s->cu = cu;
-    s->N = cu ? num_seqs : B;
-    s->T = T;
-    return s->N > INT32_MAX ? KDA_ERR_SIZE : KDA_OK;
-}
-
-kda_status check_states(const void *init, int32_t init_dtype, const void *fin, int32_t fin_dtype)
-{
-    if (init && !bf16_or_fp32(init_dtype))
-        return init_dtype == KDA_DTYPE_NONE ? KDA_ERR_NULL_POINTER : KDA_ERR_STATE_DTYPE;
-    if (fin && !bf16_or_fp32(fin_dtype))
-        return fin_dtype == KDA_DTYPE_NONE ? KDA_ERR_NULL_POINTER : KDA_ERR_STATE_DTYPE;
-    return init && fin && init_dtype != fin_dtype ? KDA_ERR_STATE_DTYPE : KDA_OK;
-}
-
-kda_status launched(hipError_t e)
-{
-    return e == hipSuccess ? KDA_OK : e == hipErrorInvalidConfiguration ? KDA_ERR_SIZE : KDA_ERR_LAUNCH;
-}
 
 }  // namespace
 
@@ -335,6 +254,90 @@ extern "C" kda_status kda_ssm_fwd(const kda_ssm_args *args, void *stream)
         p.logs = p.slabs + plan.map.slabs * plan.slab;
     }
     return launched(kda::layer::launch_ssm_chunk(p, static_cast<hipStream_t>(stream)));
+}
+
+extern "C" kda_status kda_delta_fwd(const kda_delta_args *args, void *stream)
+{
+    if (!args)
+        return KDA_ERR_NULL_POINTER;
+    const kda_delta_args &a = *args;
+    if (a.reserved != 0)
+        return KDA_ERR_OPTION;
+    if ((a.K != 64 && a.K != 128 && a.K != 256) || a.V < 16 || a.V > kDeltaMaxV || a.V % 16 != 0)
+        return KDA_ERR_SHAPE;
+    if (a.H < 1 || a.H > 65536 || a.T > kDeltaMaxTokens)
+        return KDA_ERR_SIZE;
+    if (a.G < 1 || a.H % a.G != 0)
+        return KDA_ERR_SHAPE;
+    if (!std::isfinite(a.scale) || !fp32_scale(a.scale))
+        return KDA_ERR_SCALE;
+    DeltaParams p = {};
+    kda_status st = check_seqs(a.cu_seqlens, a.num_seqs, a.B, a.T, &p.seqs);
+    if (st == KDA_OK)
+        st = check_states(a.initial_state, a.initial_state_dtype, a.final_state, a.final_state_dtype);
+    if (st != KDA_OK)
+        return st;
+    int64_t tokens, n;
+    if (!mul_ok(a.B, a.T, &tokens) || !mul_ok(tokens, a.H * a.V * 2, &n) ||
+        !mul_ok(p.seqs.N, a.H * a.K * a.V * 4, &n) || p.seqs.N * a.H > INT32_MAX)
+        return KDA_ERR_SIZE;
+    const int64_t state = p.seqs.N * a.H * a.K * a.V;
+    int64_t nq, nk, nv, ng, nb;
+    if (!extent(a.B, a.q_stride_b, a.T, a.q_stride_t, a.G * a.K, 2, &nq) ||
+        !extent(a.B, a.k_stride_b, a.T, a.k_stride_t, a.G * a.K, 2, &nk) ||
+        !extent(a.B, a.v_stride_b, a.T, a.v_stride_t, a.H * a.V, 2, &nv) ||
+        !extent(a.B, a.g_stride_b, a.T, a.g_stride_t, a.H, 2, &ng) ||
+        !extent(a.B, a.beta_stride_b, a.T, a.beta_stride_t, a.H, 2, &nb))
+        return KDA_ERR_STRIDE;
+    const bool recurrent = !a.cu_seqlens && a.T <= kDeltaRecurrentMaxTokens;
+    if (!recurrent && a.T > 1 &&
+        (a.q_stride_t > kDeltaMaxStride || a.k_stride_t > kDeltaMaxStride || a.v_stride_t > kDeltaMaxStride ||
+         a.g_stride_t > kDeltaMaxStride || a.beta_stride_t > kDeltaMaxStride))
+        return KDA_ERR_STRIDE;
+    if ((tokens > 0 && (!a.q || !a.k || !a.v || !a.g || !a.beta || !a.out)) || !a.A_log)
+        return KDA_ERR_NULL_POINTER;
+    const Span sq = span(a.q, nq), sk = span(a.k, nk), sv = span(a.v, nv), sg = span(a.g, ng), sb = span(a.beta, nb),
+               sA = span(a.A_log, a.H * 4), sd = span(a.dt_bias, a.H * 4),
+               su = span(a.cu_seqlens, a.cu_seqlens ? (p.seqs.N + 1) * 8 : 0), so = span(a.out, tokens * a.H * a.V * 2),
+               si = span(a.initial_state, a.initial_state ? state * bytes_of(a.initial_state_dtype) : 0),
+               sf = span(a.final_state, a.final_state ? state * bytes_of(a.final_state_dtype) : 0);
+    if (any_overlap(so, {sq, sk, sv, sg, sb, sA, sd, su, si, sf}) ||
+        any_overlap(sf, {sq, sk, sv, sg, sb, sA, sd, su}) || (sf.overlaps(si) && a.final_state != a.initial_state))
+        return KDA_ERR_ALIAS;
+    if (misaligned(a.q, 2) || misaligned(a.k, 2) || misaligned(a.v, 2) || misaligned(a.g, 2) || misaligned(a.beta, 2) ||
+        misaligned(a.out, 16) || misaligned(a.initial_state, 16) || misaligned(a.final_state, 16) ||
+        misaligned(a.A_log, 4) || misaligned(a.dt_bias, 4) || misaligned(a.cu_seqlens, 8))
+        return KDA_ERR_ALIGNMENT;
+    if (p.seqs.N == 0 || (tokens == 0 && !a.final_state))
+        return KDA_OK;
+    p.q = static_cast<const uint16_t *>(a.q);
+    p.k = static_cast<const uint16_t *>(a.k);
+    p.v = static_cast<const uint16_t *>(a.v);
+    p.g = static_cast<const uint16_t *>(a.g);
+    p.beta = static_cast<const uint16_t *>(a.beta);
+    p.out = static_cast<uint16_t *>(a.out);
+    p.qb = a.q_stride_b;
+    p.qt = a.q_stride_t;
+    p.kb = a.k_stride_b;
+    p.kt = a.k_stride_t;
+    p.vb = a.v_stride_b;
+    p.vt = a.v_stride_t;
+    p.gb = a.g_stride_b;
+    p.gt = a.g_stride_t;
+    p.bb = a.beta_stride_b;
+    p.bt = a.beta_stride_t;
+    p.A_log = a.A_log;
+    p.dt_bias = a.dt_bias;
+    p.init_state = a.initial_state;
+    p.final_state = a.final_state;
+    p.init_kind = a.initial_state ? a.initial_state_dtype : KDA_DTYPE_NONE;
+    p.final_kind = a.final_state ? a.final_state_dtype : KDA_DTYPE_NONE;
+    p.H = a.H;
+    p.G = a.G;
+    p.K = a.K;
+    p.V = a.V;
+    p.scale = static_cast<float>(a.scale);
+    return launched(launch_delta_recurrent(p, static_cast<hipStream_t>(stream)));
 }
 
 extern "C" kda_status kda_gated_norm(const kda_gated_norm_args *args, void *stream)

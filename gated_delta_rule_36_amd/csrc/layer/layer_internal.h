@@ -152,5 +152,79 @@ constexpr int64_t kSsmMaxTokens = INT32_MAX - 4 * kSsmChunk;
 // wave loads up to 16 rows of x, b or c from one base, and 32 of z.
 constexpr int64_t kSsmMaxStride = int64_t(1) << 27, kSsmMaxZStride = int64_t(1) << 26;
 
+struct DeltaParams {
+    const uint16_t *q, *k, *v, *g, *beta;
+    int64_t qb, qt, kb, kt, vb, vt, gb, gt, bb, bt;  // element strides of batch row and token
+    uint16_t *out;
+    const float *A_log, *dt_bias;  // dt_bias may be nullptr
+    const void *init_state;
+    void *final_state;
+    int init_kind, final_kind;
+    Seqs seqs;
+    int64_t H, G, K, V;
+    float scale;
+};
+hipError_t launch_delta_recurrent(const DeltaParams &p, hipStream_t stream);
+constexpr int64_t kDeltaMaxV = 512;
+// Tokens a call: places are counted in 32 bits with sign, up to two tiles past
+// a sequence's end.  Token strides (elements) whose 64 rows of a tile stay
+// within 32 bits of bytes.
+constexpr int64_t kDeltaMaxTokens = INT32_MAX - 128, kDeltaMaxStride = int64_t(1) << 24;
+// Calls without cu_seqlens of at most this many tokens take the token recurrence.
+constexpr int64_t kDeltaRecurrentMaxTokens = 8;
+
+// Channels of a head that the rotation kernels take.
+constexpr int64_t kMaxHeadChannels = 512;
+
+// A paged cache: element strides of page, token and head.
+struct CacheStrides {
+    int64_t page, token, head;
+};
+
+// Norm and rotation of the rows of a token: `first` heads of x and then `second`
+// of y.  For the append, x are the keys and y the values, which go as they are
+// to `slots` of two caches.
+struct RotaryParams {
+    const uint16_t *x, *y;
+    int64_t xb, xt, yb, yt;  // element strides of batch row and token
+    uint16_t *x_out, *y_out;
+    const int64_t *positions;  // or nullptr: no rotation
+    const float *inv_freq;
+    const void *x_weight, *y_weight;  // or nullptr: no norm
+    int x_kind, y_kind;
+    int64_t B, T;
+    int first, second, D, R, interleaved;
+    NormEps eps;
+    float scale;
+    // the append
+    const int64_t *slots;
+    int64_t slot_count, page_size;
+    CacheStrides xc, yc;
+};
+hipError_t launch_rotary(const RotaryParams &p, hipStream_t stream);
+
+struct AttentionParams {
+    const uint16_t *q, *k, *v;
+    int64_t qr;
+    CacheStrides ks, vs;
+    const int32_t *table, *lengths;
+    int64_t table_stride;
+    uint16_t *out;
+    float *lse;  // or nullptr
+    int64_t N, Hq, Hk, D, pages, width, window;
+    uint32_t page_size, page_mul;  // t / page_size = umulhi(t, page_mul) >> page_shift for t < 2^31 (page_size > 1)
+    int page_shift;
+    int64_t splits;
+    float scale;
+    // of several splits: their unnormalised outputs [N, Hq, splits, D] and
+    // (maximum, sum) [N, Hq, splits, 2]
+    float *part, *stats;
+};
+constexpr int64_t kAttentionMaxD = 256;
+// Query heads of a key head that a workgroup takes, and the fewest tokens that
+// are worth a workgroup of their own.
+constexpr int64_t kAttentionRows = 16, kAttentionSplitTokens = 256;
+hipError_t launch_paged_attention(const AttentionParams &p, hipStream_t stream);
+
 }  // namespace layer
 }  // namespace kda

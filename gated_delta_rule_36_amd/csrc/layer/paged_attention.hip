@@ -1,0 +1,390 @@
+// Attention of one new token per sequence over a paged cache:
+//   out = sum_t p_t v_t,  p = softmax over the visible t of scale q . k_t
+// K and V of the visible tokens are read once and bound it; the products run
+// beside on matrix instructions for up to 16 query heads of a key head at once.
+//
+// A workgroup of four waves takes (sequence, key head, 16 of its query heads,
+// split of the tokens).  Each wave walks its own tiles of 32 tokens with the
+// running maximum and sum of a softmax and nothing shared until the end, where
+// the four are joined in LDS.  Where there are few (sequence, head) pairs the
+// tokens are split over workgroups, whose unnormalised results a second launch
+// joins.
+//
+// Operands of v_mfma_f32_16x16x32_bf16: lane (r = lane % 16, g = lane / 16)
+// holds row / column r, slots 8 g .. 8 g + 7; accumulator register i is row
+// 4 g + i of column r.
+//   scores^T [token][head] = K Q^T: rows of K and Q are operands as they lie,
+//     slot 8 g + e of step s is channel 32 s + 8 g + e;
+//   out^T [channel][head] = V^T P^T over the tile's 32 tokens: the scores'
+//     accumulators are the operand as they stand, slot 8 g + 4 a + i being token
+//     16 a + 4 g + i, and V comes in the same order from LDS by reads that
+//     transpose.
+// Probabilities enter as two bf16 parts, the first cut from just below the
+// number, so that both are positive and an infinite v stays one; together good
+// to 2^-16 (what the first leaves is below 2^-7, half a step of that 2^-16).
+// The products have time to spare, and out is then off by its own rounding alone.
+#include "layer_device.h"
+
+namespace kda {
+namespace layer {
+namespace {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kWaves = 4, kThreads = 64 * kWaves, TOK = 32;  // tokens of a wave's tile
+constexpr int ROWS = static_cast<int>(kAttentionRows);
+constexpr float kBelow = 1.0f - 0x1p-10f;
+constexpr float kLn2F = 0.693147180559945f;
+
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+__device__ __forceinline__ uint32_t lds_addr(const void *p)
+{
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_u8 *)p));
+}
+// Transposing LDS read: within each 16-lane row, lane L points at four bf16
+// X[L][0..3]; lane i receives X[4 r + i / 4][i % 4] for r = 0..3.
+__device__ __forceinline__ u32x2_t lds_tr(uint32_t a)
+{
+    return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                           (__attribute__((address_space(3))) s16x4_t *)(uintptr_t)a));
+}
+__device__ __forceinline__ f32x4_t mfma(u32x4_t a, u32x4_t b, f32x4_t c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+// The upper halves of two numbers: cut to bf16 towards zero.
+__device__ __forceinline__ uint32_t cut_bf16x2(float a, float b)
+{
+    return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302);
+}
+// The largest (the sum) over the four lanes of a column.
+__device__ __forceinline__ float column_max(float x)
+{
+    uint32_t u = __float_as_uint(x);
+    auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    uint32_t r0 = r[0], r1 = r[1];
+    u = __float_as_uint(fmaxf(__uint_as_float(r0), __uint_as_float(r1)));
+    r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    r0 = r[0];
+    r1 = r[1];
+    return fmaxf(__uint_as_float(r0), __uint_as_float(r1));
+}
+__device__ __forceinline__ float column_sum(float x)
+{
+    uint32_t u = __float_as_uint(x);
+    auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    uint32_t r0 = r[0], r1 = r[1];
+    u = __float_as_uint(__uint_as_float(r0) + __uint_as_float(r1));
+    r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    r0 = r[0];
+    r1 = r[1];
+    return __uint_as_float(r0) + __uint_as_float(r1);
+}
+
+// The visible tokens [first, first + count) of a sequence, and the tokens a
+// split takes; splits from `used` on have none.
+struct Visible {
+    int first, count, chunk, used;
+};
+__device__ __forceinline__ Visible visible(const AttentionParams &p, int64_t n)
+{
+    const int64_t room = p.width * static_cast<int64_t>(p.page_size);
+    int64_t length = p.lengths[n];
+    length = length < 0 ? 0 : length > room ? room : length;
+    const int64_t first = p.window > 0 && length > p.window ? length - p.window : 0;
+    Visible v;
+    v.first = static_cast<int>(first);
+    v.count = static_cast<int>(length - first);
+    const int splits = static_cast<int>(p.splits);
+    int chunk = (v.count + splits - 1) / splits;
+    chunk = chunk < static_cast<int>(kAttentionSplitTokens) ? static_cast<int>(kAttentionSplitTokens) : chunk;
+    v.chunk = (chunk + kWaves * TOK - 1) / (kWaves * TOK) * (kWaves * TOK);
+    v.used = (v.count + v.chunk - 1) / v.chunk;
+    return v;
+}
+
+template <int KS>
+struct Shared {
+    static constexpr int D = 32 * KS, kPitch = D + 16, kOutPitch = D + 4;
+    union {
+        alignas(16) uint16_t v[kWaves][TOK][kPitch];
+        alignas(16) float out[kWaves][ROWS][kOutPitch];
+    };
+    float top[kWaves][ROWS], sum[kWaves][ROWS];
+};
+
+template <int KS>
+__global__ __launch_bounds__(kThreads) void paged_attention_kernel(AttentionParams p, int row_tiles)
+{
+    constexpr int D = Shared<KS>::D, kPitch = Shared<KS>::kPitch;
+    __shared__ Shared<KS> sh;
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // consecutive workgroups: the key heads of a split, whose rows lie side by side
+    uint32_t at = blockIdx.x;
+    const int hk = at % static_cast<uint32_t>(p.Hk);
+    at /= static_cast<uint32_t>(p.Hk);
+    const int ht = at % static_cast<uint32_t>(row_tiles);
+    at /= static_cast<uint32_t>(row_tiles);
+    const int split = at % static_cast<uint32_t>(p.splits);
+    const int64_t n = at / static_cast<uint32_t>(p.splits);
+    const Visible vis = visible(p, n);
+    if (split > 0 && split >= vis.used)
+        return;
+    const int64_t from = static_cast<int64_t>(vis.first) + static_cast<int64_t>(split) * vis.chunk;
+    const int64_t last = static_cast<int64_t>(vis.first) + vis.count;
+    const int t0 = static_cast<int>(from), t1 = static_cast<int>(last < from + vis.chunk ? last : from + vis.chunk);
+    const int group = static_cast<int>(p.Hq / p.Hk), width = static_cast<int>(p.D);
+    const int row0 = ht * ROWS, rows = group - row0 < ROWS ? group - row0 : ROWS;
+
+    u32x4_t q[KS];
+    const uint16_t *qs = p.q + n * p.qr + (static_cast<int64_t>(hk) * group + row0 + r) * p.D + 8 * g;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+        q[s] = u32x4_t{0, 0, 0, 0};
+        if (r < rows && 32 * s + 8 * g < width)  // 8 channels of a multiple of 16
+            q[s] = *reinterpret_cast<const u32x4_a2 *>(qs + 32 * s);
+    }
+
+    const int32_t *table = p.table + n * p.table_stride;
+    const uint16_t *kh = p.k + static_cast<int64_t>(hk) * p.ks.head + 8 * g, *vh = p.v + static_cast<int64_t>(hk) * p.vs.head + 8 * g;
+    const auto page_index = [&](int t) {
+        return p.page_size == 1 ? static_cast<uint32_t>(t) : __umulhi(static_cast<uint32_t>(t), p.page_mul) >> p.page_shift;
+    };
+    // A lane's tokens of a tile are r and 16 + r; their pages are looked up a tile ahead.
+    int page[2];
+    const auto look_up = [&](int base) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            const int t = base + 16 * a + r;
+            page[a] = t < t1 ? table[page_index(t)] : -1;
+        }
+    };
+    // Of a last step that the head only half fills, the lanes past it read its
+    // first channels: what those give K is taken out, rows of V^T there are not stored.
+    const bool past = 32 * (KS - 1) + 8 * g >= width;
+    const int last_step = past ? -8 * g : 32 * (KS - 1);
+    u32x4_t kt[2][KS], vt[2][KS];
+    uint32_t seen = 0;  // bit t: token t of the tile is visible
+    const auto load_half = [&](int t, int pg, u32x4_t (&kx)[KS], u32x4_t (&vx)[KS]) {
+        const u32x4_t none = {0, 0, 0, 0};
+        const bool in = pg >= 0 && pg < p.pages;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) kx[s] = vx[s] = none;
+        if (in) {
+            const uint32_t off = static_cast<uint32_t>(t) - page_index(t) * p.page_size;
+            const uint16_t *kp = kh + static_cast<int64_t>(pg) * p.ks.page + static_cast<int64_t>(off) * p.ks.token;
+            const uint16_t *vp = vh + static_cast<int64_t>(pg) * p.vs.page + static_cast<int64_t>(off) * p.vs.token;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                kx[s] = *reinterpret_cast<const u32x4_a2 *>(kp + (s + 1 < KS ? 32 * s : last_step));
+                vx[s] = *reinterpret_cast<const u32x4_a2 *>(vp + (s + 1 < KS ? 32 * s : last_step));
+            }
+        }
+        return static_cast<uint32_t>(__ballot(in)) & 0xffffu;
+    };
+    const auto load = [&](int base) {
+        const uint32_t low = load_half(base + r, page[0], kt[0], vt[0]);
+        seen = low | load_half(base + 16 + r, page[1], kt[1], vt[1]) << 16;
+    };
+
+    f32x4_t o[2 * KS];
+#pragma unroll
+    for (int d = 0; d < 2 * KS; ++d) o[d] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    float top = -__builtin_inff(), sum = 0.0f;
+    const float scale2 = p.scale * kLog2eF;
+    const uint32_t vaddr = lds_addr(&sh.v[wave][4 * g + r / 4][4 * (r & 3)]);
+
+    int base = t0 + wave * TOK;
+    if (base < t1) {
+        look_up(base);
+        load(base);
+        look_up(base + kWaves * TOK);
+    }
+    for (; base < t1; base += kWaves * TOK) {
+        f32x4_t score0 = {0.0f, 0.0f, 0.0f, 0.0f}, score1 = score0;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            if (s + 1 == KS && past)
+                kt[0][s] = kt[1][s] = u32x4_t{0, 0, 0, 0};
+            score0 = mfma(kt[0][s], q[s], score0);
+            score1 = mfma(kt[1][s], q[s], score1);
+        }
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+                *reinterpret_cast<u32x4_t *>(&sh.v[wave][16 * a + r][32 * s + 8 * g]) = vt[a][s];
+        const uint32_t mine = seen >> (4 * g);
+        if (base + kWaves * TOK < t1) {
+            load(base + kWaves * TOK);
+            look_up(base + 2 * kWaves * TOK);
+        }
+        float most = -__builtin_inff(), x2[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float x = (j < 4 ? score0[j & 3] : score1[j & 3]) * scale2;
+            x2[j] = mine >> (j < 4 ? j : 12 + j) & 1 ? x : -__builtin_inff();
+            most = fmaxf(most, x2[j]);
+        }
+        const float next = fmaxf(top, column_max(most));
+        const float from_top = next == -__builtin_inff() ? 0.0f : next;
+        const float keep = exp2_f32(top - from_top);
+        top = next;
+        sum *= keep;
+        u32x4_t hi, lo;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float x = exp2_f32(x2[2 * j] - from_top), y = exp2_f32(x2[2 * j + 1] - from_top);
+            sum += x + y;
+            const uint32_t h = cut_bf16x2(x * kBelow, y * kBelow);
+            hi[j] = h;
+            lo[j] = pack_bf16x2(x - lo_f32(h), y - hi_f32(h));
+        }
+        if (__any(keep != 1.0f)) {
+#pragma unroll
+            for (int d = 0; d < 2 * KS; ++d) o[d] *= keep;
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+        for (int d = 0; d < 2 * KS; ++d) {
+            const u32x2_t x = lds_tr(vaddr + 32 * d), y = lds_tr(vaddr + 32 * d + 32 * kPitch);
+            const u32x4_t va = {x[0], x[1], y[0], y[1]};
+            o[d] = mfma(va, hi, o[d]);
+            o[d] = mfma(va, lo, o[d]);
+        }
+        asm volatile("" ::: "memory");
+    }
+
+    // the four waves' results, one after the other in LDS
+    sum = column_sum(sum);
+    __syncthreads();
+    if (g == 0) {
+        sh.top[wave][r] = top;
+        sh.sum[wave][r] = sum;
+    }
+#pragma unroll
+    for (int d = 0; d < 2 * KS; ++d)
+        *reinterpret_cast<f32x4_t *>(&sh.out[wave][r][16 * d + 4 * g]) = o[d];
+    __syncthreads();
+    const bool whole = vis.used <= 1;
+    for (int i = tid; i < rows * (D / 4); i += kThreads) {
+        const int row = i / (D / 4), d = 4 * (i - row * (D / 4));
+        float most = sh.top[0][row];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) most = fmaxf(most, sh.top[w][row]);
+        const float from_top = most == -__builtin_inff() ? 0.0f : most;
+        float total = 0.0f;
+        f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const float f = exp2_f32(sh.top[w][row] - from_top);
+            total = fmaf(f, sh.sum[w][row], total);
+            x += f * *reinterpret_cast<const f32x4_t *>(&sh.out[w][row][d]);
+        }
+        const int64_t head = n * p.Hq + static_cast<int64_t>(hk) * group + row0 + row;
+        if (whole) {
+            const float f = total == 0.0f ? 0.0f : 1.0f / total;
+            if (d < width)
+                *reinterpret_cast<u32x2_t *>(p.out + head * p.D + d) =
+                    u32x2_t{pack_bf16x2(x[0] * f, x[1] * f), pack_bf16x2(x[2] * f, x[3] * f)};
+            if (d == 0 && p.lse)
+                p.lse[head] = total == 0.0f ? -__builtin_inff() : (from_top + log2f(total)) * kLn2F;
+        } else {
+            const int64_t slot = head * p.splits + split;
+            if (d < width)
+                *reinterpret_cast<f32x4_t *>(p.part + slot * p.D + d) = x;
+            if (d == 0) {
+                p.stats[2 * slot] = most;
+                p.stats[2 * slot + 1] = total;
+            }
+        }
+    }
+}
+
+// Joins the splits of a row (one workgroup): lanes of four channels, the
+// splits dealt over the groups of lanes.
+constexpr int kJoinThreads = 256;
+__global__ __launch_bounds__(kJoinThreads) void paged_attention_join_kernel(AttentionParams p, int lanes)
+{
+    __shared__ __align__(16) float part[kJoinThreads][4];
+    __shared__ float shared_sum[kJoinThreads], shared_top[kJoinThreads / 64];
+    const int64_t head = blockIdx.x, n = head / p.Hq;
+    const Visible vis = visible(p, n);
+    if (vis.used <= 1)
+        return;
+    const int tid = threadIdx.x;
+    const float *stats = p.stats + 2 * head * p.splits;
+    float most = -__builtin_inff();
+    for (int s = tid; s < vis.used; s += kJoinThreads) most = fmaxf(most, stats[2 * s]);
+    for (int m = 32; m > 0; m >>= 1) most = fmaxf(most, __shfl_xor(most, m));
+    if ((tid & 63) == 0)
+        shared_top[tid >> 6] = most;
+    __syncthreads();
+    for (int w = 0; w < kJoinThreads / 64; ++w) most = fmaxf(most, shared_top[w]);
+    const float from_top = most == -__builtin_inff() ? 0.0f : most;
+
+    const int groups = kJoinThreads / lanes, grp = tid / lanes, d = 4 * (tid - grp * lanes);
+    f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
+    float total = 0.0f;
+    if (grp < groups && d < p.D) {
+        const float *src = p.part + head * p.splits * p.D + d;
+#pragma unroll 4
+        for (int s = grp; s < vis.used; s += groups) {
+            const float f = exp2_f32(stats[2 * s] - from_top);
+            total = fmaf(f, stats[2 * s + 1], total);
+            x += f * *reinterpret_cast<const f32x4_t *>(src + s * p.D);
+        }
+    }
+    *reinterpret_cast<f32x4_t *>(part[tid]) = x;
+    shared_sum[tid] = total;
+    __syncthreads();
+    if (grp != 0 || d >= p.D)
+        return;
+    for (int k = 1; k < groups; ++k) {
+        x += *reinterpret_cast<const f32x4_t *>(part[k * lanes + tid]);
+        total += shared_sum[k * lanes + tid];
+    }
+    const float f = total == 0.0f ? 0.0f : 1.0f / total;
+    *reinterpret_cast<u32x2_t *>(p.out + head * p.D + d) =
+        u32x2_t{pack_bf16x2(x[0] * f, x[1] * f), pack_bf16x2(x[2] * f, x[3] * f)};
+    if (d == 0 && p.lse)
+        p.lse[head] = total == 0.0f ? -__builtin_inff() : (from_top + log2f(total)) * kLn2F;
+}
+
+template <int KS>
+hipError_t launch(const AttentionParams &p, hipStream_t stream)
+{
+    const int64_t row_tiles = (p.Hq / p.Hk + ROWS - 1) / ROWS;
+    const int64_t blocks = p.N * p.splits * row_tiles * p.Hk;
+    if (!grid_fits(blocks, kThreads) || !grid_fits(p.N * p.Hq, kJoinThreads))
+        return hipErrorInvalidConfiguration;
+    paged_attention_kernel<KS><<<dim3(static_cast<uint32_t>(blocks)), dim3(kThreads), 0, stream>>>(p, static_cast<int>(row_tiles));
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.splits == 1)
+        return e;
+    paged_attention_join_kernel<<<dim3(static_cast<uint32_t>(p.N * p.Hq)), dim3(kJoinThreads), 0, stream>>>(
+        p, static_cast<int>(p.D / 4));
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_paged_attention(const AttentionParams &p, hipStream_t stream)
+{
+    switch ((p.D + 31) / 32) {
+    case 1: return launch<1>(p, stream);
+    case 2: return launch<2>(p, stream);
+    case 3: return launch<3>(p, stream);
+    case 4: return launch<4>(p, stream);
+    case 5: return launch<5>(p, stream);
+    case 6: return launch<6>(p, stream);
+    case 7: return launch<7>(p, stream);
+    case 8: return launch<8>(p, stream);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace layer
+}  // namespace kda

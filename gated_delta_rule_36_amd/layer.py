@@ -1,5 +1,5 @@
 """Python binding of the layer operators: ``short_conv``, ``ssm_fwd``,
-``gated_norm`` and ``residual_norm``.
+``delta_fwd``, ``gated_norm`` and ``residual_norm``.
 
 Argument marshalling only, like :func:`gated_delta_rule_36_amd.fwd`: the
 caller gives the output tensors, the call is enqueued on the current stream
@@ -34,14 +34,14 @@ def _tensor(name, t, device, *dtypes):
     return t
 
 
-def _device(x):
+def _device(x, name="x"):
     """x's device, which must be a GPU; x must be bf16."""
     if not isinstance(x, torch.Tensor):
-        raise TypeError("x must be a torch.Tensor")
+        raise TypeError(f"{name} must be a torch.Tensor")
     if x.dtype != _BF16:
-        raise TypeError(f"x must be {_BF16}, got {x.dtype}")
+        raise TypeError(f"{name} must be {_BF16}, got {x.dtype}")
     if x.device.type != "cuda":
-        raise ValueError(f"x must be on a GPU device, got {x.device}")
+        raise ValueError(f"{name} must be on a GPU device, got {x.device}")
     return x.device
 
 
@@ -245,6 +245,48 @@ def ssm_fwd(x: torch.Tensor, dt: torch.Tensor, b: torch.Tensor, c: torch.Tensor,
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
         args = _pack(pack, values + (workspace.data_ptr(), nbytes))
     _call("kda_ssm_fwd", values, device, args)
+    return out
+
+
+def delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor, scale: float,
+              out: torch.Tensor, A_log: torch.Tensor, dt_bias: Optional[torch.Tensor] = None, *,
+              initial_state: Optional[torch.Tensor] = None, final_state: Optional[torch.Tensor] = None,
+              cu_seqlens: Optional[torch.Tensor] = None, check_cu_seqlens: bool = True) -> torch.Tensor:
+    """Gated delta rule with one decay per head; writes ``out`` (and ``final_state``).
+
+    Per head, with a state S of [K, V]: ``S = exp(-exp(A_log) softplus(g + dt_bias)) S``,
+    ``S += sigmoid(beta) k (v - S^T k)^T``, ``out = scale S^T q``: :func:`fwd`
+    with a decay that the channels of a head share and that has no lower
+    bound.  ``q`` and ``k`` are bf16 ``[B, T, G, K]`` (G divides H; heads share
+    a group's q and k) as the caller normalised them, ``v`` and ``out`` bf16
+    ``[B, T, H, V]``, ``g`` and ``beta`` bf16 ``[B, T, H]``, ``A_log`` and
+    ``dt_bias`` fp32 ``[H]``.  K is 64, 128 or 256, V a multiple of 16 up to
+    512.  The states are ``[N, H, V, K]`` (sequences first) in bf16 or fp32 and
+    may be one buffer.  ``cu_seqlens`` and ``check_cu_seqlens`` are those of
+    :func:`fwd`.
+    """
+    device = _device(v, "v")
+    if v.dim() != 4:
+        raise ValueError(f"v must be [B,T,H,V], got {list(v.shape)}")
+    B, T, H, V = shape = v.shape
+    _tensor("k", k, device, _BF16)
+    if k.dim() != 4:
+        raise ValueError(f"k must be [B,T,G,K], got {list(k.shape)}")
+    G, K = k.shape[2], k.shape[3]
+    pv, vb, vt = _tokens("v", v, device, shape)
+    pk, kb, kt = _tokens("k", k, device, (B, T, G, K))
+    pq, qb, qt = _tokens("q", q, device, (B, T, G, K)) if q is not None else _tensor("q", q, device, _BF16)
+    pg, gb, gt = _tokens("g", g, device, (B, T, H)) if g is not None else _tensor("g", g, device, _BF16)
+    pb, bb, bt = _tokens("beta", beta, device, (B, T, H)) if beta is not None else _tensor("beta", beta, device, _BF16)
+    po = _dense("out", out, device, shape, _BF16)
+    _tensor("A_log", A_log, device, torch.float32)
+    pA = _dense("A_log", A_log, device, (H,), torch.float32)
+    pt = _dense("dt_bias", dt_bias, device, (H,), torch.float32)
+    pu, num, seqs = _sequences(cu_seqlens, device, B, T, check_cu_seqlens)
+    pi, icode = _typed("initial_state", initial_state, device, (seqs, H, V, K))
+    pf, fcode = _typed("final_state", final_state, device, (seqs, H, V, K))
+    _call("kda_delta_fwd", (pq, pk, pv, pg, pb, po, qb, qt, kb, kt, vb, vt, gb, gt, bb, bt, pA, pt, pi, pf, pu, num,
+                            B, T, H, G, K, V, icode, fcode, 0, scale), device)
     return out
 
 

@@ -532,8 +532,200 @@ typedef struct kda_residual_norm_args {
 } kda_residual_norm_args;
 kda_status kda_residual_norm(const kda_residual_norm_args *args, void *stream);
 
+/*
+ * kda_delta_fwd - the gated delta rule with one decay per head, over prompts
+ * and single tokens.  Per (sequence, head) and token (state S is K x V, fp32):
+ *
+ *   S   = exp(-exp(A_log[h]) softplus(g_t + dt_bias[h])) S
+ *   S   = S + sigmoid(beta_t) k_t (v_t - S^T k_t)^T
+ *   o_t = scale * S^T q_t
+ *
+ * which is kda_fwd's recurrence with a decay that all channels of a head share
+ * and that has no lower bound.
+ *
+ *   q, k           bf16 [B,T,G,K]; heads h with the same h / (H / G) share q
+ *                  and k (G divides H).  The caller normalises them, as for
+ *                  kda_fwd: a k longer than 1 can make the recurrence grow.
+ *   v, out         bf16 [B,T,H,V]; out is contiguous.
+ *   g, beta        bf16 [B,T,H], the raw decay and the logit of the write.
+ *   A_log, dt_bias fp32 [H]; dt_bias may be NULL (0).
+ *   scale          0 or a normal number of fp32.
+ *   initial_state, final_state  [N,H,V,K] of their dtypes, stored as kda_fwd
+ *                  stores them; they may be one buffer.
+ *   cu_seqlens, num_seqs, B, T, H   as for kda_fwd, with T < 2^31 - 128
+ *                  (KDA_ERR_SIZE otherwise).
+ *   K              64, 128 or 256; V a multiple of 16, at most 512
+ *                  (KDA_ERR_SHAPE otherwise).
+ *   Token strides are at most 2^24 elements where more than 8 tokens are
+ *   given, or packed ones (KDA_ERR_STRIDE otherwise).
+ *
+ * A non-finite q reaches its own token's output alone; a non-finite k, v, g or
+ * beta reaches outputs of its head (k: its group's heads) from its own token
+ * on, never earlier ones, and never another sequence.  Numbers beyond 2^120
+ * that the recurrence forms on the way count as non-finite.
+ */
+typedef struct kda_delta_args {
+    const void *q;
+    const void *k;
+    const void *v;
+    const void *g;
+    const void *beta;
+    void *out;
+    int64_t q_stride_b, q_stride_t, k_stride_b, k_stride_t, v_stride_b, v_stride_t;
+    int64_t g_stride_b, g_stride_t, beta_stride_b, beta_stride_t;
+    const float *A_log;
+    const float *dt_bias;
+    const void *initial_state;
+    void *final_state;
+    const int64_t *cu_seqlens;
+    int64_t num_seqs, B, T, H, G, K, V;
+    int32_t initial_state_dtype, final_state_dtype; /* kda_dtype */
+    int64_t reserved;
+    double scale;
+} kda_delta_args;
+kda_status kda_delta_fwd(const kda_delta_args *args, void *stream);
+
+/* -------------------------------------------------------------------------
+ * The attention layers that a hybrid model alternates with recurrent ones:
+ * queries and keys normalised and rotated, the paged cache and the attention
+ * of one new token over it.  The layer operators' rules hold.
+ *
+ * A cache is bf16 [pages, page_size, Hk, D] with the channels adjacent and any
+ * strides of page, token and head (elements, >= 0).  Slot s of it is token
+ * s % page_size of page s / page_size.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * kda_qk_norm_rotary - RMS norm of every query and key head and the rotation
+ * of its first R channels by the token's position, in one pass:
+ *
+ *   y = x / sqrt(eps + mean of x^2 over the head) * weight   (x without weight)
+ *   the pair (y_i, y_j) of frequency f is turned by angle positions[t] inv_freq[f]:
+ *     out_i = rotary_scale (y_i cos - y_j sin), out_j = rotary_scale (y_j cos + y_i sin)
+ *   pairs: (f, f + R / 2), or interleaved (2 f, 2 f + 1); channels from R on stay y.
+ *
+ *   q, k           bf16 [B,T,Hq,D] and [B,T,Hk,D]; k may be NULL (Hk is 0 then).
+ *   q_out, k_out   bf16, contiguous; each may be its input, where that is
+ *                  contiguous.
+ *   positions      int64 [B,T], contiguous; inv_freq fp32 [R/2].  Angles are
+ *                  formed and reduced in 64 bits.  Both NULL: no rotation (R
+ *                  is ignored).
+ *   q_weight, k_weight   [D] of their dtypes; NULL = no norm.
+ *   D              a multiple of 2, at most 512; R a multiple of 2, 2 <= R <= D
+ *                  (KDA_ERR_SHAPE otherwise).
+ *   eps, rotary_scale    eps finite, >= 0; rotary_scale 0 or a normal number of
+ *                  fp32 (KDA_ERR_SCALE otherwise).
+ */
+typedef struct kda_rotary_args {
+    const void *q;
+    const void *k;
+    void *q_out;
+    void *k_out;
+    int64_t q_stride_b, q_stride_t, k_stride_b, k_stride_t;
+    const int64_t *positions;
+    const float *inv_freq;
+    const void *q_weight;
+    const void *k_weight;
+    int64_t B, T, Hq, Hk, D, R;
+    int32_t q_weight_dtype, k_weight_dtype; /* kda_dtype */
+    int32_t interleaved;                    /* 0 or 1 */
+    int32_t reserved;
+    double eps, rotary_scale;
+} kda_rotary_args;
+kda_status kda_qk_norm_rotary(const kda_rotary_args *args, void *stream);
+
+/*
+ * kda_append_kv - writes the keys and values of new tokens into their slots of
+ * a paged cache, the keys normalised and rotated on the way as
+ * kda_qk_norm_rotary does it.
+ *
+ *   k, v           bf16 [B,T,Hk,D].
+ *   k_cache, v_cache   see above; no two places of a cache may share memory
+ *                  (KDA_ERR_STRIDE).  Only the tokens' slots are written.
+ *   slots          int64 [B,T], contiguous: the token's slot.  Tokens with a
+ *                  slot outside [0, pages * page_size) are left out (a padded
+ *                  token has -1).  Tokens that share a slot leave one of their
+ *                  values in each element of it, which one is not defined.
+ *   positions, inv_freq, weight, D, R, eps, rotary_scale
+ *                  as for kda_qk_norm_rotary.
+ */
+typedef struct kda_append_args {
+    const void *k;
+    const void *v;
+    void *k_cache;
+    void *v_cache;
+    int64_t k_stride_b, k_stride_t, v_stride_b, v_stride_t;
+    int64_t k_cache_stride_page, k_cache_stride_token, k_cache_stride_head;
+    int64_t v_cache_stride_page, v_cache_stride_token, v_cache_stride_head;
+    const int64_t *slots;
+    const int64_t *positions;
+    const float *inv_freq;
+    const void *weight;
+    int64_t B, T, Hk, D, R, pages, page_size;
+    int32_t weight_dtype; /* kda_dtype */
+    int32_t interleaved;  /* 0 or 1 */
+    int64_t reserved;
+    double eps, rotary_scale;
+} kda_append_args;
+kda_status kda_append_kv(const kda_append_args *args, void *stream);
+
+/*
+ * kda_paged_attention - softmax attention of one new token per sequence over
+ * its keys and values in a paged cache:
+ *
+ *   out[n,h] = sum_t p_t v_t,  p = softmax over t of scale * q[n,h] . k_t,
+ *   lse[n,h] = log of the sum over t of exp(scale * q[n,h] . k_t)
+ *
+ * over the tokens t of sequence n that are visible: t < lengths[n], and with
+ * window > 0 t >= lengths[n] - window.  Token t lies in page block_table[n,
+ * t / page_size].  Query heads h with the same h / (Hq / Hk) share a key head.
+ *
+ *   q              bf16 [N,Hq,D], element stride q_stride of a sequence.
+ *   block_table    int32 [N, table_width], element stride table_stride of a
+ *                  sequence.  A page outside [0, pages) is not read: its
+ *                  tokens are not visible.
+ *   lengths        int32 [N]; clamped to [0, table_width * page_size].
+ *   out            bf16 [N,Hq,D], contiguous.
+ *   lse            fp32 [N,Hq], contiguous; NULL = not written.
+ *                  Sequences without a visible token get out = 0, lse = -inf.
+ *                  Tokens that are not visible may hold anything.
+ *   D              a multiple of 16, at most 256; Hk divides Hq
+ *                  (KDA_ERR_SHAPE otherwise).
+ *   scale          0 or a normal number of fp32 (KDA_ERR_SCALE otherwise).
+ *   window         >= 0; 0 = every token (KDA_ERR_SIZE otherwise).
+ *   workspace, workspace_bytes   DEVICE scratch, 16-byte aligned, at least
+ *                  kda_paged_attention_workspace_bytes(args) bytes (which may
+ *                  be 0), as for kda_fwd_scan (KDA_ERR_WORKSPACE otherwise).
+ * N = 0 does nothing.  The contents of block_table and lengths are not read on
+ * the host; table_width bounds the work that is launched.
+ */
+typedef struct kda_attention_args {
+    const void *q;
+    const void *k_cache;
+    const void *v_cache;
+    const int32_t *block_table;
+    const int32_t *lengths;
+    void *out;
+    float *lse;
+    int64_t q_stride, table_stride;
+    int64_t k_cache_stride_page, k_cache_stride_token, k_cache_stride_head;
+    int64_t v_cache_stride_page, v_cache_stride_token, v_cache_stride_head;
+    int64_t N, Hq, Hk, D, pages, page_size, table_width, window;
+    int64_t reserved;
+    double scale;
+    void *workspace;
+    int64_t workspace_bytes;
+} kda_attention_args;
+kda_status kda_paged_attention(const kda_attention_args *args, void *stream);
+
+/*
+ * Bytes of workspace kda_paged_attention needs for these sizes; pointers are
+ * ignored.  -1 where the sizes are ones kda_paged_attention refuses.
+ */
+int64_t kda_paged_attention_workspace_bytes(const kda_attention_args *args);
+
 /* ABI version of this header (bumped on any signature change). */
-#define KDA_ABI_VERSION 5
+#define KDA_ABI_VERSION 6
 int kda_abi_version(void);
 
 #ifdef __cplusplus

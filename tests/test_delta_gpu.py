@@ -1,0 +1,239 @@
+"""delta_fwd on the GPU against the token recurrence in 64 bits: lengths, head
+layouts, states, packed sequences, strides, strong and weak decays, inputs that
+are not finite."""
+import math
+
+import pytest
+import torch
+
+import gated_delta_rule_36_amd as kda
+import mixer_ref as ref
+from mixer_ref import check
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+NAN = float("nan")
+
+
+def inputs(B, T, G, H, K, V, seed=0, n=None, state=F32, initial=True, alike=0.0):
+    """q and k as a convolution with SiLU and its L2 norm leaves them; `alike` mixes one direction into every key."""
+    g = torch.Generator().manual_seed(seed)
+    def normal(*shape): return torch.randn(*shape, generator=g)
+    def unit(x): return (x / x.norm(dim=-1, keepdim=True)).to(BF)
+    silu = torch.nn.functional.silu
+    x = dict(q=unit(silu(normal(B, T, G, K))), k=unit(silu(normal(B, T, G, K)) + alike * normal(K)),
+             v=silu(normal(B, T, H, V)).to(BF), g=normal(B, T, H).to(BF), beta=normal(B, T, H).to(BF), scale=K ** -0.5,
+             A_log=torch.log(1 + 15 * torch.rand(H, generator=g)))
+    step = torch.exp(torch.rand(H, generator=g) * math.log(100.0) + math.log(1e-3))
+    x["dt_bias"] = step + torch.log(-torch.expm1(-step))
+    x["initial"] = (0.3 * normal(n or B, H, V, K)).to(state) if initial else None
+    return x
+
+
+def call(x, cu=None, state=F32, final=True, **over):
+    """(out, final state) of a call with x's tensors on the GPU; unwritten outputs stay NaN."""
+    y = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in {**x, **over}.items()}
+    B, T, H, V = y["v"].shape
+    n = B if cu is None else len(cu) - 1
+    out = torch.full((B, T, H, V), NAN, dtype=BF, device="cuda")
+    fin = torch.full((n, H, V, y["k"].shape[-1]), NAN, dtype=state, device="cuda") if final else None
+    kda.delta_fwd(y["q"], y["k"], y["v"], y["g"], y["beta"], y["scale"], out, y["A_log"], y["dt_bias"],
+                  initial_state=y["initial"], final_state=fin,
+                  cu_seqlens=None if cu is None else torch.tensor(cu, device="cuda"))
+    return out, fin
+
+
+def row_bound(fin, want, fbound):
+    """Rows of the state as one number each, the length of the error, against the bound."""
+    half = torch.finfo(fin.dtype).eps / 2 if fin.dtype == BF else 2.0 ** -24
+    err = (fin.cpu().double() - want).norm(dim=-1)
+    room = fbound + half * want.norm(dim=-1) * 1.001 + 2.0 ** -100
+    worst = float((err / room).max())
+    print(f"[check] state: worst {worst:.3f} of what is allowed", flush=True)
+    assert worst <= 1.0
+
+
+def hold(x, cu=None, state=F32):
+    out, fin = call(x, cu, state)
+    wo, wf, bo, bf = ref.delta(**x, cu=cu)
+    check("out", out, wo, bo)
+    row_bound(fin, wf, bf)
+    return out, fin, wf
+
+
+@pytest.mark.parametrize("T", [0, 1, 2, 7, 8, 9, 15, 16, 17, 31, 33, 48, 63, 64, 65, 79, 127, 128, 129, 200, 321])
+def test_lengths(T):
+    hold(inputs(2, T, 1, 2, 128, 32, seed=T))
+
+
+@pytest.mark.parametrize("G,H,K,V", [(1, 1, 64, 16), (2, 2, 64, 48), (1, 3, 128, 128), (2, 4, 128, 96), (4, 4, 256, 64),
+                                     (1, 2, 256, 256), (1, 1, 64, 512), (3, 9, 64, 80), (1, 1, 128, 272)])
+@pytest.mark.parametrize("T", [3, 150])
+def test_heads(G, H, K, V, T):
+    hold(inputs(1, T, G, H, K, V, seed=K + V))
+
+
+@pytest.mark.parametrize("state", [F32, BF])
+@pytest.mark.parametrize("T", [5, 130])
+def test_states(state, T):
+    x = inputs(2, T, 1, 2, 128, 64, seed=3, state=state)
+    out, fin, _ = hold(x, state=state)
+    # in place
+    s = x["initial"].cuda()
+    y = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    again = torch.empty_like(out)
+    kda.delta_fwd(y["q"], y["k"], y["v"], y["g"], y["beta"], y["scale"], again, y["A_log"], y["dt_bias"],
+                  initial_state=s, final_state=s)
+    assert torch.equal(again, out) and torch.equal(s, fin)
+    # without either state, without a bias
+    x["initial"] = x["dt_bias"] = None
+    hold(x, state=state)
+    out, fin = call(x, final=False)
+    check("out", out, *ref.delta(**x)[0:3:2])
+
+
+@pytest.mark.parametrize("cu", [[0, 100], [0, 0, 1, 1, 30, 100], [0, 64, 65, 100], [5, 20, 20, 90], [0] * 70 + [100],
+                                list(range(101)), [0, 3, 6, 9, 40, 57, 89, 100]])
+def test_packed(cu):
+    x = inputs(1, 100, 1, 2, 64, 32, seed=len(cu), n=len(cu) - 1)
+    y = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    out = torch.full((1, 100, 2, 32), NAN, dtype=BF, device="cuda")
+    fin = torch.full((len(cu) - 1, 2, 32, 64), NAN, dtype=F32, device="cuda")
+    kda.delta_fwd(y["q"], y["k"], y["v"], y["g"], y["beta"], y["scale"], out, y["A_log"], y["dt_bias"],
+                  initial_state=y["initial"], final_state=fin, cu_seqlens=torch.tensor(cu, device="cuda"),
+                  check_cu_seqlens=False)
+    wo, wf, bo, bf = ref.delta(**x, cu=cu)
+    check("out", out, wo, bo)  # rows outside every sequence stay as they were
+    row_bound(fin, wf, bf)
+
+
+def test_packed_offsets_that_are_out_of_order_stay_inside():
+    x = inputs(1, 90, 1, 1, 64, 16, seed=9, n=3)
+    y = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    out = torch.zeros(1, 90, 1, 16, dtype=BF, device="cuda")
+    fin = torch.zeros(3, 1, 16, 64, device="cuda")
+    kda.delta_fwd(y["q"], y["k"], y["v"], y["g"], y["beta"], y["scale"], out, y["A_log"], initial_state=y["initial"],
+                  final_state=fin, cu_seqlens=torch.tensor([-5, 40, 20, 1 << 40], device="cuda"), check_cu_seqlens=False)
+    assert torch.isfinite(fin).all()
+
+
+def test_slices_of_projections():
+    """Odd places and strides; the same numbers as from contiguous tensors."""
+    x = inputs(2, 70, 1, 2, 64, 32, seed=21)
+    out, fin = call(x)
+    def within(t, before, after):
+        return torch.cat([torch.full((*t.shape[:2], before), NAN, dtype=BF), t.flatten(2),
+                          torch.full((*t.shape[:2], after), NAN, dtype=BF)], 2).cuda()[..., before:before + t[0, 0].numel()].view_as(t) \
+            if t.dim() == 3 else torch.cat([torch.full((*t.shape[:2], before), NAN, dtype=BF), t.flatten(2),
+                                            torch.full((*t.shape[:2], after), NAN, dtype=BF)],
+                                           2).cuda()[..., before:before + t[0, 0].numel()].unflatten(-1, t.shape[2:])
+    y = {k: within(x[k], 3, 4) for k in ("q", "k", "v")}
+    y.update({k: within(x[k], 1, 2) for k in ("g", "beta")})
+    again, fin2 = call(x, **y)
+    assert torch.equal(out, again) and torch.equal(fin, fin2)
+
+
+@pytest.mark.parametrize("T", [6, 200])
+@pytest.mark.parametrize("A,shift", [(-20.0, 0.0), (3.0, 6.0), (8.0, 10.0), (2.77, -8.0)])
+def test_decays(A, shift, T):
+    """From none at all to a state that is gone after each token, and both in one chunk."""
+    x = inputs(1, T, 1, 2, 64, 32, seed=31)
+    x["A_log"] = torch.full((2,), A)
+    x["g"] = (x["g"].float() * 3 + shift).to(BF)
+    x["g"][:, ::17] = 30.0  # a strong one now and then among weak ones
+    hold(x)
+
+
+@pytest.mark.parametrize("alike", [0.0, 1.0, 5.0])
+@pytest.mark.parametrize("strength", [-20.0, 0.0, 20.0])
+def test_keys_alike_and_write_strengths(alike, strength):
+    x = inputs(1, 200, 1, 2, 128, 32, seed=41, alike=alike)
+    x["beta"] = (x["beta"].float() + strength).to(BF)
+    x["A_log"] -= 4.0
+    hold(x)
+
+
+def test_the_same_key_every_time():
+    """Keys all equal, full strength, hardly any decay: every token replaces the one before."""
+    x = inputs(1, 140, 1, 1, 64, 16, seed=51)
+    x["k"] = x["k"][:, :1].expand(1, 140, 1, 64).contiguous()
+    x["beta"][:] = 30.0
+    x["A_log"] -= 10.0
+    hold(x)
+
+
+@pytest.mark.parametrize("T", [8, 180])
+@pytest.mark.parametrize("where", ["q", "k", "v", "g", "beta"])
+@pytest.mark.parametrize("value", [NAN, math.inf, -math.inf])
+def test_non_finite_inputs_reach_no_earlier_token_and_no_other_sequence(where, value, T):
+    x = inputs(3, T, 1, 2, 64, 32, seed=71)
+    clean, clean_fin = call(x)
+    t = T // 2 + 3
+    bad = x[where].clone()
+    bad[1, t, 0] = value if where in ("g", "beta") else bad[1, t, 0]
+    if where not in ("g", "beta"):
+        bad[1, t, 0, 5] = value
+    out, fin = call(x, **{where: bad})
+    assert torch.equal(out[0], clean[0]) and torch.equal(out[2], clean[2])
+    assert torch.equal(fin[0], clean_fin[0]) and torch.equal(fin[2], clean_fin[2])
+    assert torch.equal(out[1, :t], clean[1, :t])
+    if where == "q":
+        assert torch.equal(out[1, t + 1:], clean[1, t + 1:]) and torch.equal(fin, clean_fin)
+        assert not torch.isfinite(out[1, t].float()).any()
+    elif where != "k":
+        assert torch.equal(out[1, :, 1], clean[1, :, 1]) and torch.equal(fin[1, 1], clean_fin[1, 1])
+    if where in ("k", "v"):
+        assert not torch.isfinite(fin[1, 0, 5]).all()
+
+
+def test_large_values_stay_finite_where_the_recurrence_does():
+    x = inputs(1, 150, 1, 1, 64, 16, seed=81)
+    x["v"] = (x["v"].float() * 1e30).to(BF)
+    x["initial"] = x["initial"] * 1e30
+    hold(x)
+    x["v"] = (x["v"].float() * 1e-66).to(BF)
+    x["initial"] = x["initial"] * 1e-66
+    x["scale"] = 1.0
+    out, fin = call(x)
+    assert torch.isfinite(out.float()).all() and torch.isfinite(fin).all()
+
+
+def test_two_captured_graphs_and_eager_calls_between():
+    x = inputs(2, 100, 1, 2, 128, 64, seed=91)
+    y = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    want, want_fin = call(x)
+    def run(out, fin):
+        kda.delta_fwd(y["q"], y["k"], y["v"], y["g"], y["beta"], y["scale"], out, y["A_log"], y["dt_bias"],
+                      initial_state=y["initial"], final_state=fin)
+    outs = [(torch.empty_like(want), torch.empty_like(want_fin)) for _ in range(2)]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        run(*outs[0])
+    side.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in outs]
+    for graph, o in zip(graphs, outs):
+        with torch.cuda.graph(graph):
+            run(*o)
+    for _ in range(4):
+        for graph, (o, f) in zip(graphs, outs):
+            o.fill_(NAN)
+            f.fill_(NAN)
+            graph.replay()
+        eager = call(x)
+        torch.cuda.synchronize()
+        for o, f in (*outs, eager):
+            assert torch.equal(o, want) and torch.equal(f, want_fin)
+
+
+def test_two_streams():
+    a, b = inputs(1, 300, 1, 2, 64, 32, seed=101), inputs(1, 170, 1, 2, 64, 32, seed=102)
+    want = [call(x) for x in (a, b)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    for _ in range(10):
+        for s, x, o in zip(streams, (a, b), got):
+            with torch.cuda.stream(s):
+                o.append(call(x))
+    torch.cuda.synchronize()
+    for w, o in zip(want, got):
+        assert all(torch.equal(w[0], y) and torch.equal(w[1], f) for y, f in o)
