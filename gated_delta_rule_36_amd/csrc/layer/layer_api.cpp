@@ -337,7 +337,7 @@ extern "C" kda_status kda_delta_fwd(const kda_delta_args *args, void *stream)
     p.K = a.K;
     p.V = a.V;
     p.scale = static_cast<float>(a.scale);
-    return launched(launch_delta_recurrent(p, static_cast<hipStream_t>(stream)));
+    return launched((recurrent ? launch_delta_recurrent : launch_delta_chunk)(p, static_cast<hipStream_t>(stream)));
 }
 
 extern "C" kda_status kda_gated_norm(const kda_gated_norm_args *args, void *stream)

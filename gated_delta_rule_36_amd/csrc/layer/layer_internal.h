@@ -165,6 +165,7 @@ struct DeltaParams {
     float scale;
 };
 hipError_t launch_delta_recurrent(const DeltaParams &p, hipStream_t stream);
+hipError_t launch_delta_chunk(const DeltaParams &p, hipStream_t stream);
 constexpr int64_t kDeltaMaxV = 512;
 // Tokens a call: places are counted in 32 bits with sign, up to two tiles past
 // a sequence's end.  Token strides (elements) whose 64 rows of a tile stay
