@@ -36,10 +36,13 @@
 // the last is left out.  G is summed in 64 bits and kept as two floats, since
 // differences of sums lose a small decay beside a strong one.
 //
-// What is not finite (or beyond 2^120, where parts overflow) must not reach
-// earlier tokens through the zeros of a block's upper half: such elements of U
-// and all behind them in their column are taken for 0, and the column's outputs
-// from there on, and its state, are made NaN.
+// What is not finite must not reach earlier tokens through the zeros of a
+// block's upper half: where what U is solved from is not, it and all behind it in
+// its column are taken for 0, and the column's outputs from there on, and its
+// state, are made NaN.  So is U where it is not finite after all (a solve that
+// overflows by itself: then also tokens of the same 16 before).
+#include <type_traits>
+
 #include "layer_device.h"
 
 namespace kda {
@@ -49,9 +52,10 @@ namespace {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int TM = 64, NB = TM / 16;  // tokens and blocks of a tile
-constexpr int kWaves = 8, kThreads = 64 * kWaves, kColumns = 16 * kWaves;
-constexpr float kLarge = 0x1p120f;
+// Waves with 16 columns of the state each, and waves that prepare tiles.
+constexpr int kStateWaves = 8, kProducers = 4, kThreads = 64 * (kStateWaves + kProducers), kColumns = 16 * kStateWaves;
+// Magnitudes from here on round to infinity as bf16 (or are not finite).
+constexpr uint32_t kOddBits = 0x7f7f8000u;
 constexpr float kGone = -1000.0f;  // log decay below which nothing is left, also in 64 tokens' sum
 
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
@@ -94,7 +98,15 @@ __device__ __forceinline__ int here(int x)
     return x;
 }
 // v as a sum of bf16 numbers, each what is left rounded to nearest: two leave
-// 2^-17 of v at most, three hold its 24 bits.
+// 2^-17 of v at most, three hold its 24 bits.  What is left of both numbers of a
+// pair comes from its rounded ones by a dot product with (-1, 0) or (0, -1), exact
+// here, which takes the place of taking the pair apart and subtracting.  (A part
+// that is not finite makes its neighbour's rest so, too.)
+__device__ __forceinline__ float rest_of(uint32_t h, uint32_t which, float v)
+{
+    asm("" : "+s"(which));  // from a register: as an inline constant -1 does not stand for the pair (-1, 0)
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, h), __builtin_bit_cast(bf16x2_t, which), v, false);
+}
 template <int PARTS>
 __device__ __forceinline__ void split(f32x4_t v, u32x2_t (&h)[PARTS])
 {
@@ -104,22 +116,19 @@ __device__ __forceinline__ void split(f32x4_t v, u32x2_t (&h)[PARTS])
 #pragma unroll
         for (int k = 0; k < PARTS; ++k) {
             h[k][j] = pack_bf16x2(a, b);
-            a -= lo_f32(h[k][j]);
-            b -= hi_f32(h[k][j]);
+            if (k + 1 < PARTS) {
+                a = rest_of(h[k][j], 0x0000bf80u, a);
+                b = rest_of(h[k][j], 0xbf800000u, b);
+            }
         }
     }
 }
-__device__ __forceinline__ uint32_t size_bits(f32x4_t v)
+// The larger of two pairs of bf16 without their signs, each by itself.
+typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t max_bf16(uint32_t a, uint32_t b)
 {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
-        m = b > m ? b : m;
-    }
-    return m;
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a), __builtin_bit_cast(u16x2_t, b & 0x7fff7fffu)));
 }
-__device__ __forceinline__ bool odd(f32x4_t v) { return size_bits(v) > __float_as_uint(kLarge); }
 
 // The sum over the wave's lanes up to and with each lane.
 __device__ __forceinline__ double prefix(double x, int lane)
@@ -132,175 +141,188 @@ __device__ __forceinline__ double prefix(double x, int lane)
     return x;
 }
 
-// Rows of K and Q: 20 mod 64 dwords apart, which puts eight rows' 16 bytes in
-// distinct banks, and nearly all of what a transposing read takes.
+// Rows of K and Q in LDS: 16-byte aligned, and apart by what spreads 16 rows'
+// pieces (and what a transposing read takes of K) over the banks.
 template <int K>
-constexpr int kRowPitch = K == 64 ? 168 : K + 40;
-constexpr int kVPitch = kColumns + 16, kAPitch = TM + 4, kPPitch = TM + 8;
+constexpr int kKPitch = K == 64 ? 168 : K + 40;
+template <int K>
+constexpr int kQPitch = K + 8;
+constexpr int kVPitch = 24, kAPitch = 20, kPPitch = 40;
 
-template <int K>
-struct Shared {
-    alignas(16) uint16_t k[TM][kRowPitch<K>];
-    alignas(16) uint16_t q[TM][kRowPitch<K>];
-    alignas(16) uint16_t v[TM][kVPitch];
-    alignas(16) float a[TM][kAPitch];         // -A below the diagonal blocks, the inverses on it
-    alignas(16) uint16_t p[2][TM][kPPitch];   // two parts of P
-    // for the tiles in turn: G in two floats, 2^G, 2^(G_63 - G), beta
-    alignas(16) float g[2][2][TM], decay[2][TM], left[2][TM], beta[2][TM];
-    float total[2];                           // 2^(G_63)
+// Lower blocks (b, c), c <= b, one after the other; of P two of them, side by side
+// in the order of the slots.
+__device__ __forceinline__ constexpr int a_block(int b, int c) { return b * (b + 1) / 2 + c; }
+__device__ __forceinline__ constexpr int p_block(int b, int e) { return (b / 2) * (b / 2 + 1) + (b % 2) * (b / 2 + 1) + e; }
+
+template <int K, int TM>
+struct Tile {
+    static constexpr int NB = TM / 16;
+    alignas(16) uint16_t k[TM][kKPitch<K>];
+    alignas(16) uint16_t q[TM][kQPitch<K>];
+    alignas(16) float a[a_block(NB - 1, NB - 1) + 1][16][kAPitch];               // -A below the diagonal, the inverses on it
+    alignas(16) uint16_t p[2][p_block(NB - 1, (NB - 1) / 2) + 1][16][kPPitch];  // two parts of P
+    // G in two floats, 2^G, 2^(G_last - G), beta; 2^G_last
+    alignas(16) float g[2][TM], decay[TM], left[TM], beta[TM];
+    float total;
 };
 
-template <int K>
-__global__ __launch_bounds__(kThreads) void delta_chunk_kernel(DeltaParams p, int vblocks, int columns)
+template <int K, int TM>
+struct Shared {
+    Tile<K, TM> tile[2];
+    alignas(16) uint16_t v[kStateWaves][TM][kVPitch];
+};
+
+// Where a workgroup's chain lies.
+struct Chain {
+    int64_t n, h, grp, row;
+    int begin, tokens, col0, width;  // its tokens, its columns
+};
+__device__ __forceinline__ Chain find_chain(const DeltaParams &p, int vblocks, int columns)
 {
-    constexpr int KT = K / 16, KSTEP = K / 32, PK = K / 8;  // state tiles; steps over k; 16-byte pieces of a row
-    constexpr int kLoad = TM * PK / kThreads;               // pieces of K (and of Q) a thread loads
-    constexpr int kLoadV = TM * kColumns / 8 / kThreads;
-    constexpr bool kAhead = K <= 128;  // with 256 state rows the registers hold no tile in flight
-    static_assert(kLoad >= 1 && kLoadV >= 1, "whole rounds of loads");
-    __shared__ __align__(16) Shared<K> sh;
-
-    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    Chain c;
     const uint32_t chain = blockIdx.x / static_cast<uint32_t>(vblocks), vb = blockIdx.x - chain * static_cast<uint32_t>(vblocks);
-    const int64_t n = chain / static_cast<uint32_t>(p.H), h = chain - static_cast<uint32_t>(n) * static_cast<uint32_t>(p.H);
-    const int64_t grp = h / (p.H / p.G);
-    int64_t row = n;
-    int begin = 0, end = static_cast<int>(p.seqs.T);
+    c.n = chain / static_cast<uint32_t>(p.H);
+    c.h = chain - static_cast<uint32_t>(c.n) * static_cast<uint32_t>(p.H);
+    c.grp = c.h / (p.H / p.G);
+    c.row = c.n;
+    c.begin = 0;
+    int end = static_cast<int>(p.seqs.T);
     if (p.seqs.cu) {
-        row = 0;
-        begin = static_cast<int>(clamp_offset(p.seqs, n));
-        end = static_cast<int>(clamp_offset(p.seqs, n + 1));
+        c.row = 0;
+        c.begin = static_cast<int>(clamp_offset(p.seqs, c.n));
+        end = static_cast<int>(clamp_offset(p.seqs, c.n + 1));
     }
-    const int tokens = end > begin ? end - begin : 0;
-    const int col0 = static_cast<int>(vb) * columns, width = static_cast<int>(p.V) - col0 < columns ? static_cast<int>(p.V) - col0 : columns;
-    const bool active = 16 * wave < width;  // waves without columns help with what is shared
-    const int col = col0 + 16 * wave;
+    c.tokens = end > c.begin ? end - c.begin : 0;
+    c.col0 = static_cast<int>(vb) * columns;
+    c.width = static_cast<int>(p.V) - c.col0 < columns ? static_cast<int>(p.V) - c.col0 : columns;
+    return c;
+}
 
-    // the state: tile t's register i is k = 16 t + 4 g + i of column r
-    f32x4_t s[KT];
-    const int64_t slab = ((n * p.H + h) * p.V + col + r) * K + 4 * g;
-#pragma unroll
-    for (int t = 0; t < KT; ++t) {
-        s[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        if (active) {
-            if (p.init_kind == kFp32) {
-                s[t] = *reinterpret_cast<const f32x4_t *>(static_cast<const float *>(p.init_state) + slab + 16 * t);
-            } else if (p.init_kind == kBf16) {
-                const u32x2_t v = *reinterpret_cast<const u32x2_t *>(static_cast<const uint16_t *>(p.init_state) + slab + 16 * t);
-                s[t] = f32x4_t{lo_f32(v[0]), hi_f32(v[0]), lo_f32(v[1]), hi_f32(v[1])};
-            }
-        }
+// The waves that prepare tiles: rows of K and Q into LDS, decays and strengths,
+// the blocks of A and P, the inverses of A's diagonal blocks.
+template <int K, int TM>
+struct Producer {
+    static constexpr int NB = TM / 16, PK = K / 8, kLoad = TM * PK / (64 * kProducers);
+    static_assert(kLoad >= 1, "whole rounds of loads");
+    const DeltaParams &p;
+    const Chain &ch;
+    const int tid, lane, r, g, wave;
+    float rate, bias;
+    const char *kbase, *qbase;
+    const uint16_t *gbase, *bbase;
+    u32x4_t nk[kLoad], nq[kLoad];
+    uint32_t ng, nb;
+
+    __device__ __forceinline__ Producer(const DeltaParams &params, const Chain &chain, int t, int w)
+        : p(params), ch(chain), tid(t), lane(t & 63), r(t & 15), g((t & 63) >> 4), wave(w)
+    {
+        rate = -expf(p.A_log[ch.h]) * kLog2eF;
+        bias = p.dt_bias ? p.dt_bias[ch.h] : 0.0f;
+        kbase = reinterpret_cast<const char *>(p.k + ch.row * p.kb + static_cast<int64_t>(ch.begin) * p.kt + ch.grp * K);
+        qbase = reinterpret_cast<const char *>(p.q + ch.row * p.qb + static_cast<int64_t>(ch.begin) * p.qt + ch.grp * K);
+        gbase = p.g + ch.row * p.gb + static_cast<int64_t>(ch.begin) * p.gt + ch.h;
+        bbase = p.beta + ch.row * p.bb + static_cast<int64_t>(ch.begin) * p.bt + ch.h;
     }
 
-    const float rate = -expf(p.A_log[h]) * kLog2eF, bias = p.dt_bias ? p.dt_bias[h] : 0.0f;
-    const char *kbase = reinterpret_cast<const char *>(p.k + row * p.kb + static_cast<int64_t>(begin) * p.kt + grp * K);
-    const char *qbase = reinterpret_cast<const char *>(p.q + row * p.qb + static_cast<int64_t>(begin) * p.qt + grp * K);
-    const char *vbase = reinterpret_cast<const char *>(p.v + row * p.vb + static_cast<int64_t>(begin) * p.vt + h * p.V + col0);
-    const uint16_t *gbase = p.g + row * p.gb + static_cast<int64_t>(begin) * p.gt + h;
-    const uint16_t *bbase = p.beta + row * p.bb + static_cast<int64_t>(begin) * p.bt + h;
-    uint16_t *obase = p.out + ((row * p.seqs.T + begin) * p.H + h) * p.V + col;
-
-    // A tile's rows on their way from memory to LDS; rows past the end are zeros.
-    u32x4_t nk[kLoad], nq[kLoad], nv[kLoadV];
-    const auto load = [&](int t0) {
-        const int left = tokens - t0, me = here(tid);
+    // The tile's rows into registers; rows past the end are zeros.
+    __device__ __forceinline__ void load(int t0)
+    {
+        const int left = ch.tokens - t0, me = here(tid);
         const char *kp = kbase + static_cast<int64_t>(t0) * p.kt * 2, *qp = qbase + static_cast<int64_t>(t0) * p.qt * 2;
-        const char *vp = vbase + static_cast<int64_t>(t0) * p.vt * 2;
 #pragma unroll
         for (int i = 0; i < kLoad; ++i) {
-            const int piece = me + kThreads * i, t = piece / PK, c = piece % PK, in = t < left ? t : left - 1;
-            const u32x4_t x = *reinterpret_cast<const u32x4_a2 *>(kp + static_cast<uint32_t>(in) * static_cast<uint32_t>(2 * p.kt) + 16 * c);
-            const u32x4_t y = *reinterpret_cast<const u32x4_a2 *>(qp + static_cast<uint32_t>(in) * static_cast<uint32_t>(2 * p.qt) + 16 * c);
-            nk[i] = t < left ? x : u32x4_t{0, 0, 0, 0};
-            nq[i] = t < left ? y : u32x4_t{0, 0, 0, 0};
+            const int piece = me + 64 * kProducers * i, t = piece / PK, c = piece % PK, in = t < left ? t : left - 1;
+            nk[i] = *reinterpret_cast<const u32x4_a2 *>(kp + static_cast<uint32_t>(in) * static_cast<uint32_t>(2 * p.kt) + 16 * c);
+            nq[i] = *reinterpret_cast<const u32x4_a2 *>(qp + static_cast<uint32_t>(in) * static_cast<uint32_t>(2 * p.qt) + 16 * c);
         }
-#pragma unroll
-        for (int i = 0; i < kLoadV; ++i) {
-            const int piece = me + kThreads * i, t = piece / (kColumns / 8), c = piece % (kColumns / 8);
-            const int in = t < left ? t : left - 1, at = 8 * c < width ? c : 0;
-            const u32x4_t x = *reinterpret_cast<const u32x4_a2 *>(vp + static_cast<uint32_t>(in) * static_cast<uint32_t>(2 * p.vt) + 16 * at);
-            nv[i] = t < left ? x : u32x4_t{0, 0, 0, 0};
+        if (wave == kProducers - 1) {
+            const int in = lane < left ? lane : left - 1;
+            ng = gbase[static_cast<int64_t>(t0 + in) * p.gt];
+            nb = bbase[static_cast<int64_t>(t0 + in) * p.bt];
         }
-    };
-    const auto store = [&] {
-        const int me = here(tid);
+    }
+    __device__ __forceinline__ void store(Tile<K, TM> &to, int t0)
+    {
+        const int left = ch.tokens - t0, me = here(tid);
 #pragma unroll
         for (int i = 0; i < kLoad; ++i) {
             // channels 8 m .. 8 m + 7 of 32: two runs of four, in the order of the slots
-            const int piece = me + kThreads * i, t = piece / PK, c = piece % PK;
+            const int piece = me + 64 * kProducers * i, t = piece / PK, c = piece % PK;
             const int at = 32 * (c / 4) + 16 * (c % 2) + 4 * (c % 4 / 2);
-            *reinterpret_cast<u32x2_t *>(&sh.k[t][at]) = u32x2_t{nk[i][0], nk[i][1]};
-            *reinterpret_cast<u32x2_t *>(&sh.k[t][at + 8]) = u32x2_t{nk[i][2], nk[i][3]};
-            *reinterpret_cast<u32x2_t *>(&sh.q[t][at]) = u32x2_t{nq[i][0], nq[i][1]};
-            *reinterpret_cast<u32x2_t *>(&sh.q[t][at + 8]) = u32x2_t{nq[i][2], nq[i][3]};
+            const u32x4_t none = {0, 0, 0, 0}, x = t < left ? nk[i] : none, y = t < left ? nq[i] : none;
+            *reinterpret_cast<u32x2_t *>(&to.k[t][at]) = u32x2_t{x[0], x[1]};
+            *reinterpret_cast<u32x2_t *>(&to.k[t][at + 8]) = u32x2_t{x[2], x[3]};
+            *reinterpret_cast<u32x2_t *>(&to.q[t][at]) = u32x2_t{y[0], y[1]};
+            *reinterpret_cast<u32x2_t *>(&to.q[t][at + 8]) = u32x2_t{y[2], y[3]};
         }
-#pragma unroll
-        for (int i = 0; i < kLoadV; ++i) {
-            const int piece = me + kThreads * i, t = piece / (kColumns / 8), c = piece % (kColumns / 8);
-            *reinterpret_cast<u32x4_t *>(&sh.v[t][8 * c]) = nv[i];
-        }
-    };
+        if (wave == kProducers - 1)
+            gates(to, left);
+    }
     // The decays and strengths of a tile, a token a lane.
-    const auto gates = [&](int t0, int buf) {
-        const int t = t0 + lane, in = t < tokens ? t : tokens - 1;
-        const float raw = lo_f32(gbase[static_cast<int64_t>(in) * p.gt]) + bias;
-        const float logit = lo_f32(bbase[static_cast<int64_t>(in) * p.bt]);
-        float a = rate * softplus_f32(raw, dt_plain_above(1));
+    __device__ __forceinline__ void gates(Tile<K, TM> &to, int left)
+    {
+        const bool in = lane < left && lane < TM;
+        float a = rate * softplus_f32(lo_f32(ng) + bias, dt_plain_above(1));
         a = a < kGone ? kGone : a;
-        const double sum = prefix(t < tokens ? static_cast<double>(a) : 0.0, lane);
+        const double sum = prefix(in ? static_cast<double>(a) : 0.0, lane);
         const float hi = static_cast<float>(sum), lo = static_cast<float>(sum - static_cast<double>(hi));
         const float last_hi = __shfl(hi, 63), last_lo = __shfl(lo, 63);
-        sh.g[buf][0][lane] = hi;
-        sh.g[buf][1][lane] = lo;
-        sh.decay[buf][lane] = exp2_f32(hi + lo);
-        sh.left[buf][lane] = exp2_f32((last_hi - hi) + (last_lo - lo));
-        sh.beta[buf][lane] = t < tokens ? sigmoid_f32(logit) : 0.0f;
-        if (lane == 63)
-            sh.total[buf] = exp2_f32(hi + lo);
-    };
+        if (lane < TM) {
+            to.g[0][lane] = hi;
+            to.g[1][lane] = lo;
+            to.decay[lane] = exp2_f32(hi + lo);
+            to.left[lane] = exp2_f32((last_hi - hi) + (last_lo - lo));
+            to.beta[lane] = in ? sigmoid_f32(lo_f32(nb)) : 0.0f;
+            if (lane == 0)
+                to.total = exp2_f32(last_hi + last_lo);
+        }
+    }
     // Blocks (b, c) of A and P: lane r is token 16 b + r, its registers tokens 16 c + 4 g + i before it.
-    const auto block_products = [&](int b, int c, int buf, bool with_a, bool with_p) {
+    template <bool A, bool P>
+    __device__ __forceinline__ void block(Tile<K, TM> &to, int b, int c)
+    {
         f32x4_t kk = {0.0f, 0.0f, 0.0f, 0.0f}, qk = kk;
 #pragma unroll
-        for (int e = 0; e < KSTEP; ++e) {
-            const u32x4_t x = *reinterpret_cast<const u32x4_t *>(&sh.k[16 * c + r][32 * e + 8 * g]);
-            if (with_a)
-                kk = mfma(x, *reinterpret_cast<const u32x4_t *>(&sh.k[16 * b + r][32 * e + 8 * g]), kk);
-            if (with_p)
-                qk = mfma(x, *reinterpret_cast<const u32x4_t *>(&sh.q[16 * b + r][32 * e + 8 * g]), qk);
+        for (int e = 0; e < K / 32; ++e) {
+            const u32x4_t x = *reinterpret_cast<const u32x4_t *>(&to.k[16 * c + r][32 * e + 8 * g]);
+            if constexpr (A)
+                kk = mfma(x, *reinterpret_cast<const u32x4_t *>(&to.k[16 * b + r][32 * e + 8 * g]), kk);
+            if constexpr (P)
+                qk = mfma(x, *reinterpret_cast<const u32x4_t *>(&to.q[16 * b + r][32 * e + 8 * g]), qk);
         }
         const int i = 16 * b + r, j = 16 * c + 4 * g;
-        const float hi = sh.g[buf][0][i], lo = sh.g[buf][1][i];
-        const f32x4_t hj = *reinterpret_cast<const f32x4_t *>(&sh.g[buf][0][j]), lj = *reinterpret_cast<const f32x4_t *>(&sh.g[buf][1][j]);
+        const float hi = to.g[0][i], lo = to.g[1][i];
+        const f32x4_t hj = *reinterpret_cast<const f32x4_t *>(&to.g[0][j]), lj = *reinterpret_cast<const f32x4_t *>(&to.g[1][j]);
         f32x4_t x, y;
-        const float strength = with_a ? -sh.beta[buf][i] : 0.0f;
+        const float strength = A ? -to.beta[i] : 0.0f;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const float f = exp2_f32((hi - hj[m]) + (lo - lj[m]));
             x[m] = j + m < i ? strength * f * kk[m] : 0.0f;
             y[m] = j + m <= i ? f * qk[m] : 0.0f;
         }
-        if (with_a)
-            *reinterpret_cast<f32x4_t *>(&sh.a[i][j]) = x;
-        if (with_p) {
+        if constexpr (A)
+            *reinterpret_cast<f32x4_t *>(&to.a[a_block(b, c)][r][4 * g]) = x;
+        if constexpr (P) {
             u32x2_t parts[2];
             split<2>(y, parts);
-            const int at = 32 * (c / 2) + 8 * g + 4 * (c % 2);
-            *reinterpret_cast<u32x2_t *>(&sh.p[0][i][at]) = parts[0];
-            *reinterpret_cast<u32x2_t *>(&sh.p[1][i][at]) = parts[1];
+            uint16_t *to0 = &to.p[0][p_block(b, c / 2)][r][8 * g + 4 * (c % 2)], *to1 = &to.p[1][p_block(b, c / 2)][r][8 * g + 4 * (c % 2)];
+            *reinterpret_cast<u32x2_t *>(to0) = parts[0];
+            *reinterpret_cast<u32x2_t *>(to1) = parts[1];
         }
-    };
+    }
     // The inverses of the diagonal blocks I + A by forward substitution: lane (g, r)
     // has column r of block g, X_i = e_i - sum_(m < i) A_im X_m.
-    const auto invert = [&] {
+    __device__ __forceinline__ void invert(Tile<K, TM> &to)
+    {
+        const int bl = a_block(g < NB ? g : 0, g < NB ? g : 0);
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             x[i] = i == here(r) ? 1.0f : 0.0f;
 #pragma unroll
             for (int m4 = 0; m4 < i; m4 += 4) {
-                const f32x4_t a = *reinterpret_cast<const f32x4_t *>(&sh.a[16 * g + i][16 * g + m4]);
+                const f32x4_t a = *reinterpret_cast<const f32x4_t *>(&to.a[bl][i][m4]);
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
                     if (m4 + m < i)
@@ -310,178 +332,269 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(DeltaParams p, in
                 asm volatile("" : "+v"(x[i]), "+v"(x[i - 1]), "+v"(x[i - 2]), "+v"(x[i - 3])::"memory");
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (g < NB) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sh.a[16 * g + i][16 * g + r] = x[i];
-    };
-
-    // what P U reads of blocks above the diagonal
-    for (int i = tid; i < 2 * TM * kPPitch / 2; i += kThreads) reinterpret_cast<uint32_t *>(sh.p)[i] = 0;
-    if (tokens > 0) {
-        load(0);
-        if (wave == kWaves - 1)
-            gates(0, 0);
-        store();
+            for (int i = 0; i < 16; ++i) to.a[bl][i][r] = x[i];
+        }
     }
-    int buf = 0;
-    for (int t0 = 0; t0 < tokens; t0 += TM, buf ^= 1) {
-        lds_barrier();
-        const bool more = t0 + TM < tokens;
-        if (kAhead && more)
-            load(t0 + TM);
+    __device__ __forceinline__ void blocks(Tile<K, TM> &to)
+    {
+        constexpr int below = NB * (NB - 1) / 2;
         if (wave == 0) {
 #pragma unroll 1
-            for (int b = 0; b < NB; ++b) block_products(b, b, buf, true, false);
+            for (int b = 0; b < NB; ++b) block<true, false>(to, b, b);
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            invert();
-        } else {
-            // 6 blocks below the diagonal, of A and P, and 4 on it, of P
-#pragma unroll 1
-            for (int i = wave - 1; i < 10; i += kWaves - 1) {
-                const int b = i < 6 ? (i < 1 ? 1 : i < 3 ? 2 : 3) : i - 6, c = i < 6 ? i - (b == 1 ? 0 : b == 2 ? 1 : 3) : i - 6;
-                block_products(b, c, buf, i < 6, true);
-            }
-            if (wave == kWaves - 1 && more)
-                gates(t0 + TM, buf ^ 1);
+            invert(to);
+            return;
         }
+#pragma unroll 1
+        for (int i = wave - 1; i < below; i += kProducers - 1) {
+            const int b = i < 1 ? 1 : i < 3 ? 2 : 3;
+            block<true, true>(to, b, i - b * (b - 1) / 2);
+        }
+#pragma unroll 1
+        for (int b = kProducers - 1 - wave; b < NB; b += kProducers - 1) block<false, true>(to, b, b);
+    }
+    __device__ __forceinline__ void run(Shared<K, TM> &sh)
+    {
+        // what P U reads of blocks above the diagonal
+        for (int buf = 0; buf < 2; ++buf) {
+            uint32_t *z = reinterpret_cast<uint32_t *>(sh.tile[buf].p);
+            for (int i = tid; i < static_cast<int>(sizeof(sh.tile[buf].p) / 4); i += 64 * kProducers) z[i] = 0;
+        }
+        load(0);
+        store(sh.tile[0], 0);
+        if (TM < ch.tokens)
+            load(TM);
+        lds_barrier();
+        blocks(sh.tile[0]);
+        lds_barrier();
+        int buf = 1;
+        for (int t0 = TM; t0 < ch.tokens; t0 += TM, buf ^= 1) {
+            store(sh.tile[buf], t0);
+            if (t0 + TM < ch.tokens)
+                load(t0 + TM);
+            lds_barrier();
+            blocks(sh.tile[buf]);
+            lds_barrier();
+        }
+        lds_barrier();  // of the last tile
+        lds_barrier();
+    }
+};
+
+// A wave with 16 columns of the state.
+template <int K, int TM>
+__device__ __forceinline__ void state_wave(const DeltaParams &p, const Chain &ch, Shared<K, TM> &sh, int lane, int wave)
+{
+    constexpr int KT = K / 16, KSTEP = K / 32, NB = TM / 16;  // state tiles; steps over k; blocks of tokens
+    const int r = lane & 15, g = lane >> 4, col = ch.col0 + 16 * wave;
+    const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+
+    // the state: tile t's register i is k = 16 t + 4 g + i of column r
+    f32x4_t s[KT];
+    const int64_t slab = ((ch.n * p.H + ch.h) * p.V + col + r) * K + 4 * g;
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+        s[t] = zero;
+        if (p.init_kind == kFp32) {
+            s[t] = *reinterpret_cast<const f32x4_t *>(static_cast<const float *>(p.init_state) + slab + 16 * t);
+        } else if (p.init_kind == kBf16) {
+            const u32x2_t v = *reinterpret_cast<const u32x2_t *>(static_cast<const uint16_t *>(p.init_state) + slab + 16 * t);
+            s[t] = f32x4_t{lo_f32(v[0]), hi_f32(v[0]), lo_f32(v[1]), hi_f32(v[1])};
+        }
+    }
+    // The wave's own columns of V: half a row a lane, a tile ahead in registers.
+    constexpr int kLoad = TM / 32;
+    u32x4_t nv[kLoad];
+    const char *vbase = reinterpret_cast<const char *>(p.v + ch.row * p.vb + static_cast<int64_t>(ch.begin) * p.vt + ch.h * p.V + col);
+    const auto load = [&](int t0) {
+        const char *vp = vbase + static_cast<int64_t>(t0) * p.vt * 2;
+        const int left = ch.tokens - t0, me = here(lane);
+#pragma unroll
+        for (int i = 0; i < kLoad; ++i) {
+            const int t = me / 2 + 32 * i, in = t < left ? t : left - 1;
+            nv[i] = *reinterpret_cast<const u32x4_a2 *>(vp + static_cast<uint32_t>(in) * static_cast<uint32_t>(2 * p.vt) + 16 * (me & 1));
+        }
+    };
+    uint16_t *obase = p.out + ((ch.row * p.seqs.T + ch.begin) * p.H + ch.h) * p.V + col;
+    const int64_t ostride = p.H * p.V;
+
+    if (ch.tokens > 0) {
+        load(0);
+        lds_barrier();
+        lds_barrier();
+    }
+    int buf = 0;
+    for (int t0 = 0; t0 < ch.tokens; t0 += TM, buf ^= 1) {
+        const Tile<K, TM> &tl = sh.tile[buf];
+        const int left = ch.tokens - t0, me = here(lane);
+#pragma unroll
+        for (int i = 0; i < kLoad; ++i) {
+            const int t = me / 2 + 32 * i;
+            *reinterpret_cast<u32x4_t *>(&sh.v[wave][t][8 * (me & 1)]) = t < left ? nv[i] : u32x4_t{0, 0, 0, 0};
+        }
+        if (TM < left)
+            load(t0 + TM);
 
         // K S and Q S: rows are tokens of K S, columns of (Q S)^T
         f32x4_t u[NB], o[NB];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) u[b] = o[b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        if (active) {
+        for (int b = 0; b < NB; ++b) u[b] = o[b] = zero;
 #pragma unroll
-            for (int e = 0; e < KSTEP; ++e) {
-                u32x2_t x[3], y[3];
-                split<3>(s[2 * e], x);
-                split<3>(s[2 * e + 1], y);
-                const u32x4_t s0 = cat(x[0], y[0]), s1 = cat(x[1], y[1]), s2 = cat(x[2], y[2]);
+        for (int e = 0; e < KSTEP; ++e) {
+            u32x2_t x[3], y[3];
+            split<3>(s[2 * e], x);
+            split<3>(s[2 * e + 1], y);
+            const u32x4_t s0 = cat(x[0], y[0]), s1 = cat(x[1], y[1]), s2 = cat(x[2], y[2]);
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const u32x4_t kr = *reinterpret_cast<const u32x4_t *>(&sh.k[16 * b + r][32 * e + 8 * g]);
-                    const u32x4_t qr = *reinterpret_cast<const u32x4_t *>(&sh.q[16 * b + r][32 * e + 8 * g]);
-                    u[b] = mfma(kr, s0, u[b]);
-                    o[b] = mfma(s0, qr, o[b]);
-                    u[b] = mfma(kr, s1, u[b]);
-                    o[b] = mfma(s1, qr, o[b]);
-                    u[b] = mfma(kr, s2, u[b]);
-                }
-                fence();
+            for (int b = 0; b < NB; ++b) {
+                const u32x4_t kr = *reinterpret_cast<const u32x4_t *>(&tl.k[16 * b + r][32 * e + 8 * g]);
+                const u32x4_t qr = *reinterpret_cast<const u32x4_t *>(&tl.q[16 * b + r][32 * e + 8 * g]);
+                u[b] = mfma(kr, s0, u[b]);
+                o[b] = mfma(s0, qr, o[b]);
+                u[b] = mfma(kr, s1, u[b]);
+                o[b] = mfma(s1, qr, o[b]);
+                u[b] = mfma(kr, s2, u[b]);
             }
+            fence();
         }
         lds_barrier();
-        if (active) {
-            const uint32_t vaddr = lds_addr(&sh.v[4 * g + r / 4][16 * wave + 4 * (r & 3)]);
-            int poison = TM;  // of column r: the first token whose U is not finite
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const u32x2_t vr = lds_tr(vaddr + 32 * b * kVPitch);
-                const f32x4_t d = *reinterpret_cast<const f32x4_t *>(&sh.decay[buf][16 * b + 4 * g]);
-                const f32x4_t beta = *reinterpret_cast<const f32x4_t *>(&sh.beta[buf][16 * b + 4 * g]);
-                const f32x4_t v = {lo_f32(vr[0]), hi_f32(vr[0]), lo_f32(vr[1]), hi_f32(vr[1])};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) u[b][i] = beta[i] * fmaf(-d[i], u[b][i], v[i]);
-            }
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                // takes out what is odd in the block (16 tokens of each column), from its first on
-                const auto scrub = [&](f32x4_t &x) {
-                    if (!__any(odd(x) || poison < TM))
-                        return;
-                    int first = poison;
-#pragma unroll
-                    for (int i = 3; i >= 0; --i)
-                        if ((__float_as_uint(x[i]) & 0x7fffffffu) > __float_as_uint(kLarge) && 16 * b + 4 * g + i < first)
-                            first = 16 * b + 4 * g + i;
-                    const int other = __shfl_xor(first, 16), both = other < first ? other : first;
-                    const int far = __shfl_xor(both, 32);
-                    poison = far < both ? far : both;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[i] = 16 * b + 4 * g + i >= poison ? 0.0f : x[i];
-                };
-                f32x4_t rest = u[b];
-#pragma unroll
-                for (int c = 0; c < b; ++c)
-                    rest = mfma_f32(*reinterpret_cast<const f32x4_t *>(&sh.a[16 * b + r][16 * c + 4 * g]), u[c], rest);
-                scrub(rest);
-                u[b] = mfma_f32(*reinterpret_cast<const f32x4_t *>(&sh.a[16 * b + r][16 * b + 4 * g]), rest, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
-                scrub(u[b]);
-            }
 
-            fence();
-            // out
-            u32x2_t up[NB][2];
+        // beta (V - 2^G K S)
+        const uint32_t vaddr = lds_addr(&sh.v[wave][here(lane) / 4][4 * (here(lane) & 3)]);  // 4 g + r / 4
+        float fine[2] = {0.0f, 0.0f};
 #pragma unroll
-            for (int b = 0; b < NB; ++b) split<2>(u[b], up[b]);
+        for (int b = 0; b < NB; ++b) {
+            const u32x2_t vr = lds_tr(vaddr + 32 * b * kVPitch);
+            const f32x4_t d = *reinterpret_cast<const f32x4_t *>(&tl.decay[16 * b + 4 * g]);
+            const f32x4_t beta = *reinterpret_cast<const f32x4_t *>(&tl.beta[16 * b + 4 * g]);
+            const f32x4_t v = {lo_f32(vr[0]), hi_f32(vr[0]), lo_f32(vr[1]), hi_f32(vr[1])};
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                o[b] *= sh.decay[buf][16 * b + r];
-#pragma unroll
-                for (int e = 0; e <= b / 2; ++e) {
-                    const u32x2_t none = {0, 0};
-                    const bool two = 2 * e + 1 <= b;
-                    const u32x4_t u0 = cat(up[2 * e][0], two ? up[2 * e + 1][0] : none), u1 = cat(up[2 * e][1], two ? up[2 * e + 1][1] : none);
-                    const u32x4_t p0 = *reinterpret_cast<const u32x4_t *>(&sh.p[0][16 * b + r][32 * e + 8 * g]);
-                    const u32x4_t p1 = *reinterpret_cast<const u32x4_t *>(&sh.p[1][16 * b + r][32 * e + 8 * g]);
-                    o[b] = mfma(u0, p0, o[b]);
-                    o[b] = mfma(u1, p0, o[b]);
-                    o[b] = mfma(u0, p1, o[b]);
-                }
-                o[b] *= p.scale;
+            for (int i = 0; i < 4; ++i) {
+                u[b][i] = beta[i] * fmaf(-d[i], u[b][i], v[i]);
+                fine[i & 1] = fmaf(u[b][i], 0.0f, fine[i & 1]);
             }
-            const bool poisoned = __any(poison < TM);
-            if (poisoned) {
+        }
+        // The first token of column r that is odd; all from there on is taken out.
+        int poison = TM;
+        const auto clear = [&](int b) {
+            const int g4 = here(4 * g);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int from = __shfl(poison, 4 * g + i);
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) o[b][i] = 16 * b + r >= from ? __builtin_nanf("") : o[b][i];
-                }
-            }
+            for (int i = 0; i < 4; ++i) u[b][i] = 16 * b + g4 + i >= poison ? 0.0f : u[b][i];
+        };
+        const auto scrub = [&] {
+            const int g4 = here(4 * g);
+            int first = poison;
 #pragma unroll
             for (int b = 0; b < NB; ++b)
-                if (t0 + 16 * b + r < tokens)
-                    *reinterpret_cast<u32x2_t *>(obase + static_cast<int64_t>(t0 + 16 * b + r) * p.H * p.V + 4 * g) =
-                        u32x2_t{pack_bf16x2(o[b][0], o[b][1]), pack_bf16x2(o[b][2], o[b][3])};
-
-            fence();
-            // the state
-            u32x2_t w[NB][3];
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const f32x4_t left = *reinterpret_cast<const f32x4_t *>(&sh.left[buf][16 * b + 4 * g]);
-                split<3>(u[b] * left, w[b]);
-            }
-            const float total = sh.total[buf];
-            const uint32_t kaddr = lds_addr(&sh.k[4 * g + r / 4][8 * (r & 3)]);
-#pragma unroll
-            for (int t = 0; t < KT; ++t) {
-                s[t] *= total;
-#pragma unroll
-                for (int e = 0; e < NB / 2; ++e) {
-                    const uint32_t at = kaddr + 2 * (32 * (t / 2) + 4 * (t % 2)) + 2 * 32 * e * kRowPitch<K>;
-                    const u32x4_t kr = cat(lds_tr(at), lds_tr(at + 2 * 16 * kRowPitch<K>));
-#pragma unroll
-                    for (int k = 0; k < 3; ++k) s[t] = mfma(kr, cat(w[2 * e][k], w[2 * e + 1][k]), s[t]);
+                for (int i = 0; i < 4; ++i) {
+                    const int t = 16 * b + g4 + i;
+                    first = (__float_as_uint(u[b][i]) & 0x7fffffffu) >= kOddBits && t < first ? t : first;
                 }
-                if (t % 2 == 1)
-                    fence();
+            const int other = __shfl_xor(first, 16), both = other < first ? other : first;
+            const int far = __shfl_xor(both, 32);
+            poison = far < both ? far : both;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) clear(b);
+        };
+        bool poisoned = __any(fine[0] + fine[1] != 0.0f);
+        if (poisoned)
+            scrub();
+        fence();
+        // U, block by block
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            if (poisoned)
+                clear(b);  // rows of A may not be finite, either
+            u[b] = mfma_f32(*reinterpret_cast<const f32x4_t *>(&tl.a[a_block(b, b)][r][4 * g]), u[b], zero);
+#pragma unroll
+            for (int c = b + 1; c < NB; ++c)
+                u[c] = mfma_f32(*reinterpret_cast<const f32x4_t *>(&tl.a[a_block(c, b)][r][4 * g]), u[b], u[c]);
+            fence();
+        }
+        u32x2_t up[NB][2];
+        uint32_t most = 0;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            split<2>(u[b], up[b]);
+            most = max_bf16(max_bf16(most, up[b][0][0]), up[b][0][1]);
+        }
+        if (__any((most & 0xffffu) >= 0x7f80u || most >= 0x7f800000u)) {
+            scrub();
+            poisoned = true;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) split<2>(u[b], up[b]);
+        }
+        fence();
+
+        // out
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            o[b] *= tl.decay[16 * b + r];
+#pragma unroll
+            for (int e = 0; e <= b / 2; ++e) {
+                const u32x2_t none = {0, 0};
+                const bool two = 2 * e + 1 <= b;
+                const u32x4_t u0 = cat(up[2 * e][0], two ? up[2 * e + 1][0] : none), u1 = cat(up[2 * e][1], two ? up[2 * e + 1][1] : none);
+                const u32x4_t p0 = *reinterpret_cast<const u32x4_t *>(&tl.p[0][p_block(b, e)][r][8 * g]);
+                const u32x4_t p1 = *reinterpret_cast<const u32x4_t *>(&tl.p[1][p_block(b, e)][r][8 * g]);
+                o[b] = mfma(u0, p0, o[b]);
+                o[b] = mfma(u1, p0, o[b]);
+                o[b] = mfma(u0, p1, o[b]);
             }
-            if (poisoned) {
+            o[b] *= p.scale;
+            fence();
+        }
+        if (poisoned) {
 #pragma unroll
-                for (int t = 0; t < KT; ++t)
+            for (int i = 0; i < 4; ++i) {
+                const int from = __shfl(poison, here(4 * g) + i);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) s[t][i] = poison < TM ? __builtin_nanf("") : s[t][i];
+                for (int b = 0; b < NB; ++b) o[b][i] = 16 * b + here(r) >= from ? __builtin_nanf("") : o[b][i];
             }
         }
-        if (more) {
-            if (!kAhead)
-                load(t0 + TM);
-            lds_barrier();
-            store();
+        uint16_t *op = obase + (t0 + here(r)) * ostride + here(4 * g);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+            if (16 * b + r < left)
+                *reinterpret_cast<u32x2_t *>(op + 16 * b * ostride) =
+                    u32x2_t{pack_bf16x2(o[b][0], o[b][1]), pack_bf16x2(o[b][2], o[b][3])};
+        fence();
+
+        // the state
+        u32x2_t w[NB][3];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const f32x4_t weight = *reinterpret_cast<const f32x4_t *>(&tl.left[16 * b + 4 * g]);
+            split<3>(u[b] * weight, w[b]);
         }
+        const float total = tl.total;
+        const uint32_t kaddr = lds_addr(&tl.k[here(lane) / 4][8 * (here(lane) & 3)]);
+#pragma unroll
+        for (int t = 0; t < KT; ++t) {
+            s[t] *= total;
+#pragma unroll
+            for (int e = 0; e < NB / 2; ++e) {
+                const uint32_t at = kaddr + 2 * (32 * (t / 2) + 4 * (t % 2)) + 2 * 32 * e * kKPitch<K>;
+                const u32x4_t kr = cat(lds_tr(at), lds_tr(at + 2 * 16 * kKPitch<K>));
+#pragma unroll
+                for (int k = 0; k < 3; ++k) s[t] = mfma(kr, cat(w[2 * e][k], w[2 * e + 1][k]), s[t]);
+            }
+            if (t % 2 == 1)
+                fence();
+        }
+        if (poisoned) {
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[t][i] = poison < TM ? __builtin_nanf("") : s[t][i];
+        }
+        lds_barrier();
     }
 
-    if (!p.final_state || !active)
+    if (!p.final_state)
         return;
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
@@ -493,14 +606,37 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(DeltaParams p, in
     }
 }
 
-template <int K>
+template <int K, int TM>
+__global__ __launch_bounds__(kThreads) void delta_chunk_kernel(DeltaParams p, int vblocks, int columns)
+{
+    __shared__ __align__(16) Shared<K, TM> sh;
+    static_assert(sizeof(sh) <= 160 * 1024, "LDS of a compute unit");
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const Chain ch = find_chain(p, vblocks, columns);
+    if (wave >= kStateWaves) {
+        if (ch.tokens > 0) {
+            Producer<K, TM> producer(p, ch, tid - 64 * kStateWaves, wave - kStateWaves);
+            producer.run(sh);
+        }
+    } else if (16 * wave < ch.width) {
+        state_wave<K, TM>(p, ch, sh, tid & 63, wave);
+    } else {
+        // a wave without columns keeps the others' count of barriers: two a tile and two before
+        for (int t0 = -TM; t0 < ch.tokens && ch.tokens > 0; t0 += TM) {
+            lds_barrier();
+            lds_barrier();
+        }
+    }
+}
+
+template <int K, int TM>
 hipError_t launch(const DeltaParams &p, hipStream_t stream)
 {
     const int columns = static_cast<int>(p.V < kColumns ? p.V : kColumns);
     const int64_t vblocks = (p.V + columns - 1) / columns, blocks = p.seqs.N * p.H * vblocks;
     if (!grid_fits(blocks, kThreads))
         return hipErrorInvalidConfiguration;
-    delta_chunk_kernel<K><<<dim3(static_cast<uint32_t>(blocks)), dim3(kThreads), 0, stream>>>(p, static_cast<int>(vblocks), columns);
+    delta_chunk_kernel<K, TM><<<dim3(static_cast<uint32_t>(blocks)), dim3(kThreads), 0, stream>>>(p, static_cast<int>(vblocks), columns);
     return hipGetLastError();
 }
 
@@ -509,9 +645,9 @@ hipError_t launch(const DeltaParams &p, hipStream_t stream)
 hipError_t launch_delta_chunk(const DeltaParams &p, hipStream_t stream)
 {
     switch (p.K) {
-    case 64: return launch<64>(p, stream);
-    case 128: return launch<128>(p, stream);
-    case 256: return launch<256>(p, stream);
+    case 64: return launch<64, 64>(p, stream);
+    case 128: return launch<128, 64>(p, stream);
+    case 256: return launch<256, 32>(p, stream);
     default: return hipErrorInvalidValue;
     }
 }

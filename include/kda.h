@@ -561,8 +561,10 @@ kda_status kda_residual_norm(const kda_residual_norm_args *args, void *stream);
  *
  * A non-finite q reaches its own token's output alone; a non-finite k, v, g or
  * beta reaches outputs of its head (k: its group's heads) from its own token
- * on, never earlier ones, and never another sequence.  Numbers beyond 2^120
- * that the recurrence forms on the way count as non-finite.
+ * on, never earlier ones, and never another sequence.  Numbers on the way that
+ * round to infinity as bf16 (from 3.39e38 on) count as non-finite.  Where the
+ * recurrence itself overflows, which keys no longer than 1 keep it from, up to
+ * 15 tokens before that may be lost, too.
  */
 typedef struct kda_delta_args {
     const void *q;
