@@ -21,13 +21,18 @@
 // Operands.  In v_mfma_f32_16x16x32_bf16 lane (r = lane % 16, g = lane / 16)
 // holds row / column r, slots 8 g .. 8 g + 7, and accumulator register i is row
 // 4 g + i of column r.  Which contraction index a slot stands for is free as
-// long as both operands agree, so with slot 8 g + 4 a + i standing for index 16 a
-// + 4 g + i two accumulators on top of each other are an operand as they stand:
-// S over k, U over tokens, as right factor and, transposed, as left.  K, Q and P
-// lie in LDS in that order, 32 at a time, so that a lane's slots are adjacent.
-// out comes transposed, four adjacent columns of a token to a lane.  In
+// long as both operands agree, so two accumulators on top of each other are an
+// operand as they stand, as right factor and, transposed, as left: S over k, with
+// row 4 g + i of tile 2 e + a standing for k = 32 e + 8 g + 4 a + i, so that K and Q
+// lie in LDS as in memory; and U over tokens, with slot 8 g + 4 a + i standing for
+// token 16 a + 4 g + i of 32, the order in which P lies in LDS.  out comes
+// transposed, four adjacent columns of a token to a lane.  In
 // v_mfma_f32_16x16x4_f32 of the solve, step i takes row 4 g + i: accumulator
 // register i again.
+//
+// Rows in LDS are 8 mod 16 dwords apart: 16 lanes' 16-byte pieces of 16 rows, four
+// times, then take 6 cycles (10 at 4 mod 16, 34 at 0), and what a transposing read
+// takes of K 6 (10 and 6).
 //
 // Numerics.  k, q and v are bf16 and enter as they are.  Of what is fp32, S
 // enters K S and the weighted U enters S as three bf16 parts, which hold all 24
@@ -41,7 +46,7 @@
 // its column are taken for 0, and the column's outputs from there on, and its
 // state, are made NaN.  So is U where it is not finite after all (a solve that
 // overflows by itself: then also tokens of the same 16 before).
-#include <type_traits>
+#include <cstddef>
 
 #include "layer_device.h"
 
@@ -70,10 +75,20 @@ __device__ __forceinline__ u32x2_t lds_tr(uint32_t a)
     return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                                            (__attribute__((address_space(3))) s16x4_t *)(uintptr_t)a));
 }
+template <class T>
+__device__ __forceinline__ T lds_load(uint32_t a)
+{
+    return *(const __attribute__((address_space(3))) T *)(uintptr_t)a;
+}
 __device__ __forceinline__ u32x4_t cat(u32x2_t a, u32x2_t b) { return u32x4_t{a[0], a[1], b[0], b[1]}; }
 __device__ __forceinline__ f32x4_t mfma(u32x4_t a, u32x4_t b, f32x4_t c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+// The same over 16 slots, 4 g .. 4 g + 3 in a lane.
+__device__ __forceinline__ f32x4_t mfma16(u32x2_t a, u32x2_t b, f32x4_t c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4_t, a), __builtin_bit_cast(s16x4_t, b), c, 0, 0, 0);
 }
 // c + a b of 16 x 16 fp32 blocks: a's rows lie over the lanes (four adjacent
 // elements each), b is an accumulator.
@@ -141,24 +156,16 @@ __device__ __forceinline__ double prefix(double x, int lane)
     return x;
 }
 
-// Rows of K and Q in LDS: 16-byte aligned, and apart by what spreads 16 rows'
-// pieces (and what a transposing read takes of K) over the banks.
-template <int K>
-constexpr int kKPitch = K == 64 ? 168 : K + 40;
-template <int K>
-constexpr int kQPitch = K + 8;
-constexpr int kVPitch = 24, kAPitch = 20, kPPitch = 40;
-
 // Lower blocks (b, c), c <= b, one after the other; of P two of them, side by side
-// in the order of the slots.
+// in the order of the slots (of an odd one out the second half is not used).
 __device__ __forceinline__ constexpr int a_block(int b, int c) { return b * (b + 1) / 2 + c; }
 __device__ __forceinline__ constexpr int p_block(int b, int e) { return (b / 2) * (b / 2 + 1) + (b % 2) * (b / 2 + 1) + e; }
 
 template <int K, int TM>
 struct Tile {
-    static constexpr int NB = TM / 16;
-    alignas(16) uint16_t k[TM][kKPitch<K>];
-    alignas(16) uint16_t q[TM][kQPitch<K>];
+    static constexpr int NB = TM / 16, kPitch = K + 16, kAPitch = 24, kPPitch = 48;
+    alignas(16) uint16_t k[TM][kPitch];
+    alignas(16) uint16_t q[TM][kPitch];
     alignas(16) float a[a_block(NB - 1, NB - 1) + 1][16][kAPitch];               // -A below the diagonal, the inverses on it
     alignas(16) uint16_t p[2][p_block(NB - 1, (NB - 1) / 2) + 1][16][kPPitch];  // two parts of P
     // G in two floats, 2^G, 2^(G_last - G), beta; 2^G_last
@@ -169,7 +176,7 @@ struct Tile {
 template <int K, int TM>
 struct Shared {
     Tile<K, TM> tile[2];
-    alignas(16) uint16_t v[kStateWaves][TM][kVPitch];
+    alignas(16) uint16_t v[kStateWaves][TM][16];
 };
 
 // Where a workgroup's chain lies.
@@ -202,14 +209,16 @@ __device__ __forceinline__ Chain find_chain(const DeltaParams &p, int vblocks, i
 // the blocks of A and P, the inverses of A's diagonal blocks.
 template <int K, int TM>
 struct Producer {
-    static constexpr int NB = TM / 16, PK = K / 8, kLoad = TM * PK / (64 * kProducers);
-    static_assert(kLoad >= 1, "whole rounds of loads");
+    static constexpr int NB = TM / 16, PK = K / 8;                 // 16-byte pieces of a row
+    static constexpr int kRows = 64 * kProducers / PK, kLoad = TM / kRows;  // rows loaded at once, and how often
+    static_assert(kLoad >= 1 && kLoad * kRows == TM, "whole rounds of loads");
     const DeltaParams &p;
     const Chain &ch;
     const int tid, lane, r, g, wave;
     float rate, bias;
     const char *kbase, *qbase;
     const uint16_t *gbase, *bbase;
+    uint32_t koff, qoff;  // of a thread's piece of the first rows
     u32x4_t nk[kLoad], nq[kLoad];
     uint32_t ng, nb;
 
@@ -222,18 +231,29 @@ struct Producer {
         qbase = reinterpret_cast<const char *>(p.q + ch.row * p.qb + static_cast<int64_t>(ch.begin) * p.qt + ch.grp * K);
         gbase = p.g + ch.row * p.gb + static_cast<int64_t>(ch.begin) * p.gt + ch.h;
         bbase = p.beta + ch.row * p.bb + static_cast<int64_t>(ch.begin) * p.bt + ch.h;
+        koff = static_cast<uint32_t>(tid / PK) * static_cast<uint32_t>(2 * p.kt) + 16 * (tid % PK);
+        qoff = static_cast<uint32_t>(tid / PK) * static_cast<uint32_t>(2 * p.qt) + 16 * (tid % PK);
     }
 
-    // The tile's rows into registers; rows past the end are zeros.
+    // The tile's rows into registers; rows past the end are the last one, once more.
     __device__ __forceinline__ void load(int t0)
     {
-        const int left = ch.tokens - t0, me = here(tid);
+        const int left = ch.tokens - t0;
         const char *kp = kbase + static_cast<int64_t>(t0) * p.kt * 2, *qp = qbase + static_cast<int64_t>(t0) * p.qt * 2;
+        if (left >= TM) {
 #pragma unroll
-        for (int i = 0; i < kLoad; ++i) {
-            const int piece = me + 64 * kProducers * i, t = piece / PK, c = piece % PK, in = t < left ? t : left - 1;
-            nk[i] = *reinterpret_cast<const u32x4_a2 *>(kp + static_cast<uint32_t>(in) * static_cast<uint32_t>(2 * p.kt) + 16 * c);
-            nq[i] = *reinterpret_cast<const u32x4_a2 *>(qp + static_cast<uint32_t>(in) * static_cast<uint32_t>(2 * p.qt) + 16 * c);
+            for (int i = 0; i < kLoad; ++i) {
+                nk[i] = *reinterpret_cast<const u32x4_a2 *>(kp + static_cast<int64_t>(i * kRows) * p.kt * 2 + koff);
+                nq[i] = *reinterpret_cast<const u32x4_a2 *>(qp + static_cast<int64_t>(i * kRows) * p.qt * 2 + qoff);
+            }
+        } else {
+            const int t = here(tid / PK), c = here(tid % PK);
+#pragma unroll
+            for (int i = 0; i < kLoad; ++i) {
+                const int in = t + kRows * i < left ? t + kRows * i : left - 1;
+                nk[i] = *reinterpret_cast<const u32x4_a2 *>(kp + static_cast<uint32_t>(in) * static_cast<uint32_t>(2 * p.kt) + 16 * c);
+                nq[i] = *reinterpret_cast<const u32x4_a2 *>(qp + static_cast<uint32_t>(in) * static_cast<uint32_t>(2 * p.qt) + 16 * c);
+            }
         }
         if (wave == kProducers - 1) {
             const int in = lane < left ? lane : left - 1;
@@ -241,19 +261,20 @@ struct Producer {
             nb = bbase[static_cast<int64_t>(t0 + in) * p.bt];
         }
     }
+    // And from there into LDS; rows past the end are zeros.
     __device__ __forceinline__ void store(Tile<K, TM> &to, int t0)
     {
-        const int left = ch.tokens - t0, me = here(tid);
+        const int left = ch.tokens - t0, t = tid / PK, c = tid % PK;
+        if (left < TM) {
+#pragma unroll
+            for (int i = 0; i < kLoad; ++i)
+                if (t + kRows * i >= left)
+                    nk[i] = nq[i] = u32x4_t{0, 0, 0, 0};
+        }
 #pragma unroll
         for (int i = 0; i < kLoad; ++i) {
-            // channels 8 m .. 8 m + 7 of 32: two runs of four, in the order of the slots
-            const int piece = me + 64 * kProducers * i, t = piece / PK, c = piece % PK;
-            const int at = 32 * (c / 4) + 16 * (c % 2) + 4 * (c % 4 / 2);
-            const u32x4_t none = {0, 0, 0, 0}, x = t < left ? nk[i] : none, y = t < left ? nq[i] : none;
-            *reinterpret_cast<u32x2_t *>(&to.k[t][at]) = u32x2_t{x[0], x[1]};
-            *reinterpret_cast<u32x2_t *>(&to.k[t][at + 8]) = u32x2_t{x[2], x[3]};
-            *reinterpret_cast<u32x2_t *>(&to.q[t][at]) = u32x2_t{y[0], y[1]};
-            *reinterpret_cast<u32x2_t *>(&to.q[t][at + 8]) = u32x2_t{y[2], y[3]};
+            *reinterpret_cast<u32x4_t *>(&to.k[t + kRows * i][8 * c]) = nk[i];
+            *reinterpret_cast<u32x4_t *>(&to.q[t + kRows * i][8 * c]) = nq[i];
         }
         if (wave == kProducers - 1)
             gates(to, left);
@@ -278,38 +299,56 @@ struct Producer {
         }
     }
     // Blocks (b, c) of A and P: lane r is token 16 b + r, its registers tokens 16 c + 4 g + i before it.
-    template <bool A, bool P>
-    __device__ __forceinline__ void block(Tile<K, TM> &to, int b, int c)
+    struct Products {
+        f32x4_t kk, qk;
+    };
+    template <int b, int c>
+    __device__ __forceinline__ Products products(const Tile<K, TM> &to)
     {
-        f32x4_t kk = {0.0f, 0.0f, 0.0f, 0.0f}, qk = kk;
+        const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+        Products y = {zero, zero};
 #pragma unroll
         for (int e = 0; e < K / 32; ++e) {
             const u32x4_t x = *reinterpret_cast<const u32x4_t *>(&to.k[16 * c + r][32 * e + 8 * g]);
-            if constexpr (A)
-                kk = mfma(x, *reinterpret_cast<const u32x4_t *>(&to.k[16 * b + r][32 * e + 8 * g]), kk);
-            if constexpr (P)
-                qk = mfma(x, *reinterpret_cast<const u32x4_t *>(&to.q[16 * b + r][32 * e + 8 * g]), qk);
+            y.kk = mfma(x, b == c ? x : *reinterpret_cast<const u32x4_t *>(&to.k[16 * b + r][32 * e + 8 * g]), y.kk);
+            y.qk = mfma(x, *reinterpret_cast<const u32x4_t *>(&to.q[16 * b + r][32 * e + 8 * g]), y.qk);
         }
-        const int i = 16 * b + r, j = 16 * c + 4 * g;
-        const float hi = to.g[0][i], lo = to.g[1][i];
-        const f32x4_t hj = *reinterpret_cast<const f32x4_t *>(&to.g[0][j]), lj = *reinterpret_cast<const f32x4_t *>(&to.g[1][j]);
+        return y;
+    }
+    template <int b, int c>
+    __device__ __forceinline__ void finish(Tile<K, TM> &to, const Products &raw)
+    {
+        const float hi = to.g[0][16 * b + r], lo = to.g[1][16 * b + r], strength = -to.beta[16 * b + r];
+        const f32x4_t hj = *reinterpret_cast<const f32x4_t *>(&to.g[0][16 * c + 4 * g]);
+        const f32x4_t lj = *reinterpret_cast<const f32x4_t *>(&to.g[1][16 * c + 4 * g]);
         f32x4_t x, y;
-        const float strength = A ? -to.beta[i] : 0.0f;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const float f = exp2_f32((hi - hj[m]) + (lo - lj[m]));
-            x[m] = j + m < i ? strength * f * kk[m] : 0.0f;
-            y[m] = j + m <= i ? f * qk[m] : 0.0f;
+            x[m] = b > c || 4 * g + m < r ? strength * f * raw.kk[m] : 0.0f;
+            y[m] = b > c || 4 * g + m <= r ? f * raw.qk[m] : 0.0f;
         }
-        if constexpr (A)
-            *reinterpret_cast<f32x4_t *>(&to.a[a_block(b, c)][r][4 * g]) = x;
-        if constexpr (P) {
-            u32x2_t parts[2];
-            split<2>(y, parts);
-            uint16_t *to0 = &to.p[0][p_block(b, c / 2)][r][8 * g + 4 * (c % 2)], *to1 = &to.p[1][p_block(b, c / 2)][r][8 * g + 4 * (c % 2)];
-            *reinterpret_cast<u32x2_t *>(to0) = parts[0];
-            *reinterpret_cast<u32x2_t *>(to1) = parts[1];
-        }
+        u32x2_t parts[2];
+        split<2>(y, parts);
+        *reinterpret_cast<f32x4_t *>(&to.a[a_block(b, c)][r][4 * g]) = x;
+        *reinterpret_cast<u32x2_t *>(&to.p[0][p_block(b, c / 2)][r][8 * g + 4 * (c % 2)]) = parts[0];
+        *reinterpret_cast<u32x2_t *>(&to.p[1][p_block(b, c / 2)][r][8 * g + 4 * (c % 2)]) = parts[1];
+    }
+    // Three blocks at once, their products interleaved.
+    template <int b0, int c0, int b1, int c1, int b2, int c2>
+    __device__ __forceinline__ void three(Tile<K, TM> &to)
+    {
+        const Products x = products<b0, c0>(to), y = products<b1, c1>(to), z = products<b2, c2>(to);
+        finish<b0, c0>(to, x);
+        finish<b1, c1>(to, y);
+        finish<b2, c2>(to, z);
+    }
+    template <int b0, int c0, int b1, int c1>
+    __device__ __forceinline__ void two(Tile<K, TM> &to)
+    {
+        const Products x = products<b0, c0>(to), y = products<b1, c1>(to);
+        finish<b0, c0>(to, x);
+        finish<b1, c1>(to, y);
     }
     // The inverses of the diagonal blocks I + A by forward substitution: lane (g, r)
     // has column r of block g, X_i = e_i - sum_(m < i) A_im X_m.
@@ -337,31 +376,31 @@ struct Producer {
             for (int i = 0; i < 16; ++i) to.a[bl][i][r] = x[i];
         }
     }
+    // A wave's share of them (the first wave inverts, the last one works out the gates).
     __device__ __forceinline__ void blocks(Tile<K, TM> &to)
     {
-        constexpr int below = NB * (NB - 1) / 2;
-        if (wave == 0) {
-#pragma unroll 1
-            for (int b = 0; b < NB; ++b) block<true, false>(to, b, b);
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            invert(to);
-            return;
+        static_assert(NB == 2 || NB == 4, "shares of two or four blocks");
+        if constexpr (NB == 4) {
+            if (wave == 0)
+                two<0, 0, 1, 0>(to);
+            else if (wave == 1)
+                three<1, 1, 2, 0, 3, 0>(to);
+            else if (wave == 2)
+                three<2, 2, 2, 1, 3, 1>(to);
+            else
+                two<3, 2, 3, 3>(to);
+        } else {
+            if (wave == 0)
+                finish<0, 0>(to, products<0, 0>(to));
+            else if (wave == 1)
+                finish<1, 0>(to, products<1, 0>(to));
+            else if (wave == 2)
+                finish<1, 1>(to, products<1, 1>(to));
         }
-#pragma unroll 1
-        for (int i = wave - 1; i < below; i += kProducers - 1) {
-            const int b = i < 1 ? 1 : i < 3 ? 2 : 3;
-            block<true, true>(to, b, i - b * (b - 1) / 2);
-        }
-#pragma unroll 1
-        for (int b = kProducers - 1 - wave; b < NB; b += kProducers - 1) block<false, true>(to, b, b);
     }
     __device__ __forceinline__ void run(Shared<K, TM> &sh)
     {
-        // what P U reads of blocks above the diagonal
-        for (int buf = 0; buf < 2; ++buf) {
-            uint32_t *z = reinterpret_cast<uint32_t *>(sh.tile[buf].p);
-            for (int i = tid; i < static_cast<int>(sizeof(sh.tile[buf].p) / 4); i += 64 * kProducers) z[i] = 0;
-        }
+
         load(0);
         store(sh.tile[0], 0);
         if (TM < ch.tokens)
@@ -369,17 +408,22 @@ struct Producer {
         lds_barrier();
         blocks(sh.tile[0]);
         lds_barrier();
-        int buf = 1;
-        for (int t0 = TM; t0 < ch.tokens; t0 += TM, buf ^= 1) {
-            store(sh.tile[buf], t0);
-            if (t0 + TM < ch.tokens)
-                load(t0 + TM);
+        int buf = 0;
+        for (int t0 = 0; t0 < ch.tokens; t0 += TM, buf ^= 1) {
+            // while the state waves read with K and Q of a tile, its inverses and the next one's rows ...
+            if (wave == 0)
+                invert(sh.tile[buf]);
+            const bool more = t0 + TM < ch.tokens;
+            if (more)
+                store(sh.tile[buf ^ 1], t0 + TM);
+            if (t0 + 2 * TM < ch.tokens)
+                load(t0 + 2 * TM);
             lds_barrier();
-            blocks(sh.tile[buf]);
+            // ... and while they go through the tile, the next one's blocks
+            if (more)
+                blocks(sh.tile[buf ^ 1]);
             lds_barrier();
         }
-        lds_barrier();  // of the last tile
-        lds_barrier();
     }
 };
 
@@ -391,16 +435,17 @@ __device__ __forceinline__ void state_wave(const DeltaParams &p, const Chain &ch
     const int r = lane & 15, g = lane >> 4, col = ch.col0 + 16 * wave;
     const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
 
-    // the state: tile t's register i is k = 16 t + 4 g + i of column r
+    // the state: register i of tile 2 e + a is k = 32 e + 8 g + 4 a + i of column r
     f32x4_t s[KT];
-    const int64_t slab = ((ch.n * p.H + ch.h) * p.V + col + r) * K + 4 * g;
+    const int64_t slab = ((ch.n * p.H + ch.h) * p.V + col + r) * K + 8 * g;
+    const auto place = [&](int t) { return slab + 32 * (t / 2) + 4 * (t % 2); };
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
         s[t] = zero;
         if (p.init_kind == kFp32) {
-            s[t] = *reinterpret_cast<const f32x4_t *>(static_cast<const float *>(p.init_state) + slab + 16 * t);
+            s[t] = *reinterpret_cast<const f32x4_t *>(static_cast<const float *>(p.init_state) + place(t));
         } else if (p.init_kind == kBf16) {
-            const u32x2_t v = *reinterpret_cast<const u32x2_t *>(static_cast<const uint16_t *>(p.init_state) + slab + 16 * t);
+            const u32x2_t v = *reinterpret_cast<const u32x2_t *>(static_cast<const uint16_t *>(p.init_state) + place(t));
             s[t] = f32x4_t{lo_f32(v[0]), hi_f32(v[0]), lo_f32(v[1]), hi_f32(v[1])};
         }
     }
@@ -427,7 +472,15 @@ __device__ __forceinline__ void state_wave(const DeltaParams &p, const Chain &ch
     }
     int buf = 0;
     for (int t0 = 0; t0 < ch.tokens; t0 += TM, buf ^= 1) {
-        const Tile<K, TM> &tl = sh.tile[buf];
+        // places in the tile: a base for each pattern of lanes, and constants
+        using T = Tile<K, TM>;
+        const uint32_t base = lds_addr(&sh.tile[buf]), row = base + 2 * T::kPitch * r + 16 * g;
+        const uint32_t ap = base + offsetof(T, a) + 4 * T::kAPitch * r + 16 * g;  // rows of A and P are equally long
+        static_assert(4 * T::kAPitch == 2 * T::kPPitch, "");
+        const uint32_t four = base + offsetof(T, decay) + 16 * g, one = base + offsetof(T, decay) + 4 * r;
+        constexpr uint32_t kQ = offsetof(T, q), kABlock = sizeof(T::a[0]), kP = offsetof(T, p) - offsetof(T, a), kPart = sizeof(T::p[0]),
+                           kPBlock = sizeof(T::p[0][0]), kBeta = offsetof(T, beta) - offsetof(T, decay),
+                           kLeft = offsetof(T, left) - offsetof(T, decay), kTotal = offsetof(T, total) - offsetof(T, decay);
         const int left = ch.tokens - t0, me = here(lane);
 #pragma unroll
         for (int i = 0; i < kLoad; ++i) {
@@ -440,39 +493,52 @@ __device__ __forceinline__ void state_wave(const DeltaParams &p, const Chain &ch
         // K S and Q S: rows are tokens of K S, columns of (Q S)^T
         f32x4_t u[NB], o[NB];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) u[b] = o[b] = zero;
-#pragma unroll
         for (int e = 0; e < KSTEP; ++e) {
             u32x2_t x[3], y[3];
             split<3>(s[2 * e], x);
             split<3>(s[2 * e + 1], y);
             const u32x4_t s0 = cat(x[0], y[0]), s1 = cat(x[1], y[1]), s2 = cat(x[2], y[2]);
+            // accumulators in turn, so that none waits for its own last product
+            u32x4_t kr[NB], qr[NB];
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const u32x4_t kr = *reinterpret_cast<const u32x4_t *>(&tl.k[16 * b + r][32 * e + 8 * g]);
-                const u32x4_t qr = *reinterpret_cast<const u32x4_t *>(&tl.q[16 * b + r][32 * e + 8 * g]);
-                u[b] = mfma(kr, s0, u[b]);
-                o[b] = mfma(s0, qr, o[b]);
-                u[b] = mfma(kr, s1, u[b]);
-                o[b] = mfma(s1, qr, o[b]);
-                u[b] = mfma(kr, s2, u[b]);
+                kr[b] = lds_load<u32x4_t>(row + 32 * T::kPitch * b + 64 * e);
+                qr[b] = lds_load<u32x4_t>(row + kQ + 32 * T::kPitch * b + 64 * e);
             }
-            fence();
+#pragma unroll
+            for (int b = 0; b < NB; ++b) u[b] = mfma(kr[b], s0, e > 0 ? u[b] : zero);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) o[b] = mfma(s0, qr[b], e > 0 ? o[b] : zero);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) u[b] = mfma(kr[b], s1, u[b]);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) o[b] = mfma(s1, qr[b], o[b]);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) u[b] = mfma(kr[b], s2, u[b]);
+        }
+        // what the residual takes is there already
+        const uint32_t vaddr = lds_addr(&sh.v[wave][here(lane) / 4][4 * (here(lane) & 3)]);  // 4 g + r / 4
+        u32x2_t vr[NB];
+        f32x4_t decay[NB], beta[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            vr[b] = lds_tr(vaddr + 512 * b);
+            decay[b] = lds_load<f32x4_t>(four + 64 * b);
+            beta[b] = lds_load<f32x4_t>(four + kBeta + 64 * b);
         }
         lds_barrier();
 
         // beta (V - 2^G K S)
-        const uint32_t vaddr = lds_addr(&sh.v[wave][here(lane) / 4][4 * (here(lane) & 3)]);  // 4 g + r / 4
+        f32x4_t inv[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) inv[b] = lds_load<f32x4_t>(ap + kABlock * a_block(b, b));
         float fine[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            const u32x2_t vr = lds_tr(vaddr + 32 * b * kVPitch);
-            const f32x4_t d = *reinterpret_cast<const f32x4_t *>(&tl.decay[16 * b + 4 * g]);
-            const f32x4_t beta = *reinterpret_cast<const f32x4_t *>(&tl.beta[16 * b + 4 * g]);
-            const f32x4_t v = {lo_f32(vr[0]), hi_f32(vr[0]), lo_f32(vr[1]), hi_f32(vr[1])};
+            const f32x4_t v = {lo_f32(vr[b][0]), hi_f32(vr[b][0]), lo_f32(vr[b][1]), hi_f32(vr[b][1])};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                u[b][i] = beta[i] * fmaf(-d[i], u[b][i], v[i]);
+                u[b][i] = beta[b][i] * fmaf(-decay[b][i], u[b][i], v[i]);
                 fine[i & 1] = fmaf(u[b][i], 0.0f, fine[i & 1]);
             }
         }
@@ -502,17 +568,20 @@ __device__ __forceinline__ void state_wave(const DeltaParams &p, const Chain &ch
         bool poisoned = __any(fine[0] + fine[1] != 0.0f);
         if (poisoned)
             scrub();
-        fence();
         // U, block by block
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             if (poisoned)
                 clear(b);  // rows of A may not be finite, either
-            u[b] = mfma_f32(*reinterpret_cast<const f32x4_t *>(&tl.a[a_block(b, b)][r][4 * g]), u[b], zero);
+            u[b] = mfma_f32(inv[b], u[b], zero);
+            // step by step over the blocks below, so that none waits for its own last product
+            f32x4_t below[NB];
 #pragma unroll
-            for (int c = b + 1; c < NB; ++c)
-                u[c] = mfma_f32(*reinterpret_cast<const f32x4_t *>(&tl.a[a_block(c, b)][r][4 * g]), u[b], u[c]);
-            fence();
+            for (int c = b + 1; c < NB; ++c) below[c] = lds_load<f32x4_t>(ap + kABlock * a_block(c, b));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = b + 1; c < NB; ++c) u[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(below[c][i], u[b][i], u[c], 0, 0, 0);
         }
         u32x2_t up[NB][2];
         uint32_t most = 0;
@@ -527,25 +596,28 @@ __device__ __forceinline__ void state_wave(const DeltaParams &p, const Chain &ch
 #pragma unroll
             for (int b = 0; b < NB; ++b) split<2>(u[b], up[b]);
         }
-        fence();
 
         // out
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            o[b] *= tl.decay[16 * b + r];
+            o[b] *= lds_load<float>(one + 64 * b);
 #pragma unroll
             for (int e = 0; e <= b / 2; ++e) {
-                const u32x2_t none = {0, 0};
-                const bool two = 2 * e + 1 <= b;
-                const u32x4_t u0 = cat(up[2 * e][0], two ? up[2 * e + 1][0] : none), u1 = cat(up[2 * e][1], two ? up[2 * e + 1][1] : none);
-                const u32x4_t p0 = *reinterpret_cast<const u32x4_t *>(&tl.p[0][p_block(b, e)][r][8 * g]);
-                const u32x4_t p1 = *reinterpret_cast<const u32x4_t *>(&tl.p[1][p_block(b, e)][r][8 * g]);
-                o[b] = mfma(u0, p0, o[b]);
-                o[b] = mfma(u1, p0, o[b]);
-                o[b] = mfma(u0, p1, o[b]);
+                const uint32_t at = ap + kP + kPBlock * p_block(b, e);
+                if (2 * e + 1 <= b) {
+                    const u32x4_t p0 = lds_load<u32x4_t>(at), p1 = lds_load<u32x4_t>(at + kPart);
+                    const u32x4_t u0 = cat(up[2 * e][0], up[2 * e + 1][0]), u1 = cat(up[2 * e][1], up[2 * e + 1][1]);
+                    o[b] = mfma(u0, p0, o[b]);
+                    o[b] = mfma(u1, p0, o[b]);
+                    o[b] = mfma(u0, p1, o[b]);
+                } else {
+                    const u32x2_t p0 = lds_load<u32x2_t>(at), p1 = lds_load<u32x2_t>(at + kPart);
+                    o[b] = mfma16(up[2 * e][0], p0, o[b]);
+                    o[b] = mfma16(up[2 * e][1], p0, o[b]);
+                    o[b] = mfma16(up[2 * e][0], p1, o[b]);
+                }
             }
             o[b] *= p.scale;
-            fence();
         }
         if (poisoned) {
 #pragma unroll
@@ -567,18 +639,17 @@ __device__ __forceinline__ void state_wave(const DeltaParams &p, const Chain &ch
         u32x2_t w[NB][3];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            const f32x4_t weight = *reinterpret_cast<const f32x4_t *>(&tl.left[16 * b + 4 * g]);
-            split<3>(u[b] * weight, w[b]);
+            split<3>(u[b] * lds_load<f32x4_t>(four + kLeft + 64 * b), w[b]);
         }
-        const float total = tl.total;
-        const uint32_t kaddr = lds_addr(&tl.k[here(lane) / 4][8 * (here(lane) & 3)]);
+        const float total = lds_load<float>(base + offsetof(T, decay) + kTotal);
+        const uint32_t kaddr = base + 2 * T::kPitch * (here(lane) / 4) + 16 * (here(lane) & 3);
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
             s[t] *= total;
 #pragma unroll
             for (int e = 0; e < NB / 2; ++e) {
-                const uint32_t at = kaddr + 2 * (32 * (t / 2) + 4 * (t % 2)) + 2 * 32 * e * kKPitch<K>;
-                const u32x4_t kr = cat(lds_tr(at), lds_tr(at + 2 * 16 * kKPitch<K>));
+                const uint32_t at = kaddr + 2 * (32 * (t / 2) + 4 * (t % 2)) + 64 * T::kPitch * e;
+                const u32x4_t kr = cat(lds_tr(at), lds_tr(at + 32 * T::kPitch));
 #pragma unroll
                 for (int k = 0; k < 3; ++k) s[t] = mfma(kr, cat(w[2 * e][k], w[2 * e + 1][k]), s[t]);
             }
@@ -599,9 +670,9 @@ __device__ __forceinline__ void state_wave(const DeltaParams &p, const Chain &ch
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
         if (p.final_kind == kFp32)
-            *reinterpret_cast<f32x4_t *>(static_cast<float *>(p.final_state) + slab + 16 * t) = s[t];
+            *reinterpret_cast<f32x4_t *>(static_cast<float *>(p.final_state) + place(t)) = s[t];
         else
-            *reinterpret_cast<u32x2_t *>(static_cast<uint16_t *>(p.final_state) + slab + 16 * t) =
+            *reinterpret_cast<u32x2_t *>(static_cast<uint16_t *>(p.final_state) + place(t)) =
                 u32x2_t{pack_bf16x2(s[t][0], s[t][1]), pack_bf16x2(s[t][2], s[t][3])};
     }
 }
