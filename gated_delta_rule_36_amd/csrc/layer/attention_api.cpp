@@ -240,17 +240,30 @@ kda_status check_attention_sizes(const kda_attention_args &a)
     return KDA_OK;
 }
 
-// Splits of every sequence's tokens: as many as give each compute unit four
-// workgroups, of at least kAttentionSplitTokens tokens.
+// Tokens a split: the same for all sequences, so that waves do the same work
+// however lengths differ, and as many splits as make kTarget waves if every
+// sequence were as long as its table allows.  Short contexts go in one split,
+// which needs neither a workspace nor a second launch; a workgroup shares it.
+constexpr int64_t kTarget = 32768, kFewest = 4 * kAttentionTile, kShared = 1024;
+int64_t longest(const kda_attention_args &a)
+{
+    const int64_t room = a.table_width * a.page_size;
+    return a.window > 0 && a.window < room ? a.window : room;
+}
+int64_t attention_chunk(const kda_attention_args &a)
+{
+    const int64_t most = longest(a);
+    if (most <= kShared)
+        return kShared;
+    const int64_t pairs = a.N * a.Hk * ((a.Hq / a.Hk + kAttentionRows - 1) / kAttentionRows);
+    const int64_t parts = std::max(int64_t(1), kTarget / std::max(int64_t(1), pairs));
+    const int64_t chunk = std::max((most + parts - 1) / parts, kFewest);
+    return (chunk + kAttentionTile - 1) / kAttentionTile * kAttentionTile;
+}
 int64_t attention_splits(const kda_attention_args &a)
 {
-    constexpr int64_t kTarget = 1024;
-    const int64_t pairs = a.N * a.Hk * ((a.Hq / a.Hk + kAttentionRows - 1) / kAttentionRows);
-    int64_t most = a.table_width * a.page_size;
-    if (a.window > 0 && a.window < most)
-        most = a.window;
-    const int64_t room = (most + kAttentionSplitTokens - 1) / kAttentionSplitTokens;
-    return std::max(int64_t(1), std::min(room, kTarget / std::max(int64_t(1), pairs)));
+    const int64_t chunk = attention_chunk(a);
+    return std::max(int64_t(1), (longest(a) + chunk - 1) / chunk);
 }
 
 int64_t attention_workspace(const kda_attention_args &a)
@@ -329,6 +342,8 @@ extern "C" kda_status kda_paged_attention(const kda_attention_args *args, void *
         p.page_mul = static_cast<uint32_t>(((uint64_t(1) << (32 + p.page_shift)) + p.page_size - 1) / p.page_size);
     }
     p.splits = attention_splits(a);
+    p.chunk = static_cast<int>(attention_chunk(a));
+    p.shared = p.splits == 1 && longest(a) <= kShared;
     p.scale = static_cast<float>(a.scale);
     if (p.splits > 1) {
         p.part = static_cast<float *>(a.workspace);

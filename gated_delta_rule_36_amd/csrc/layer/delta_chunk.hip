@@ -700,10 +700,25 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(DeltaParams p, in
     }
 }
 
+// Columns a workgroup takes.  Its tile takes 14000 cycles with eight state
+// waves, two a SIMD, and 7000 to 9000 with one to four, so few chains are spread:
+// as thinly as 256 workgroups, one a compute unit, allow.  Of packed sequences,
+// whose lengths differ, 512: the second half starts where short ones end.  Of
+// one of 8191 tokens with 12 heads of 64 x 96 128 columns take 567 us, 48 417, 32
+// 404 and 16 391; of 19595 tokens in 8 sequences with 32 heads of 128 x 128 128
+// take 430, 64 396 and 32 638; of 8 x 16384 128 take 1690, 64 2070.
+int columns_of(const DeltaParams &p)
+{
+    const int64_t chains = p.seqs.N * p.H, most = p.seqs.cu ? 512 : 256;
+    int columns = 16;
+    while (columns < kColumns && columns < p.V && chains * ((p.V + columns - 1) / columns) > most) columns *= 2;
+    return columns < p.V ? columns : static_cast<int>(p.V);
+}
+
 template <int K, int TM>
 hipError_t launch(const DeltaParams &p, hipStream_t stream)
 {
-    const int columns = static_cast<int>(p.V < kColumns ? p.V : kColumns);
+    const int columns = columns_of(p);
     const int64_t vblocks = (p.V + columns - 1) / columns, blocks = p.seqs.N * p.H * vblocks;
     if (!grid_fits(blocks, kThreads))
         return hipErrorInvalidConfiguration;

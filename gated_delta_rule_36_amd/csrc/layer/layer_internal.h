@@ -216,15 +216,16 @@ struct AttentionParams {
     uint32_t page_size, page_mul;  // t / page_size = umulhi(t, page_mul) >> page_shift for t < 2^31 (page_size > 1)
     int page_shift;
     int64_t splits;
+    int chunk;    // tokens a split
+    bool shared;  // a workgroup's waves share a split
     float scale;
     // of several splits: their unnormalised outputs [N, Hq, splits, D] and
     // (maximum, sum) [N, Hq, splits, 2]
     float *part, *stats;
 };
 constexpr int64_t kAttentionMaxD = 256;
-// Query heads of a key head that a workgroup takes, and the fewest tokens that
-// are worth a workgroup of their own.
-constexpr int64_t kAttentionRows = 16, kAttentionSplitTokens = 256;
+// Query heads of a key head that a wave takes, and tokens at a time.
+constexpr int64_t kAttentionRows = 16, kAttentionTile = 32;
 hipError_t launch_paged_attention(const AttentionParams &p, hipStream_t stream);
 
 }  // namespace layer

@@ -82,10 +82,10 @@ __device__ __forceinline__ float column_sum(float x)
     return __uint_as_float(r0) + __uint_as_float(r1);
 }
 
-// The visible tokens [first, first + count) of a sequence, and the tokens a
-// split takes; splits from `used` on have none.
+// The visible tokens [first, first + count) of a sequence; its splits from `used`
+// on have none.
 struct Visible {
-    int first, count, chunk, used;
+    int first, count, used;
 };
 __device__ __forceinline__ Visible visible(const AttentionParams &p, int64_t n)
 {
@@ -96,45 +96,41 @@ __device__ __forceinline__ Visible visible(const AttentionParams &p, int64_t n)
     Visible v;
     v.first = static_cast<int>(first);
     v.count = static_cast<int>(length - first);
-    const int splits = static_cast<int>(p.splits);
-    int chunk = (v.count + splits - 1) / splits;
-    chunk = chunk < static_cast<int>(kAttentionSplitTokens) ? static_cast<int>(kAttentionSplitTokens) : chunk;
-    v.chunk = (chunk + kWaves * TOK - 1) / (kWaves * TOK) * (kWaves * TOK);
-    v.used = (v.count + v.chunk - 1) / v.chunk;
+    v.used = static_cast<int>((static_cast<uint32_t>(v.count) + static_cast<uint32_t>(p.chunk) - 1) / static_cast<uint32_t>(p.chunk));
     return v;
 }
 
-template <int KS>
-struct Shared {
-    static constexpr int D = 32 * KS, kPitch = D + 16, kOutPitch = D + 4;
-    union {
-        alignas(16) uint16_t v[kWaves][TOK][kPitch];
-        alignas(16) float out[kWaves][ROWS][kOutPitch];
-    };
-    float top[kWaves][ROWS], sum[kWaves][ROWS];
-};
-
-template <int KS>
-__global__ __launch_bounds__(kThreads) void paged_attention_kernel(AttentionParams p, int row_tiles)
+// SHARED: a workgroup's waves share its (sequence, key head, split) and join in
+// LDS; otherwise each has its own.  KS steps of 32 channels; a head of D channels
+// half fills the last one, or all of it.
+template <int KS, bool SHARED>
+__global__ __launch_bounds__(kThreads, KS <= 4 ? 3 : KS <= 6 ? 2 : 1) void paged_attention_kernel(AttentionParams p, int row_tiles, int64_t items)
 {
-    constexpr int D = Shared<KS>::D, kPitch = Shared<KS>::kPitch;
-    __shared__ Shared<KS> sh;
+    constexpr int D = 32 * KS, kPitch = D + 16, kOutPitch = D + 4;
+    __shared__ union {
+        alignas(16) uint16_t v[kWaves][TOK][kPitch];
+        alignas(16) float out[SHARED ? kWaves : 1][ROWS][kOutPitch];
+    } sh;
+    __shared__ float shared_top[kWaves][ROWS], shared_sum[kWaves][ROWS];
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    // consecutive workgroups: the key heads of a split, whose rows lie side by side
-    uint32_t at = blockIdx.x;
-    const int hk = at % static_cast<uint32_t>(p.Hk);
-    at /= static_cast<uint32_t>(p.Hk);
+    // consecutive items: the key heads of a split, whose rows lie side by side
+    if (!SHARED && static_cast<int64_t>(blockIdx.x) * kWaves + wave >= items)
+        return;
+    uint32_t at = SHARED ? blockIdx.x : blockIdx.x * kWaves + wave;
     const int ht = at % static_cast<uint32_t>(row_tiles);
     at /= static_cast<uint32_t>(row_tiles);
+    const int hk = at % static_cast<uint32_t>(p.Hk);
+    at /= static_cast<uint32_t>(p.Hk);
     const int split = at % static_cast<uint32_t>(p.splits);
     const int64_t n = at / static_cast<uint32_t>(p.splits);
+    constexpr int kStep = SHARED ? kWaves * TOK : TOK;
     const Visible vis = visible(p, n);
     if (split > 0 && split >= vis.used)
         return;
-    const int64_t from = static_cast<int64_t>(vis.first) + static_cast<int64_t>(split) * vis.chunk;
+    const int64_t from = static_cast<int64_t>(vis.first) + static_cast<int64_t>(split) * p.chunk;
     const int64_t last = static_cast<int64_t>(vis.first) + vis.count;
-    const int t0 = static_cast<int>(from), t1 = static_cast<int>(last < from + vis.chunk ? last : from + vis.chunk);
+    const int t0 = static_cast<int>(from), t1 = static_cast<int>(last < from + p.chunk ? last : from + p.chunk);
     const int group = static_cast<int>(p.Hq / p.Hk), width = static_cast<int>(p.D);
     const int row0 = ht * ROWS, rows = group - row0 < ROWS ? group - row0 : ROWS;
 
@@ -152,13 +148,15 @@ __global__ __launch_bounds__(kThreads) void paged_attention_kernel(AttentionPara
     const auto page_index = [&](int t) {
         return p.page_size == 1 ? static_cast<uint32_t>(t) : __umulhi(static_cast<uint32_t>(t), p.page_mul) >> p.page_shift;
     };
-    // A lane's tokens of a tile are r and 16 + r; their pages are looked up a tile ahead.
+    // A lane's tokens of a tile are r and 16 + r; their pages are looked up a tile
+    // ahead, as far as the table goes.
+    const int room = static_cast<int>(p.width * static_cast<int64_t>(p.page_size));
     int page[2];
     const auto look_up = [&](int base) {
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
             const int t = base + 16 * a + r;
-            page[a] = t < t1 ? table[page_index(t)] : -1;
+            page[a] = t < room ? table[page_index(t)] : -1;
         }
     };
     // Of a last step that the head only half fills, the lanes past it read its
@@ -169,7 +167,7 @@ __global__ __launch_bounds__(kThreads) void paged_attention_kernel(AttentionPara
     uint32_t seen = 0;  // bit t: token t of the tile is visible
     const auto load_half = [&](int t, int pg, u32x4_t (&kx)[KS], u32x4_t (&vx)[KS]) {
         const u32x4_t none = {0, 0, 0, 0};
-        const bool in = pg >= 0 && pg < p.pages;
+        const bool in = t < t1 && pg >= 0 && pg < p.pages;
 #pragma unroll
         for (int s = 0; s < KS; ++s) kx[s] = vx[s] = none;
         if (in) {
@@ -196,13 +194,13 @@ __global__ __launch_bounds__(kThreads) void paged_attention_kernel(AttentionPara
     const float scale2 = p.scale * kLog2eF;
     const uint32_t vaddr = lds_addr(&sh.v[wave][4 * g + r / 4][4 * (r & 3)]);
 
-    int base = t0 + wave * TOK;
+    int base = t0 + (SHARED ? wave * TOK : 0);
     if (base < t1) {
         look_up(base);
         load(base);
-        look_up(base + kWaves * TOK);
+        look_up(base + kStep);
     }
-    for (; base < t1; base += kWaves * TOK) {
+    for (; base < t1; base += kStep) {
         f32x4_t score0 = {0.0f, 0.0f, 0.0f, 0.0f}, score1 = score0;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
@@ -217,9 +215,9 @@ __global__ __launch_bounds__(kThreads) void paged_attention_kernel(AttentionPara
             for (int s = 0; s < KS; ++s)
                 *reinterpret_cast<u32x4_t *>(&sh.v[wave][16 * a + r][32 * s + 8 * g]) = vt[a][s];
         const uint32_t mine = seen >> (4 * g);
-        if (base + kWaves * TOK < t1) {
-            load(base + kWaves * TOK);
-            look_up(base + 2 * kWaves * TOK);
+        if (base + kStep < t1) {
+            load(base + kStep);
+            look_up(base + 2 * kStep);
         }
         float most = -__builtin_inff(), x2[8];
 #pragma unroll
@@ -257,65 +255,78 @@ __global__ __launch_bounds__(kThreads) void paged_attention_kernel(AttentionPara
         asm volatile("" ::: "memory");
     }
 
-    // the four waves' results, one after the other in LDS
     sum = column_sum(sum);
-    __syncthreads();
-    if (g == 0) {
-        sh.top[wave][r] = top;
-        sh.sum[wave][r] = sum;
-    }
+    if constexpr (SHARED) {
+        // the waves' results, one after the other in LDS; each goes on with a quarter of the channels
+        __syncthreads();
+        if (g == 0) {
+            shared_top[wave][r] = top;
+            shared_sum[wave][r] = sum;
+        }
 #pragma unroll
-    for (int d = 0; d < 2 * KS; ++d)
-        *reinterpret_cast<f32x4_t *>(&sh.out[wave][r][16 * d + 4 * g]) = o[d];
-    __syncthreads();
-    const bool whole = vis.used <= 1;
-    for (int i = tid; i < rows * (D / 4); i += kThreads) {
-        const int row = i / (D / 4), d = 4 * (i - row * (D / 4));
-        float most = sh.top[0][row];
+        for (int d = 0; d < 2 * KS; ++d) *reinterpret_cast<f32x4_t *>(&sh.out[wave][r][16 * d + 4 * g]) = o[d];
+        __syncthreads();
+        float most = shared_top[0][r];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) most = fmaxf(most, sh.top[w][row]);
+        for (int w = 1; w < kWaves; ++w) most = fmaxf(most, shared_top[w][r]);
         const float from_top = most == -__builtin_inff() ? 0.0f : most;
-        float total = 0.0f;
-        f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
+        float f[kWaves];
+        top = most;
+        sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-            const float f = exp2_f32(sh.top[w][row] - from_top);
-            total = fmaf(f, sh.sum[w][row], total);
-            x += f * *reinterpret_cast<const f32x4_t *>(&sh.out[w][row][d]);
+            f[w] = exp2_f32(shared_top[w][r] - from_top);
+            sum = fmaf(f[w], shared_sum[w][r], sum);
         }
-        const int64_t head = n * p.Hq + static_cast<int64_t>(hk) * group + row0 + row;
-        if (whole) {
-            const float f = total == 0.0f ? 0.0f : 1.0f / total;
-            if (d < width)
-                *reinterpret_cast<u32x2_t *>(p.out + head * p.D + d) =
-                    u32x2_t{pack_bf16x2(x[0] * f, x[1] * f), pack_bf16x2(x[2] * f, x[3] * f)};
-            if (d == 0 && p.lse)
-                p.lse[head] = total == 0.0f ? -__builtin_inff() : (from_top + log2f(total)) * kLn2F;
-        } else {
-            const int64_t slot = head * p.splits + split;
-            if (d < width)
-                *reinterpret_cast<f32x4_t *>(p.part + slot * p.D + d) = x;
-            if (d == 0) {
-                p.stats[2 * slot] = most;
-                p.stats[2 * slot + 1] = total;
+#pragma unroll
+        for (int d = 0; d < 2 * KS; ++d)
+            if ((d & (kWaves - 1)) == wave) {
+                o[d] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) o[d] += f[w] * *reinterpret_cast<const f32x4_t *>(&sh.out[w][r][16 * d + 4 * g]);
             }
+    }
+    const auto mine = [&](int d) { return 16 * d < width && (!SHARED || (d & (kWaves - 1)) == wave); };
+    const bool first = g == 0 && (!SHARED || wave == 0);
+    if (r >= rows)
+        return;
+    const int64_t head = n * p.Hq + static_cast<int64_t>(hk) * group + row0 + r;
+    if (vis.used <= 1) {
+        const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+        for (int d = 0; d < 2 * KS; ++d)
+            if (mine(d))
+                *reinterpret_cast<u32x2_t *>(p.out + head * p.D + 16 * d + 4 * g) =
+                    u32x2_t{pack_bf16x2(o[d][0] * f, o[d][1] * f), pack_bf16x2(o[d][2] * f, o[d][3] * f)};
+        if (first && p.lse)
+            p.lse[head] = sum == 0.0f ? -__builtin_inff() : (top + log2f(sum)) * kLn2F;
+    } else {
+        const int64_t slot = head * p.splits + split;
+#pragma unroll
+        for (int d = 0; d < 2 * KS; ++d)
+            if (mine(d))
+                *reinterpret_cast<f32x4_t *>(p.part + slot * p.D + 16 * d + 4 * g) = o[d];
+        if (first) {
+            p.stats[2 * slot] = top;
+            p.stats[2 * slot + 1] = sum;
         }
     }
 }
 
-// Joins the splits of a row (one workgroup): lanes of four channels, the
-// splits dealt over the groups of lanes.
-constexpr int kJoinThreads = 256;
-__global__ __launch_bounds__(kJoinThreads) void paged_attention_join_kernel(AttentionParams p, int lanes)
+// Joins the splits of a row: a workgroup for every 32 channels, lanes of four
+// channels, the splits dealt over the 32 groups of lanes.
+constexpr int kJoinThreads = 256, kJoinLanes = 8, kJoinGroups = kJoinThreads / kJoinLanes;
+__global__ __launch_bounds__(kJoinThreads) void paged_attention_join_kernel(AttentionParams p, int parts)
 {
-    __shared__ __align__(16) float part[kJoinThreads][4];
-    __shared__ float shared_sum[kJoinThreads], shared_top[kJoinThreads / 64];
-    const int64_t head = blockIdx.x, n = head / p.Hq;
-    const Visible vis = visible(p, n);
+    __shared__ __align__(16) float part[kJoinGroups][4 * kJoinLanes];
+    __shared__ float shared_sum[kJoinGroups], shared_top[kJoinThreads / 64];
+    const uint32_t head = blockIdx.x / static_cast<uint32_t>(parts), at = blockIdx.x - head * static_cast<uint32_t>(parts);
+    const Visible vis = visible(p, head / static_cast<uint32_t>(p.Hq));
     if (vis.used <= 1)
         return;
-    const int tid = threadIdx.x;
-    const float *stats = p.stats + 2 * head * p.splits;
+    const int tid = threadIdx.x, grp = tid / kJoinLanes, l = tid % kJoinLanes, d = 4 * kJoinLanes * static_cast<int>(at) + 4 * l;
+    const bool here = d < p.D;
+    const float *stats = p.stats + 2 * head * p.splits, *src = p.part + head * p.splits * p.D + (here ? d : 0);
     float most = -__builtin_inff();
     for (int s = tid; s < vis.used; s += kJoinThreads) most = fmaxf(most, stats[2 * s]);
     for (int m = 32; m > 0; m >>= 1) most = fmaxf(most, __shfl_xor(most, m));
@@ -325,26 +336,23 @@ __global__ __launch_bounds__(kJoinThreads) void paged_attention_join_kernel(Atte
     for (int w = 0; w < kJoinThreads / 64; ++w) most = fmaxf(most, shared_top[w]);
     const float from_top = most == -__builtin_inff() ? 0.0f : most;
 
-    const int groups = kJoinThreads / lanes, grp = tid / lanes, d = 4 * (tid - grp * lanes);
     f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
     float total = 0.0f;
-    if (grp < groups && d < p.D) {
-        const float *src = p.part + head * p.splits * p.D + d;
 #pragma unroll 4
-        for (int s = grp; s < vis.used; s += groups) {
-            const float f = exp2_f32(stats[2 * s] - from_top);
-            total = fmaf(f, stats[2 * s + 1], total);
-            x += f * *reinterpret_cast<const f32x4_t *>(src + s * p.D);
-        }
+    for (int s = grp; s < vis.used; s += kJoinGroups) {
+        const float f = exp2_f32(stats[2 * s] - from_top);
+        total = fmaf(f, stats[2 * s + 1], total);
+        x += f * *reinterpret_cast<const f32x4_t *>(src + s * p.D);
     }
-    *reinterpret_cast<f32x4_t *>(part[tid]) = x;
-    shared_sum[tid] = total;
+    *reinterpret_cast<f32x4_t *>(&part[grp][4 * l]) = x;
+    if (l == 0)
+        shared_sum[grp] = total;
     __syncthreads();
-    if (grp != 0 || d >= p.D)
+    if (tid >= kJoinLanes || !here)
         return;
-    for (int k = 1; k < groups; ++k) {
-        x += *reinterpret_cast<const f32x4_t *>(part[k * lanes + tid]);
-        total += shared_sum[k * lanes + tid];
+    for (int k = 1; k < kJoinGroups; ++k) {
+        x += *reinterpret_cast<const f32x4_t *>(&part[k][4 * l]);
+        total += shared_sum[k];
     }
     const float f = total == 0.0f ? 0.0f : 1.0f / total;
     *reinterpret_cast<u32x2_t *>(p.out + head * p.D + d) =
@@ -357,15 +365,20 @@ template <int KS>
 hipError_t launch(const AttentionParams &p, hipStream_t stream)
 {
     const int64_t row_tiles = (p.Hq / p.Hk + ROWS - 1) / ROWS;
-    const int64_t blocks = p.N * p.splits * row_tiles * p.Hk;
-    if (!grid_fits(blocks, kThreads) || !grid_fits(p.N * p.Hq, kJoinThreads))
+    const int64_t items = p.N * p.splits * row_tiles * p.Hk, blocks = p.shared ? items : (items + kWaves - 1) / kWaves;
+    const int64_t parts = (p.D + 4 * kJoinLanes - 1) / (4 * kJoinLanes);
+    if (!grid_fits(blocks, kThreads) || !grid_fits(p.N * p.Hq * parts, kJoinThreads))
         return hipErrorInvalidConfiguration;
-    paged_attention_kernel<KS><<<dim3(static_cast<uint32_t>(blocks)), dim3(kThreads), 0, stream>>>(p, static_cast<int>(row_tiles));
+    const dim3 grid(static_cast<uint32_t>(blocks));
+    if (p.shared)
+        paged_attention_kernel<KS, true><<<grid, dim3(kThreads), 0, stream>>>(p, static_cast<int>(row_tiles), items);
+    else
+        paged_attention_kernel<KS, false><<<grid, dim3(kThreads), 0, stream>>>(p, static_cast<int>(row_tiles), items);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1)
         return e;
-    paged_attention_join_kernel<<<dim3(static_cast<uint32_t>(p.N * p.Hq)), dim3(kJoinThreads), 0, stream>>>(
-        p, static_cast<int>(p.D / 4));
+    paged_attention_join_kernel<<<dim3(static_cast<uint32_t>(p.N * p.Hq * parts)), dim3(kJoinThreads), 0, stream>>>(
+        p, static_cast<int>(parts));
     return hipGetLastError();
 }
 
