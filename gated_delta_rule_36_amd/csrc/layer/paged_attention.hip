@@ -313,46 +313,54 @@ __global__ __launch_bounds__(kThreads, KS <= 4 ? 3 : KS <= 6 ? 2 : 1) void paged
     }
 }
 
-// Joins the splits of a row: a workgroup for every 32 channels, lanes of four
-// channels, the splits dealt over the 32 groups of lanes.
-constexpr int kJoinThreads = 256, kJoinLanes = 8, kJoinGroups = kJoinThreads / kJoinLanes;
+// Joins the splits of a row: LANES lanes of four channels each, the splits dealt
+// over the workgroup's groups of lanes, each of which keeps a running maximum
+// and sum of its own; they meet in LDS.  A workgroup takes 4 LANES channels: 32 of
+// a row of many splits, so that several share it, all of one of few (64
+// requests of up to 65 splits, 32 heads: 15 us by 32 channels, 7 by 128; one of
+// 1024 splits and 16 heads 8 by 32 channels).
+constexpr int kJoinThreads = 256;
+template <int LANES>
 __global__ __launch_bounds__(kJoinThreads) void paged_attention_join_kernel(AttentionParams p, int parts)
 {
-    __shared__ __align__(16) float part[kJoinGroups][4 * kJoinLanes];
-    __shared__ float shared_sum[kJoinGroups], shared_top[kJoinThreads / 64];
+    constexpr int GROUPS = kJoinThreads / LANES;
+    __shared__ __align__(16) float part[GROUPS][4 * LANES];
+    __shared__ float tops[GROUPS], sums[GROUPS];
     const uint32_t head = blockIdx.x / static_cast<uint32_t>(parts), at = blockIdx.x - head * static_cast<uint32_t>(parts);
     const Visible vis = visible(p, head / static_cast<uint32_t>(p.Hq));
     if (vis.used <= 1)
         return;
-    const int tid = threadIdx.x, grp = tid / kJoinLanes, l = tid % kJoinLanes, d = 4 * kJoinLanes * static_cast<int>(at) + 4 * l;
+    const int tid = threadIdx.x, grp = tid / LANES, l = tid % LANES, d = 4 * LANES * static_cast<int>(at) + 4 * l;
     const bool here = d < p.D;
     const float *stats = p.stats + 2 * head * p.splits, *src = p.part + head * p.splits * p.D + (here ? d : 0);
-    float most = -__builtin_inff();
-    for (int s = tid; s < vis.used; s += kJoinThreads) most = fmaxf(most, stats[2 * s]);
-    for (int m = 32; m > 0; m >>= 1) most = fmaxf(most, __shfl_xor(most, m));
-    if ((tid & 63) == 0)
-        shared_top[tid >> 6] = most;
-    __syncthreads();
-    for (int w = 0; w < kJoinThreads / 64; ++w) most = fmaxf(most, shared_top[w]);
-    const float from_top = most == -__builtin_inff() ? 0.0f : most;
-
     f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
-    float total = 0.0f;
+    float top = -__builtin_inff(), total = 0.0f;
 #pragma unroll 4
-    for (int s = grp; s < vis.used; s += kJoinGroups) {
-        const float f = exp2_f32(stats[2 * s] - from_top);
-        total = fmaf(f, stats[2 * s + 1], total);
-        x += f * *reinterpret_cast<const f32x4_t *>(src + s * p.D);
+    for (int s = grp; s < vis.used; s += GROUPS) {
+        const float m = stats[2 * s], next = fmaxf(top, m), from_top = next == -__builtin_inff() ? 0.0f : next;
+        const float keep = exp2_f32(top - from_top), f = exp2_f32(m - from_top);
+        total = fmaf(f, stats[2 * s + 1], total * keep);
+        x = f * *reinterpret_cast<const f32x4_t *>(src + s * p.D) + x * keep;
+        top = next;
     }
     *reinterpret_cast<f32x4_t *>(&part[grp][4 * l]) = x;
-    if (l == 0)
-        shared_sum[grp] = total;
+    if (l == 0) {
+        tops[grp] = top;
+        sums[grp] = total;
+    }
     __syncthreads();
-    if (tid >= kJoinLanes || !here)
+    if (tid >= LANES || !here)
         return;
-    for (int k = 1; k < kJoinGroups; ++k) {
-        x += *reinterpret_cast<const f32x4_t *>(&part[k][4 * l]);
-        total += shared_sum[k];
+    float most = tops[0];
+    for (int k = 1; k < GROUPS; ++k) most = fmaxf(most, tops[k]);
+    const float from_top = most == -__builtin_inff() ? 0.0f : most;
+    x = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    total = 0.0f;
+#pragma unroll 4
+    for (int k = 0; k < GROUPS; ++k) {
+        const float f = exp2_f32(tops[k] - from_top);
+        total = fmaf(f, sums[k], total);
+        x += f * *reinterpret_cast<const f32x4_t *>(&part[k][4 * l]);
     }
     const float f = total == 0.0f ? 0.0f : 1.0f / total;
     *reinterpret_cast<u32x2_t *>(p.out + head * p.D + d) =
@@ -361,13 +369,21 @@ __global__ __launch_bounds__(kJoinThreads) void paged_attention_join_kernel(Atte
         p.lse[head] = total == 0.0f ? -__builtin_inff() : (from_top + log2f(total)) * kLn2F;
 }
 
+template <int LANES>
+hipError_t launch_join(const AttentionParams &p, hipStream_t stream)
+{
+    const int64_t parts = (p.D + 4 * LANES - 1) / (4 * LANES);
+    paged_attention_join_kernel<LANES><<<dim3(static_cast<uint32_t>(p.N * p.Hq * parts)), dim3(kJoinThreads), 0, stream>>>(
+        p, static_cast<int>(parts));
+    return hipGetLastError();
+}
+
 template <int KS>
 hipError_t launch(const AttentionParams &p, hipStream_t stream)
 {
     const int64_t row_tiles = (p.Hq / p.Hk + ROWS - 1) / ROWS;
     const int64_t items = p.N * p.splits * row_tiles * p.Hk, blocks = p.shared ? items : (items + kWaves - 1) / kWaves;
-    const int64_t parts = (p.D + 4 * kJoinLanes - 1) / (4 * kJoinLanes);
-    if (!grid_fits(blocks, kThreads) || !grid_fits(p.N * p.Hq * parts, kJoinThreads))
+    if (!grid_fits(blocks, kThreads) || !grid_fits(p.N * p.Hq * ((p.D + 31) / 32), kJoinThreads))
         return hipErrorInvalidConfiguration;
     const dim3 grid(static_cast<uint32_t>(blocks));
     if (p.shared)
@@ -377,9 +393,7 @@ hipError_t launch(const AttentionParams &p, hipStream_t stream)
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1)
         return e;
-    paged_attention_join_kernel<<<dim3(static_cast<uint32_t>(p.N * p.Hq * parts)), dim3(kJoinThreads), 0, stream>>>(
-        p, static_cast<int>(parts));
-    return hipGetLastError();
+    return p.splits > 128 ? launch_join<8>(p, stream) : p.D <= 128 ? launch_join<32>(p, stream) : launch_join<64>(p, stream);
 }
 
 }  // namespace

@@ -15,6 +15,7 @@
 // as many tokens as fill its lanes once, and works out their angles once, in
 // LDS: in turns, with the product and its reduction to half a turn in 64 bits,
 // since fp32 has no digits left for a turn's fraction at far positions.
+#include <algorithm>
 #include <type_traits>
 
 #include "layer_device.h"
@@ -24,6 +25,7 @@ namespace layer {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int64_t kManyBlocks = 4096, kDepth = 4;
 
 __device__ __forceinline__ void load_unit(const uint16_t *p, float f[4], std::integral_constant<int, 4>)
 {
@@ -63,12 +65,27 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryParams p, int pe
     // a workgroup's tokens times R / 2 angles: at most 256 / LPR tokens, VEC LPR ITEMS angles each
     constexpr int kAngles = kThreads * VEC * ITEMS;
     __shared__ float2 turn[kAngles];
-    __shared__ int64_t place[APPEND ? kThreads : 1][2];
+    __shared__ int64_t from[kThreads / LPR][2], to[kThreads / LPR][2];  // where a token's x and y lie, and where they go
     const int tid = threadIdx.x, l = tid % LPR, group = tid / LPR;
     const int64_t tokens = p.B * p.T, first = static_cast<int64_t>(blockIdx.x) * per_wg;
     const int here = static_cast<int>(tokens - first < per_wg ? tokens - first : per_wg);
     const int half = p.positions ? p.R / 2 : 0;
 
+    if (tid < here) {
+        const int64_t token = first + tid, b = token / p.T, at = token - b * p.T;
+        from[tid][0] = b * p.xb + at * p.xt;
+        from[tid][1] = b * p.yb + at * p.yt;
+        if constexpr (APPEND) {
+            const int64_t slot = p.slots[token];
+            const bool in = slot >= 0 && slot < p.slot_count;
+            const int64_t page = in ? slot / p.page_size : 0, off = in ? slot - page * p.page_size : 0;
+            to[tid][0] = in ? page * p.xc.page + off * p.xc.token : -1;
+            to[tid][1] = in ? page * p.yc.page + off * p.yc.token : -1;
+        } else {
+            to[tid][0] = token * p.first * p.D;
+            to[tid][1] = token * p.second * p.D;
+        }
+    }
     for (int i = tid; i < here * half; i += kThreads) {
         const int t = i / half, f = i - t * half;
         const double turns = static_cast<double>(p.positions[first + t]) * static_cast<double>(p.inv_freq[f]) * 0.15915494309189533577;
@@ -77,78 +94,77 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryParams p, int pe
         sincospif(part, &sn, &cs);
         turn[i] = make_float2(cs * p.scale, sn * p.scale);
     }
-    if constexpr (APPEND) {
-        if (tid < here) {
-            const int64_t slot = p.slots[first + tid];
-            const bool in = slot >= 0 && slot < p.slot_count;
-            const int64_t page = in ? slot / p.page_size : 0, at = in ? slot - page * p.page_size : 0;
-            place[tid][0] = in ? page * p.xc.page + at * p.xc.token : -1;
-            place[tid][1] = page * p.yc.page + at * p.yc.token;
-        }
-    }
     __syncthreads();
 
     const int rows = p.first + p.second;
-    for (int w = group; w < here * rows; w += kThreads / LPR) {
-        const int t = w / rows, r = w - t * rows;
-        const bool second = r >= p.first;
-        const int head = second ? r - p.first : r;
-        const int64_t token = first + t, b = token / p.T, at = token - b * p.T;
-        const uint16_t *x = (second ? p.y + b * p.yb + at * p.yt : p.x + b * p.xb + at * p.xt) + static_cast<int64_t>(head) * p.D;
-        uint16_t *out;
-        bool plain = false;  // the values of an append
-        if constexpr (APPEND) {
-            if (place[t][0] < 0)
-                continue;
-            out = second ? p.y_out + place[t][1] + head * p.yc.head : p.x_out + place[t][0] + head * p.xc.head;
-            plain = second;
-        } else {
-            out = second ? p.y_out + (token * p.second + head) * p.D : p.x_out + (token * p.first + head) * p.D;
-        }
-
-        float a[ITEMS][VEC], c[ITEMS][VEC];
-        int ua[ITEMS], uc[ITEMS];  // first channels of an item's units
-        bool turned[ITEMS], in[ITEMS];
+    const float inverse_size = 1.0f / static_cast<float>(p.D);
+    // An item's units start at these channels; the values of an append go as they are.
+    const auto turned = [&](bool second, int i) { return VEC * (l + LPR * i) < half && !(APPEND && second); };
+    const auto inside = [&](int i) { return 2 * VEC * (l + LPR * i) < p.D; };
+    const auto unit_a = [&](bool second, int i) { return (turned(second, i) && !p.interleaved ? VEC : 2 * VEC) * (l + LPR * i); };
+    const auto unit_c = [&](bool second, int i) { return unit_a(second, i) + (turned(second, i) && !p.interleaved ? half : VEC); };
+    // the weights of x and of y
+    float wa[2][ITEMS][VEC], wc[2][ITEMS][VEC];
+#pragma unroll
+    for (int y = 0; y < (APPEND ? 1 : 2); ++y) {
+        const void *weight = y ? p.y_weight : p.x_weight;
+        const int kind = y ? p.y_kind : p.x_kind;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-            const int item = l + LPR * i;
-            in[i] = 2 * VEC * item < p.D;
-            turned[i] = VEC * item < half && !plain;
-            const bool split = turned[i] && !p.interleaved;
-            ua[i] = split ? VEC * item : 2 * VEC * item;
-            uc[i] = ua[i] + (split ? half : VEC);
+            if (!weight || !inside(i))
+                continue;
+            const int ua = unit_a(y, i), uc = unit_c(y, i);
+            if (kind == kBf16) {
+                load_unit(static_cast<const uint16_t *>(weight) + ua, wa[y][i], width);
+                load_unit(static_cast<const uint16_t *>(weight) + uc, wc[y][i], width);
+            } else {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) a[i][e] = c[i][e] = 0.0f;
-            if (in[i]) {
-                load_unit(x + ua[i], a[i], width);
-                load_unit(x + uc[i], c[i], width);
+                for (int e = 0; e < VEC; ++e) {
+                    wa[y][i][e] = static_cast<const float *>(weight)[ua + e];
+                    wc[y][i][e] = static_cast<const float *>(weight)[uc + e];
+                }
             }
         }
-        const void *weight = second ? p.y_weight : p.x_weight;
-        if (weight && !plain) {
-            const int kind = second ? p.y_kind : p.x_kind;
-            float wa[ITEMS][VEC], wc[ITEMS][VEC];
+    }
+
+    // A row on its way: the next one's numbers are asked for before this one's are used.
+    struct Row {
+        int t;
+        bool second;
+        uint16_t *out;  // nullptr: left out
+        float a[ITEMS][VEC], c[ITEMS][VEC];
+    };
+    const auto fetch = [&](int t, int r) {
+        Row row;
+        row.t = t;
+        row.second = r >= p.first;
+        const int head = row.second ? r - p.first : r;
+        const uint16_t *x = (row.second ? p.y : p.x) + from[t][row.second] + head * p.D;
+        const int64_t place = to[t][row.second];
+        if constexpr (APPEND)
+            row.out = place < 0 ? nullptr : (row.second ? p.y_out : p.x_out) + place + head * (row.second ? p.yc.head : p.xc.head);
+        else
+            row.out = (row.second ? p.y_out : p.x_out) + place + head * p.D;
 #pragma unroll
-            for (int i = 0; i < ITEMS; ++i)
-                if (in[i]) {
-                    if (kind == kBf16) {
-                        load_unit(static_cast<const uint16_t *>(weight) + ua[i], wa[i], width);
-                        load_unit(static_cast<const uint16_t *>(weight) + uc[i], wc[i], width);
-                    } else {
+        for (int i = 0; i < ITEMS; ++i) {
 #pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            wa[i][e] = static_cast<const float *>(weight)[ua[i] + e];
-                            wc[i][e] = static_cast<const float *>(weight)[uc[i] + e];
-                        }
-                    }
-                }
+            for (int e = 0; e < VEC; ++e) row.a[i][e] = row.c[i][e] = 0.0f;
+            if (inside(i)) {
+                load_unit(x + unit_a(row.second, i), row.a[i], width);
+                load_unit(x + unit_c(row.second, i), row.c[i], width);
+            }
+        }
+        return row;
+    };
+    const auto finish = [&](Row &row) {
+        if ((row.second ? p.y_weight : p.x_weight) && !(APPEND && row.second)) {
             const auto squares = [&] {
                 float ss = 0.0f;
 #pragma unroll
                 for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) ss = fmaf(a[i][e], a[i][e], fmaf(c[i][e], c[i][e], ss));
-                return lane_sum<LPR>(ss) / static_cast<float>(p.D);
+                    for (int e = 0; e < VEC; ++e) ss = fmaf(row.a[i][e], row.a[i][e], fmaf(row.c[i][e], row.c[i][e], ss));
+                return lane_sum<LPR>(ss) * inverse_size;
             };
             float m = squares() + p.eps.plain;
             if (!norm_in_range(m)) {  // one row's lanes together: m is theirs
@@ -157,35 +173,36 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryParams p, int pe
                 for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
-                        a[i][e] *= f;
-                        c[i][e] *= f;
+                        row.a[i][e] *= f;
+                        row.c[i][e] *= f;
                     }
                 m = squares() + eps;
             }
             const float s = __builtin_amdgcn_rsqf(m);
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i)
-                if (in[i]) {
+                if (inside(i)) {
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
-                        a[i][e] *= s * wa[i][e];
-                        c[i][e] *= s * wc[i][e];
+                        row.a[i][e] *= s * (!APPEND && row.second ? wa[1][i][e] : wa[0][i][e]);
+                        row.c[i][e] *= s * (!APPEND && row.second ? wc[1][i][e] : wc[0][i][e]);
                     }
                 }
         }
+        if (APPEND && !row.out)
+            return;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-            if (!in[i])
+            if (!inside(i))
                 continue;
-            if (turned[i]) {
-                float v[2 * VEC];
+            float v[2 * VEC], o[2 * VEC];
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    v[e] = a[i][e];
-                    v[VEC + e] = c[i][e];
-                }
-                const float2 *cs = turn + t * half + VEC * (l + LPR * i);
-                float o[2 * VEC];
+            for (int e = 0; e < VEC; ++e) {
+                v[e] = o[e] = row.a[i][e];
+                v[VEC + e] = o[VEC + e] = row.c[i][e];
+            }
+            if (turned(row.second, i)) {
+                const float2 *cs = turn + row.t * half + VEC * (l + LPR * i);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     const float2 f = cs[e];
@@ -197,29 +214,46 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryParams p, int pe
                         o[VEC + e] = fmaf(v[VEC + e], f.x, v[e] * f.y);
                     }
                 }
-                store_unit<VEC>(out + ua[i], o);
-                store_unit<VEC>(out + uc[i], o + VEC);
-            } else {
-                store_unit<VEC>(out + ua[i], a[i]);
-                store_unit<VEC>(out + uc[i], c[i]);
             }
+            store_unit<VEC>(row.out + unit_a(row.second, i), o);
+            store_unit<VEC>(row.out + unit_c(row.second, i), o + VEC);
         }
+    };
+    constexpr int kGroups = kThreads / LPR;
+    int t = group / rows, r = group - t * rows;
+    if (t >= here)
+        return;
+    Row now = fetch(t, r);
+    for (;;) {
+        for (r += kGroups; r >= rows && t < here; ++t) r -= rows;
+        const bool more = t < here;
+        Row next;
+        if (more)
+            next = fetch(t, r);
+        finish(now);
+        if (!more)
+            return;
+        now = next;
     }
 }
 
 template <int VEC, int LPR, int ITEMS>
 hipError_t launch(const RotaryParams &p, hipStream_t stream)
 {
-    const int64_t rows = p.first + p.second, fill = kThreads / LPR;
-    const int per_wg = static_cast<int>(rows >= fill ? 1 : fill / rows);
-    const int64_t blocks = (p.B * p.T + per_wg - 1) / per_wg;
+    // tokens a workgroup: those that fill its lanes once, and of many tokens up to
+    // four times, so that loads of a row run beside the one before
+    const int64_t rows = p.first + p.second, fill = kThreads / LPR, tokens = p.B * p.T;
+    const int64_t most = std::min(fill, static_cast<int64_t>(kThreads * VEC * ITEMS) / std::max(1, p.positions ? p.R / 2 : 1));
+    int64_t per_wg = rows >= fill ? 1 : fill / rows;
+    while (tokens / per_wg > kManyBlocks && 2 * per_wg <= most && per_wg * rows < kDepth * fill) per_wg *= 2;
+    const int64_t blocks = (tokens + per_wg - 1) / per_wg;
     if (!grid_fits(blocks, kThreads))
         return hipErrorInvalidConfiguration;
     const dim3 grid(static_cast<uint32_t>(blocks));
     if (p.slots)
-        rotary_kernel<VEC, LPR, ITEMS, true><<<grid, dim3(kThreads), 0, stream>>>(p, per_wg);
+        rotary_kernel<VEC, LPR, ITEMS, true><<<grid, dim3(kThreads), 0, stream>>>(p, static_cast<int>(per_wg));
     else
-        rotary_kernel<VEC, LPR, ITEMS, false><<<grid, dim3(kThreads), 0, stream>>>(p, per_wg);
+        rotary_kernel<VEC, LPR, ITEMS, false><<<grid, dim3(kThreads), 0, stream>>>(p, static_cast<int>(per_wg));
     return hipGetLastError();
 }
 
