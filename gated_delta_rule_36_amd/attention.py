@@ -13,7 +13,9 @@ from typing import Optional
 import torch
 
 from . import _lib
-from .layer import _BF16, _call, _dense, _device, _entry, _pack, _tensor, _tokens, _typed
+from .layer import _BF16, _FP32, _call, _dense, _device, _entry, _pack, _tensor, _tokens, _typed
+
+_INT32, _INT64 = torch.int32, torch.int64
 
 
 def _rotation(positions, inv_freq, device, shape):
@@ -22,16 +24,18 @@ def _rotation(positions, inv_freq, device, shape):
         raise ValueError("positions and inv_freq go together")
     if positions is None:
         return 0, 0, 0
-    pp = _dense("positions", positions, device, shape, torch.int64)
-    _tensor("inv_freq", inv_freq, device, torch.float32)
-    if inv_freq.dim() != 1:
-        raise ValueError(f"inv_freq must be [R/2], got {list(inv_freq.shape)}")
-    return pp, _dense("inv_freq", inv_freq, device, inv_freq.shape, torch.float32), 2 * inv_freq.shape[0]
+    pp = _dense("positions", positions, device, shape, _INT64)
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype is not _FP32 or inv_freq.device != device:
+        _tensor("inv_freq", inv_freq, device, _FP32)
+    if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError(f"inv_freq must be contiguous [R/2], got {list(inv_freq.shape)} with strides {inv_freq.stride()}")
+    return pp, inv_freq.data_ptr(), 2 * inv_freq.shape[0]
 
 
 def _cache(name, t, device, heads, channels):
     """(pointer, strides of page, token and head) of a paged cache [pages, page_size, heads, channels]."""
-    _tensor(name, t, device, _BF16)
+    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.device != device:
+        _tensor(name, t, device, _BF16)
     shape, strides = t.shape, t.stride()
     if len(shape) != 4 or shape[2] != heads or shape[3] != channels:
         raise ValueError(f"{name} must be [pages,page_size,{heads},{channels}], got {list(shape)}")
@@ -101,15 +105,17 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         raise ValueError(f"k must be [B,T,H,D], got {list(k.shape)}")
     B, T, H, D = shape = k.shape
     pk, kb, kt = _tokens("k", k, device, shape)
-    _tensor("v", v, device, _BF16)
+    if v is None:
+        _tensor("v", v, device, _BF16)
     pv, vb, vt = _tokens("v", v, device, shape)
     pkc, kp, ks, kh = _cache("k_cache", k_cache, device, H, D)
     pvc, vp, vs, vh = _cache("v_cache", v_cache, device, H, D)
     pages, page_size = k_cache.shape[:2]
     if v_cache.shape[:2] != k_cache.shape[:2]:
         raise ValueError(f"the caches differ in pages: {list(k_cache.shape)} and {list(v_cache.shape)}")
-    _tensor("slots", slots, device, torch.int64)
-    ps = _dense("slots", slots, device, (B, T), torch.int64)
+    if slots is None:
+        _tensor("slots", slots, device, _INT64)
+    ps = _dense("slots", slots, device, (B, T), _INT64)
     pp, pf, R = _rotation(positions, inv_freq, device, (B, T))
     pw, wcode = _typed("weight", weight, device, (D,))
     _call("kda_append_kv", (pk, pv, pkc, pvc, kb, kt, vb, vt, kp, ks, kh, vp, vs, vh, ps, pp, pf, pw, B, T, H, D, R,
@@ -139,29 +145,32 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     if q.dim() != 3:
         raise ValueError(f"q must be [N,Hq,D], got {list(q.shape)}")
     N, Hq, D = shape = q.shape
-    pq, _, qr = _tokens("q", q.unsqueeze(0), device, (1, N, Hq, D))
-    _tensor("k_cache", k_cache, device, _BF16)
-    if k_cache.dim() != 4:
+    strides = q.stride()
+    if (strides[2] != 1 and D != 1) or (strides[1] != D and Hq != 1):
+        raise ValueError(f"q: the channels of a sequence must be adjacent, got strides {strides}")
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        _tensor("k_cache", k_cache, device, _BF16)
         raise ValueError(f"k_cache must be [pages,page_size,Hk,D], got {list(k_cache.shape)}")
-    pages, page_size, Hk = k_cache.shape[:3]
+    pages, page_size, Hk, _ = k_cache.shape
     pk, kp, ks, kh = _cache("k_cache", k_cache, device, Hk, D)
     pv, vp, vs, vh = _cache("v_cache", v_cache, device, Hk, D)
     if v_cache.shape[:2] != k_cache.shape[:2]:
         raise ValueError(f"the caches differ in pages: {list(k_cache.shape)} and {list(v_cache.shape)}")
-    _tensor("block_table", block_table, device, torch.int32)
+    if not isinstance(block_table, torch.Tensor) or block_table.dtype is not _INT32 or block_table.device != device:
+        _tensor("block_table", block_table, device, _INT32)
     if block_table.dim() != 2 or block_table.shape[0] != N:
         raise ValueError(f"block_table must be [{N},width], got {list(block_table.shape)}")
     width = block_table.shape[1]
     if width > 1 and block_table.stride(1) != 1:
         raise ValueError(f"block_table: a sequence's pages must be adjacent, got strides {block_table.stride()}")
-    _tensor("lengths", lengths, device, torch.int32)
-    pl = _dense("lengths", lengths, device, (N,), torch.int32)
-    _tensor("out", out, device, _BF16)
+    if lengths is None or out is None:
+        _tensor("out" if out is None else "lengths", None, device)
+    pl = _dense("lengths", lengths, device, (N,), _INT32)
     po = _dense("out", out, device, shape, _BF16)
-    pe = _dense("lse", lse, device, (N, Hq), torch.float32)
+    pe = _dense("lse", lse, device, (N, Hq), _FP32)
     if window is not None and (not isinstance(window, int) or isinstance(window, bool) or window < 1):
         raise ValueError(f"window must be a positive int or None, got {window!r}")
-    values = (pq, pk, pv, block_table.data_ptr(), pl, po, pe, qr, block_table.stride(0), kp, ks, kh, vp, vs, vh,
+    values = (q.data_ptr(), pk, pv, block_table.data_ptr(), pl, po, pe, strides[0], block_table.stride(0), kp, ks, kh, vp, vs, vh,
               N, Hq, Hk, D, pages, page_size, width, window or 0, 0, scale)
     workspace_bytes, pack = _entry("kda_paged_attention_workspace_bytes")
     args = _pack(pack, values + (0, 0))
@@ -171,5 +180,5 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         # again only to work ordered after this call on the same stream
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
         args = _pack(pack, values + (workspace.data_ptr(), nbytes))
-    _call("kda_paged_attention", values, device, args)
+    _call("kda_paged_attention", None, device, args)
     return out

@@ -20,7 +20,8 @@ from .api import KdaArgumentError, KdaError
 
 _CODES = {torch.bfloat16: _lib.KDA_DTYPE_BF16, torch.float32: _lib.KDA_DTYPE_FP32}
 _ACTIVATIONS = {None: _lib.KDA_ACT_NONE, "silu": _lib.KDA_ACT_SILU, "sigmoid": _lib.KDA_ACT_SIGMOID}
-_BF16 = torch.bfloat16
+_BF16, _FP32 = torch.bfloat16, torch.float32
+_NONE = _lib.KDA_DTYPE_NONE
 
 
 def _tensor(name, t, device, *dtypes):
@@ -62,10 +63,13 @@ def _tokens(name, t, device, shape):
     """(pointer, batch stride, token stride) of bf16 [B, T, ...] whose trailing dimensions are adjacent."""
     if t is None:
         return 0, 0, 0
-    _tensor(name, t, device, _BF16)
+    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.device != device:
+        _tensor(name, t, device, _BF16)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     strides, width = t.stride(), 1
+    if len(strides) == 4 and strides[3] == 1 and strides[2] == shape[3]:  # heads side by side
+        return t.data_ptr(), strides[0], strides[1]
     for size, stride in zip(reversed(shape[2:]), reversed(strides[2:])):
         if size != 1 and stride != width:
             raise ValueError(f"{name}: the channels of a token must be adjacent, got strides {strides}")
@@ -109,8 +113,8 @@ def _sequences(cu_seqlens, device, B, T, check):
 def _typed(name, t, device, shape):
     """(pointer, dtype code) of a contiguous bf16 or fp32 tensor of exactly `shape`, or of None."""
     if t is None:
-        return 0, _lib.KDA_DTYPE_NONE
-    return _dense(name, t, device, shape, _BF16, torch.float32), _CODES[t.dtype]
+        return 0, _NONE
+    return _dense(name, t, device, shape, _BF16, _FP32), _CODES[t.dtype]
 
 
 def _pack(pack, values):
