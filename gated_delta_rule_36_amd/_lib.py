@@ -11,8 +11,8 @@ LIBRARY = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
 EXPORTS = ("kda_fwd", "kda_fwd_ex", "kda_fwd_scan", "kda_fwd_scan_static",
            "kda_fwd_scan_workspace_bytes", "kda_status_string", "kda_fwd_kernel",
            "kda_abi_version", "kda_short_conv", "kda_ssm_fwd", "kda_ssm_workspace_bytes",
-           "kda_gated_norm", "kda_residual_norm", "kda_delta_fwd", "kda_qk_norm_rotary", "kda_append_kv",
-           "kda_paged_attention", "kda_paged_attention_workspace_bytes")
+           "kda_gated_norm", "kda_residual_norm", "kda_delta_fwd", "kda_delta_workspace_bytes",
+           "kda_qk_norm_rotary", "kda_append_kv", "kda_paged_attention", "kda_paged_attention_workspace_bytes")
 SCAN_STATIC_BYTES = 32 << 20  # KDA_SCAN_STATIC_BYTES
 ABI_VERSION = 6
 
@@ -104,7 +104,8 @@ class DeltaArgs(ctypes.Structure):
                 + _fields(_P, "A_log dt_bias initial_state final_state cu_seqlens")
                 + _fields(_I64, "num_seqs B T H G K V")
                 + _fields(_I32, "initial_state_dtype final_state_dtype") + _fields(_I64, "reserved")
-                + _fields(_F64, "scale"))
+                + _fields(_F64, "scale") + _fields(_I64, "seg_tokens") + _fields(_P, "workspace")
+                + _fields(_I64, "workspace_bytes"))
 
 
 class RotaryArgs(ctypes.Structure):
@@ -192,7 +193,8 @@ def load() -> ctypes.CDLL:
         getattr(lib, name).argtypes = [ctypes.POINTER(args), p]
         getattr(lib, name).restype = ctypes.c_int
         LAYER[name] = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p, p)((name, lib)), packer(args)
-    for name, args in (("kda_ssm_workspace_bytes", SsmArgs), ("kda_paged_attention_workspace_bytes", AttentionArgs)):
+    for name, args in (("kda_ssm_workspace_bytes", SsmArgs), ("kda_delta_workspace_bytes", DeltaArgs),
+                       ("kda_paged_attention_workspace_bytes", AttentionArgs)):
         getattr(lib, name).argtypes = [ctypes.POINTER(args)]
         getattr(lib, name).restype = i64
         LAYER[name] = ctypes.CFUNCTYPE(i64, ctypes.c_char_p)((name, lib)), packer(args)

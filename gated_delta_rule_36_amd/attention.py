@@ -13,7 +13,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from .layer import _BF16, _FP32, _call, _dense, _device, _entry, _pack, _tensor, _tokens, _typed
+from .layer import _BF16, _FP32, _call, _call_with_workspace, _dense, _device, _tensor, _tokens, _typed
 
 _INT32, _INT64 = torch.int32, torch.int64
 
@@ -172,13 +172,5 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         raise ValueError(f"window must be a positive int or None, got {window!r}")
     values = (q.data_ptr(), pk, pv, block_table.data_ptr(), pl, po, pe, strides[0], block_table.stride(0), kp, ks, kh, vp, vs, vh,
               N, Hq, Hk, D, pages, page_size, width, window or 0, 0, scale)
-    workspace_bytes, pack = _entry("kda_paged_attention_workspace_bytes")
-    args = _pack(pack, values + (0, 0))
-    nbytes = workspace_bytes(args)
-    if nbytes > 0:
-        # freed right after the call: the caching allocator hands it out
-        # again only to work ordered after this call on the same stream
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        args = _pack(pack, values + (workspace.data_ptr(), nbytes))
-    _call("kda_paged_attention", None, device, args)
+    _call_with_workspace("kda_paged_attention", "kda_paged_attention_workspace_bytes", values, device)
     return out

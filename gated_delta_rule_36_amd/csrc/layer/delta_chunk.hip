@@ -162,7 +162,7 @@ __device__ __forceinline__ constexpr int a_block(int b, int c) { return b * (b +
 __device__ __forceinline__ constexpr int p_block(int b, int e) { return (b / 2) * (b / 2 + 1) + (b % 2) * (b / 2 + 1) + e; }
 
 template <int K, int TM>
-struct Tile {
+struct LdsTile {
     static constexpr int NB = TM / 16, kPitch = K + 16, kAPitch = 24, kPPitch = 48;
     alignas(16) uint16_t k[TM][kPitch];
     alignas(16) uint16_t q[TM][kPitch];
@@ -175,39 +175,64 @@ struct Tile {
 
 template <int K, int TM>
 struct Shared {
-    Tile<K, TM> tile[2];
+    LdsTile<K, TM> tile[2];
     alignas(16) uint16_t v[kStateWaves][TM][16];
 };
 
-// Where a workgroup's chain lies.
+// Where a workgroup's chain lies: a (sequence, head), or a segment of one.
 struct Chain {
     int64_t n, h, grp, row;
     int begin, tokens, col0, width;  // its tokens, its columns
+    int index;                       // of the segment
+    bool several, last;              // one of several; the sequence's last
+    int64_t slab;                    // the sequence's first slab
+    bool valid;
 };
-__device__ __forceinline__ Chain find_chain(const DeltaParams &p, int vblocks, int columns)
+// Rows of a slab: the state [V, K] at the end of the segment before, and behind it
+// [K, K] what that segment makes of each unit vector.
+__device__ __forceinline__ int64_t slab_row(const DeltaParams &p, int64_t slab, int64_t h, int64_t row)
+{
+    return ((slab * p.H + h) * (p.V + p.K) + row) * p.K;
+}
+__device__ __forceinline__ Chain find_chain(const DeltaParams &p, int all, int vblocks, int columns)
 {
     Chain c;
     const uint32_t chain = blockIdx.x / static_cast<uint32_t>(vblocks), vb = blockIdx.x - chain * static_cast<uint32_t>(vblocks);
-    c.n = chain / static_cast<uint32_t>(p.H);
-    c.h = chain - static_cast<uint32_t>(c.n) * static_cast<uint32_t>(p.H);
+    const uint32_t slot = chain / static_cast<uint32_t>(p.H);
+    c.h = chain - slot * static_cast<uint32_t>(p.H);
     c.grp = c.h / (p.H / p.G);
-    c.row = c.n;
-    c.begin = 0;
-    int end = static_cast<int>(p.seqs.T);
-    if (p.seqs.cu) {
-        c.row = 0;
-        c.begin = static_cast<int>(clamp_offset(p.seqs, c.n));
-        end = static_cast<int>(clamp_offset(p.seqs, c.n + 1));
-    }
-    c.tokens = end > c.begin ? end - c.begin : 0;
     c.col0 = static_cast<int>(vb) * columns;
-    c.width = static_cast<int>(p.V) - c.col0 < columns ? static_cast<int>(p.V) - c.col0 : columns;
+    c.width = all - c.col0 < columns ? all - c.col0 : columns;
+    if (p.seg == 0) {
+        c.n = slot;
+        c.row = p.seqs.cu ? 0 : c.n;
+        c.begin = p.seqs.cu ? static_cast<int>(clamp_offset(p.seqs, c.n)) : 0;
+        const int end = p.seqs.cu ? static_cast<int>(clamp_offset(p.seqs, c.n + 1)) : static_cast<int>(p.seqs.T);
+        c.tokens = end > c.begin ? end - c.begin : 0;
+        c.index = 0;
+        c.several = false;
+        c.last = c.valid = true;
+        c.slab = 0;
+        return c;
+    }
+    const uint32_t seg = static_cast<uint32_t>(p.seg);
+    const layer::Tile t = find_tile(p.seqs, seg, slot);
+    const uint32_t t0 = t.index * seg, left = t.end - t.begin - t0;
+    c.n = t.n;
+    c.row = t.row;
+    c.begin = static_cast<int>(t.begin + t0);
+    c.last = left <= seg;
+    c.tokens = static_cast<int>(c.last ? left : seg);
+    c.index = static_cast<int>(t.index);
+    c.several = t.end - t.begin > seg;
+    c.slab = p.map.mul * (t.begin / seg) + p.map.add * t.n;
+    c.valid = t.valid;
     return c;
 }
 
 // The waves that prepare tiles: rows of K and Q into LDS, decays and strengths,
 // the blocks of A and P, the inverses of A's diagonal blocks.
-template <int K, int TM>
+template <int K, int TM, bool OUT>
 struct Producer {
     static constexpr int NB = TM / 16, PK = K / 8;                 // 16-byte pieces of a row
     static constexpr int kRows = 64 * kProducers / PK, kLoad = TM / kRows;  // rows loaded at once, and how often
@@ -244,7 +269,8 @@ struct Producer {
 #pragma unroll
             for (int i = 0; i < kLoad; ++i) {
                 nk[i] = *reinterpret_cast<const u32x4_a2 *>(kp + static_cast<int64_t>(i * kRows) * p.kt * 2 + koff);
-                nq[i] = *reinterpret_cast<const u32x4_a2 *>(qp + static_cast<int64_t>(i * kRows) * p.qt * 2 + qoff);
+                if constexpr (OUT)
+                    nq[i] = *reinterpret_cast<const u32x4_a2 *>(qp + static_cast<int64_t>(i * kRows) * p.qt * 2 + qoff);
             }
         } else {
             const int t = here(tid / PK), c = here(tid % PK);
@@ -252,7 +278,8 @@ struct Producer {
             for (int i = 0; i < kLoad; ++i) {
                 const int in = t + kRows * i < left ? t + kRows * i : left - 1;
                 nk[i] = *reinterpret_cast<const u32x4_a2 *>(kp + static_cast<uint32_t>(in) * static_cast<uint32_t>(2 * p.kt) + 16 * c);
-                nq[i] = *reinterpret_cast<const u32x4_a2 *>(qp + static_cast<uint32_t>(in) * static_cast<uint32_t>(2 * p.qt) + 16 * c);
+                if constexpr (OUT)
+                    nq[i] = *reinterpret_cast<const u32x4_a2 *>(qp + static_cast<uint32_t>(in) * static_cast<uint32_t>(2 * p.qt) + 16 * c);
             }
         }
         if (wave == kProducers - 1) {
@@ -262,7 +289,7 @@ struct Producer {
         }
     }
     // And from there into LDS; rows past the end are zeros.
-    __device__ __forceinline__ void store(Tile<K, TM> &to, int t0)
+    __device__ __forceinline__ void store(LdsTile<K, TM> &to, int t0)
     {
         const int left = ch.tokens - t0, t = tid / PK, c = tid % PK;
         if (left < TM) {
@@ -274,13 +301,14 @@ struct Producer {
 #pragma unroll
         for (int i = 0; i < kLoad; ++i) {
             *reinterpret_cast<u32x4_t *>(&to.k[t + kRows * i][8 * c]) = nk[i];
-            *reinterpret_cast<u32x4_t *>(&to.q[t + kRows * i][8 * c]) = nq[i];
+            if constexpr (OUT)
+                *reinterpret_cast<u32x4_t *>(&to.q[t + kRows * i][8 * c]) = nq[i];
         }
         if (wave == kProducers - 1)
             gates(to, left);
     }
     // The decays and strengths of a tile, a token a lane.
-    __device__ __forceinline__ void gates(Tile<K, TM> &to, int left)
+    __device__ __forceinline__ void gates(LdsTile<K, TM> &to, int left)
     {
         const bool in = lane < left && lane < TM;
         float a = rate * softplus_f32(lo_f32(ng) + bias, dt_plain_above(1));
@@ -303,7 +331,7 @@ struct Producer {
         f32x4_t kk, qk;
     };
     template <int b, int c>
-    __device__ __forceinline__ Products products(const Tile<K, TM> &to)
+    __device__ __forceinline__ Products products(const LdsTile<K, TM> &to)
     {
         const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
         Products y = {zero, zero};
@@ -311,12 +339,13 @@ struct Producer {
         for (int e = 0; e < K / 32; ++e) {
             const u32x4_t x = *reinterpret_cast<const u32x4_t *>(&to.k[16 * c + r][32 * e + 8 * g]);
             y.kk = mfma(x, b == c ? x : *reinterpret_cast<const u32x4_t *>(&to.k[16 * b + r][32 * e + 8 * g]), y.kk);
-            y.qk = mfma(x, *reinterpret_cast<const u32x4_t *>(&to.q[16 * b + r][32 * e + 8 * g]), y.qk);
+            if constexpr (OUT)
+                y.qk = mfma(x, *reinterpret_cast<const u32x4_t *>(&to.q[16 * b + r][32 * e + 8 * g]), y.qk);
         }
         return y;
     }
     template <int b, int c>
-    __device__ __forceinline__ void finish(Tile<K, TM> &to, const Products &raw)
+    __device__ __forceinline__ void finish(LdsTile<K, TM> &to, const Products &raw)
     {
         const float hi = to.g[0][16 * b + r], lo = to.g[1][16 * b + r], strength = -to.beta[16 * b + r];
         const f32x4_t hj = *reinterpret_cast<const f32x4_t *>(&to.g[0][16 * c + 4 * g]);
@@ -328,15 +357,17 @@ struct Producer {
             x[m] = b > c || 4 * g + m < r ? strength * f * raw.kk[m] : 0.0f;
             y[m] = b > c || 4 * g + m <= r ? f * raw.qk[m] : 0.0f;
         }
+        *reinterpret_cast<f32x4_t *>(&to.a[a_block(b, c)][r][4 * g]) = x;
+        if constexpr (!OUT)
+            return;
         u32x2_t parts[2];
         split<2>(y, parts);
-        *reinterpret_cast<f32x4_t *>(&to.a[a_block(b, c)][r][4 * g]) = x;
         *reinterpret_cast<u32x2_t *>(&to.p[0][p_block(b, c / 2)][r][8 * g + 4 * (c % 2)]) = parts[0];
         *reinterpret_cast<u32x2_t *>(&to.p[1][p_block(b, c / 2)][r][8 * g + 4 * (c % 2)]) = parts[1];
     }
     // Three blocks at once, their products interleaved.
     template <int b0, int c0, int b1, int c1, int b2, int c2>
-    __device__ __forceinline__ void three(Tile<K, TM> &to)
+    __device__ __forceinline__ void three(LdsTile<K, TM> &to)
     {
         const Products x = products<b0, c0>(to), y = products<b1, c1>(to), z = products<b2, c2>(to);
         finish<b0, c0>(to, x);
@@ -344,7 +375,7 @@ struct Producer {
         finish<b2, c2>(to, z);
     }
     template <int b0, int c0, int b1, int c1>
-    __device__ __forceinline__ void two(Tile<K, TM> &to)
+    __device__ __forceinline__ void two(LdsTile<K, TM> &to)
     {
         const Products x = products<b0, c0>(to), y = products<b1, c1>(to);
         finish<b0, c0>(to, x);
@@ -352,7 +383,7 @@ struct Producer {
     }
     // The inverses of the diagonal blocks I + A by forward substitution: lane (g, r)
     // has column r of block g, X_i = e_i - sum_(m < i) A_im X_m.
-    __device__ __forceinline__ void invert(Tile<K, TM> &to)
+    __device__ __forceinline__ void invert(LdsTile<K, TM> &to)
     {
         const int bl = a_block(g < NB ? g : 0, g < NB ? g : 0);
         float x[16];
@@ -377,7 +408,7 @@ struct Producer {
         }
     }
     // A wave's share of them (the first wave inverts, the last one works out the gates).
-    __device__ __forceinline__ void blocks(Tile<K, TM> &to)
+    __device__ __forceinline__ void blocks(LdsTile<K, TM> &to)
     {
         static_assert(NB == 2 || NB == 4, "shares of two or four blocks");
         if constexpr (NB == 4) {
@@ -427,8 +458,11 @@ struct Producer {
     }
 };
 
-// A wave with 16 columns of the state.
-template <int K, int TM>
+// A wave with 16 columns of the state.  OUT: the pass that writes out, from the
+// states that the chains start with.  Otherwise the pass that forms every segment's
+// own state, from zero (the first one's from the initial state), and, in K more
+// columns without values, what it makes of each unit vector.
+template <int K, int TM, bool OUT>
 __device__ __forceinline__ void state_wave(const DeltaParams &p, const Chain &ch, Shared<K, TM> &sh, int lane, int wave)
 {
     constexpr int KT = K / 16, KSTEP = K / 32, NB = TM / 16;  // state tiles; steps over k; blocks of tokens
@@ -437,23 +471,44 @@ __device__ __forceinline__ void state_wave(const DeltaParams &p, const Chain &ch
 
     // the state: register i of tile 2 e + a is k = 32 e + 8 g + 4 a + i of column r
     f32x4_t s[KT];
-    const int64_t slab = ((ch.n * p.H + ch.h) * p.V + col + r) * K + 8 * g;
-    const auto place = [&](int t) { return slab + 32 * (t / 2) + 4 * (t % 2); };
+    const auto place = [&](int t) { return 8 * g + 32 * (t / 2) + 4 * (t % 2); };
+    const int64_t own = ((ch.n * p.H + ch.h) * p.V + col + r) * K;  // in the call's states
+    const bool unit = !OUT && col >= p.V;
+    const void *start = p.init_state;
+    int kind = p.init_kind;
+    int64_t from = own;
+    if (OUT ? ch.several : ch.index > 0) {
+        kind = OUT ? kFp32 : kNone;
+        start = p.slabs;
+        from = slab_row(p, ch.slab + ch.index, ch.h, col + r);
+    }
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
         s[t] = zero;
-        if (p.init_kind == kFp32) {
-            s[t] = *reinterpret_cast<const f32x4_t *>(static_cast<const float *>(p.init_state) + place(t));
-        } else if (p.init_kind == kBf16) {
-            const u32x2_t v = *reinterpret_cast<const u32x2_t *>(static_cast<const uint16_t *>(p.init_state) + place(t));
+        if (kind == kFp32) {
+            s[t] = *reinterpret_cast<const f32x4_t *>(static_cast<const float *>(start) + from + place(t));
+        } else if (kind == kBf16) {
+            const u32x2_t v = *reinterpret_cast<const u32x2_t *>(static_cast<const uint16_t *>(start) + from + place(t));
             s[t] = f32x4_t{lo_f32(v[0]), hi_f32(v[0]), lo_f32(v[1]), hi_f32(v[1])};
+        }
+        if (!OUT && ch.index == 0)  // for the pass to come, which may write the final state over the initial one
+            *reinterpret_cast<f32x4_t *>(p.slabs + slab_row(p, ch.slab, ch.h, col + r) + place(t)) = s[t];
+        if (unit) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[t][i] = place(t) + i == col + r - static_cast<int>(p.V) ? 1.0f : 0.0f;
         }
     }
     // The wave's own columns of V: half a row a lane, a tile ahead in registers.
     constexpr int kLoad = TM / 32;
     u32x4_t nv[kLoad];
+    if (unit) {
+#pragma unroll
+        for (int i = 0; i < kLoad; ++i) nv[i] = u32x4_t{0, 0, 0, 0};
+    }
     const char *vbase = reinterpret_cast<const char *>(p.v + ch.row * p.vb + static_cast<int64_t>(ch.begin) * p.vt + ch.h * p.V + col);
     const auto load = [&](int t0) {
+        if (unit)
+            return;
         const char *vp = vbase + static_cast<int64_t>(t0) * p.vt * 2;
         const int left = ch.tokens - t0, me = here(lane);
 #pragma unroll
@@ -473,7 +528,7 @@ __device__ __forceinline__ void state_wave(const DeltaParams &p, const Chain &ch
     int buf = 0;
     for (int t0 = 0; t0 < ch.tokens; t0 += TM, buf ^= 1) {
         // places in the tile: a base for each pattern of lanes, and constants
-        using T = Tile<K, TM>;
+        using T = LdsTile<K, TM>;
         const uint32_t base = lds_addr(&sh.tile[buf]), row = base + 2 * T::kPitch * r + 16 * g;
         const uint32_t ap = base + offsetof(T, a) + 4 * T::kAPitch * r + 16 * g;  // rows of A and P are equally long
         static_assert(4 * T::kAPitch == 2 * T::kPPitch, "");
@@ -503,16 +558,17 @@ __device__ __forceinline__ void state_wave(const DeltaParams &p, const Chain &ch
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 kr[b] = lds_load<u32x4_t>(row + 32 * T::kPitch * b + 64 * e);
-                qr[b] = lds_load<u32x4_t>(row + kQ + 32 * T::kPitch * b + 64 * e);
+                if constexpr (OUT)
+                    qr[b] = lds_load<u32x4_t>(row + kQ + 32 * T::kPitch * b + 64 * e);
             }
 #pragma unroll
             for (int b = 0; b < NB; ++b) u[b] = mfma(kr[b], s0, e > 0 ? u[b] : zero);
 #pragma unroll
-            for (int b = 0; b < NB; ++b) o[b] = mfma(s0, qr[b], e > 0 ? o[b] : zero);
+            for (int b = 0; OUT && b < NB; ++b) o[b] = mfma(s0, qr[b], e > 0 ? o[b] : zero);
 #pragma unroll
             for (int b = 0; b < NB; ++b) u[b] = mfma(kr[b], s1, u[b]);
 #pragma unroll
-            for (int b = 0; b < NB; ++b) o[b] = mfma(s1, qr[b], o[b]);
+            for (int b = 0; OUT && b < NB; ++b) o[b] = mfma(s1, qr[b], o[b]);
 #pragma unroll
             for (int b = 0; b < NB; ++b) u[b] = mfma(kr[b], s2, u[b]);
         }
@@ -597,42 +653,47 @@ __device__ __forceinline__ void state_wave(const DeltaParams &p, const Chain &ch
             for (int b = 0; b < NB; ++b) split<2>(u[b], up[b]);
         }
 
-        // out
+        if constexpr (OUT) {
+            // out
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            o[b] *= lds_load<float>(one + 64 * b);
+            for (int b = 0; b < NB; ++b) {
+                o[b] *= lds_load<float>(one + 64 * b);
 #pragma unroll
-            for (int e = 0; e <= b / 2; ++e) {
-                const uint32_t at = ap + kP + kPBlock * p_block(b, e);
-                if (2 * e + 1 <= b) {
+                for (int e = 0; 2 * e + 1 <= b; ++e) {
+                    const uint32_t at = ap + kP + kPBlock * p_block(b, e);
                     const u32x4_t p0 = lds_load<u32x4_t>(at), p1 = lds_load<u32x4_t>(at + kPart);
                     const u32x4_t u0 = cat(up[2 * e][0], up[2 * e + 1][0]), u1 = cat(up[2 * e][1], up[2 * e + 1][1]);
                     o[b] = mfma(u0, p0, o[b]);
                     o[b] = mfma(u1, p0, o[b]);
                     o[b] = mfma(u0, p1, o[b]);
-                } else {
+                }
+                if (b % 2 == 0) {
+                    // the block that is left, in a sum of its own: a product over 16 slots right behind one over 32
+                    // on the same accumulator, which the compiler does not keep apart, gave wrong sums
+                    const uint32_t at = ap + kP + kPBlock * p_block(b, b / 2);
                     const u32x2_t p0 = lds_load<u32x2_t>(at), p1 = lds_load<u32x2_t>(at + kPart);
-                    o[b] = mfma16(up[2 * e][0], p0, o[b]);
-                    o[b] = mfma16(up[2 * e][1], p0, o[b]);
-                    o[b] = mfma16(up[2 * e][0], p1, o[b]);
+                    f32x4_t x = mfma16(up[b][0], p0, zero);
+                    x = mfma16(up[b][1], p0, x);
+                    x = mfma16(up[b][0], p1, x);
+                    o[b] += x;
+                }
+                o[b] *= p.scale;
+            }
+            if (poisoned) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int from = __shfl(poison, here(4 * g) + i);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) o[b][i] = 16 * b + here(r) >= from ? __builtin_nanf("") : o[b][i];
                 }
             }
-            o[b] *= p.scale;
+            uint16_t *op = obase + (t0 + here(r)) * ostride + here(4 * g);
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                if (16 * b + r < left)
+                    *reinterpret_cast<u32x2_t *>(op + 16 * b * ostride) =
+                        u32x2_t{pack_bf16x2(o[b][0], o[b][1]), pack_bf16x2(o[b][2], o[b][3])};
         }
-        if (poisoned) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int from = __shfl(poison, here(4 * g) + i);
-#pragma unroll
-                for (int b = 0; b < NB; ++b) o[b][i] = 16 * b + here(r) >= from ? __builtin_nanf("") : o[b][i];
-            }
-        }
-        uint16_t *op = obase + (t0 + here(r)) * ostride + here(4 * g);
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-            if (16 * b + r < left)
-                *reinterpret_cast<u32x2_t *>(op + 16 * b * ostride) =
-                    u32x2_t{pack_bf16x2(o[b][0], o[b][1]), pack_bf16x2(o[b][2], o[b][3])};
         fence();
 
         // the state
@@ -665,38 +726,99 @@ __device__ __forceinline__ void state_wave(const DeltaParams &p, const Chain &ch
         lds_barrier();
     }
 
-    if (!p.final_state)
+    if (OUT && (!p.final_state || !ch.last))
         return;
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
-        if (p.final_kind == kFp32)
-            *reinterpret_cast<f32x4_t *>(static_cast<float *>(p.final_state) + place(t)) = s[t];
+        if (!OUT)
+            *reinterpret_cast<f32x4_t *>(p.slabs + slab_row(p, ch.slab + ch.index + 1, ch.h, col + r) + place(t)) = s[t];
+        else if (p.final_kind == kFp32)
+            *reinterpret_cast<f32x4_t *>(static_cast<float *>(p.final_state) + own + place(t)) = s[t];
         else
-            *reinterpret_cast<u32x2_t *>(static_cast<uint16_t *>(p.final_state) + place(t)) =
+            *reinterpret_cast<u32x2_t *>(static_cast<uint16_t *>(p.final_state) + own + place(t)) =
                 u32x2_t{pack_bf16x2(s[t][0], s[t][1]), pack_bf16x2(s[t][2], s[t][3])};
     }
 }
 
-template <int K, int TM>
+template <int K, int TM, bool OUT>
 __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(DeltaParams p, int vblocks, int columns)
 {
     __shared__ __align__(16) Shared<K, TM> sh;
     static_assert(sizeof(sh) <= 160 * 1024, "LDS of a compute unit");
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const Chain ch = find_chain(p, vblocks, columns);
+    const Chain ch = find_chain(p, static_cast<int>(OUT ? p.V : p.V + p.K), vblocks, columns);
+    // own states: of all segments but a sequence's last; what the first one makes of unit vectors is not asked
+    if (!ch.valid || (!OUT && (ch.last || (ch.index == 0 && ch.col0 >= p.V))))
+        return;
     if (wave >= kStateWaves) {
         if (ch.tokens > 0) {
-            Producer<K, TM> producer(p, ch, tid - 64 * kStateWaves, wave - kStateWaves);
+            Producer<K, TM, OUT> producer(p, ch, tid - 64 * kStateWaves, wave - kStateWaves);
             producer.run(sh);
         }
-    } else if (16 * wave < ch.width) {
-        state_wave<K, TM>(p, ch, sh, tid & 63, wave);
+    } else if (16 * wave < ch.width && (OUT || ch.index > 0 || ch.col0 + 16 * wave < p.V)) {
+        state_wave<K, TM, OUT>(p, ch, sh, tid & 63, wave);
     } else {
         // a wave without columns keeps the others' count of barriers: two a tile and two before
         for (int t0 = -TM; t0 < ch.tokens && ch.tokens > 0; t0 += TM) {
             lds_barrier();
             lds_barrier();
         }
+    }
+}
+
+// The states that segments start with, one after the other: the end of segment j is
+// its own state plus what it makes of the end of the one before,
+//   S_j[v, :] <- S_j[v, :] + sum_k S_(j-1)[v, k] M_j[k, :]
+// in fp32 throughout.  A workgroup takes 16 rows v of a chain, a wave 16 of its K
+// columns, in v_mfma_f32_16x16x4_f32: rows of the result are columns of M, and the
+// state before, shared in LDS, is the right factor.
+template <int K>
+__global__ __launch_bounds__(4 * K) void delta_join_kernel(DeltaParams p)
+{
+    constexpr int KT = K / 16;
+    __shared__ __align__(16) float before[2][16][K + 4];
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t vblocks = static_cast<uint32_t>(p.V / 16), chain = blockIdx.x / vblocks, v0 = 16 * (blockIdx.x - chain * vblocks);
+    const uint32_t n = chain / static_cast<uint32_t>(p.H);
+    const int64_t h = chain - n * static_cast<uint32_t>(p.H);
+    const uint32_t seg = static_cast<uint32_t>(p.seg), begin = p.seqs.cu ? clamp_offset(p.seqs, n) : 0,
+                   end = p.seqs.cu ? clamp_offset(p.seqs, n + 1) : static_cast<uint32_t>(p.seqs.T);
+    const uint32_t count = end > begin ? (end - begin + seg - 1) / seg : 0;
+    if (count < 3)
+        return;
+    const int64_t first = p.map.mul * (begin / seg) + p.map.add * n;
+    const auto at = [&](uint32_t j) { return reinterpret_cast<f32x4_t *>(p.slabs + slab_row(p, first + j, h, v0 + r) + 16 * wave + 4 * g); };
+    // M a step ahead, where the registers hold it
+    constexpr bool kAhead = K <= 128;
+    float m[kAhead ? KT : 1][4];
+    const auto map = [&](uint32_t j) { return p.slabs + slab_row(p, first + j, h, p.V + 4 * g) + 16 * wave + r; };
+    const auto load = [&](uint32_t j) {
+        const float *src = map(j);
+#pragma unroll
+        for (int t = 0; t < (kAhead ? KT : 0); ++t, src += 16 * K)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m[t][i] = src[i * K];
+    };
+    f32x4_t s = *at(1), next = *at(2);
+    load(2);
+    int buf = 0;
+    for (uint32_t j = 2; j < count; ++j, buf ^= 1) {
+        *reinterpret_cast<f32x4_t *>(&before[buf][r][16 * wave + 4 * g]) = s;
+        lds_barrier();
+        s = next;
+        const float *src = map(j);
+#pragma unroll(kAhead ? KT : 2)
+        for (int t = 0; t < KT; ++t, src += 16 * K) {
+            const f32x4_t x = *reinterpret_cast<const f32x4_t *>(&before[buf][r][16 * t + 4 * g]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s = __builtin_amdgcn_mfma_f32_16x16x4f32(kAhead ? m[kAhead ? t : 0][i] : src[i * K], x[i], s, 0, 0, 0);
+        }
+        if (j + 1 < count) {
+            load(j + 1);
+            next = *at(j + 1);
+        }
+        *at(j) = s;
     }
 }
 
@@ -707,23 +829,40 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_kernel(DeltaParams p, in
 // one of 8191 tokens with 12 heads of 64 x 96 128 columns take 567 us, 48 417, 32
 // 404 and 16 391; of 19595 tokens in 8 sequences with 32 heads of 128 x 128 128
 // take 430, 64 396 and 32 638; of 8 x 16384 128 take 1690, 64 2070.
-int columns_of(const DeltaParams &p)
+int columns_of(int64_t chains, int64_t all, bool packed)
 {
-    const int64_t chains = p.seqs.N * p.H, most = p.seqs.cu ? 512 : 256;
+    const int64_t most = packed ? 512 : 256;
     int columns = 16;
-    while (columns < kColumns && columns < p.V && chains * ((p.V + columns - 1) / columns) > most) columns *= 2;
-    return columns < p.V ? columns : static_cast<int>(p.V);
+    while (columns < kColumns && columns < all && chains * ((all + columns - 1) / columns) > most) columns *= 2;
+    return columns < all ? columns : static_cast<int>(all);
+}
+
+template <int K, int TM, bool OUT>
+hipError_t launch_pass(const DeltaParams &p, int64_t slots, hipStream_t stream)
+{
+    const int64_t all = OUT ? p.V : p.V + p.K;
+    const int columns = columns_of(slots * p.H, all, p.seqs.cu && p.seg == 0);
+    const int64_t vblocks = (all + columns - 1) / columns, blocks = slots * p.H * vblocks;
+    if (!grid_fits(blocks, kThreads))
+        return hipErrorInvalidConfiguration;
+    delta_chunk_kernel<K, TM, OUT><<<dim3(static_cast<uint32_t>(blocks)), dim3(kThreads), 0, stream>>>(p, static_cast<int>(vblocks), columns);
+    return hipGetLastError();
 }
 
 template <int K, int TM>
 hipError_t launch(const DeltaParams &p, hipStream_t stream)
 {
-    const int columns = columns_of(p);
-    const int64_t vblocks = (p.V + columns - 1) / columns, blocks = p.seqs.N * p.H * vblocks;
-    if (!grid_fits(blocks, kThreads))
-        return hipErrorInvalidConfiguration;
-    delta_chunk_kernel<K, TM><<<dim3(static_cast<uint32_t>(blocks)), dim3(kThreads), 0, stream>>>(p, static_cast<int>(vblocks), columns);
-    return hipGetLastError();
+    if (p.seg == 0)
+        return launch_pass<K, TM, true>(p, p.seqs.N, stream);
+    const int64_t slots = tile_slots(p.seqs, p.seg), joins = p.seqs.N * p.H * (p.V / 16);
+    if (!grid_fits(joins, 4 * K) || !grid_fits(slots * p.H * ((p.V + p.K + 15) / 16), kThreads))
+        return hipErrorInvalidConfiguration;  // before anything is enqueued
+    hipError_t e = launch_pass<K, TM, false>(p, slots, stream);
+    if (e != hipSuccess)
+        return e;
+    delta_join_kernel<K><<<dim3(static_cast<uint32_t>(joins)), dim3(4 * K), 0, stream>>>(p);
+    e = hipGetLastError();
+    return e != hipSuccess ? e : launch_pass<K, TM, true>(p, slots, stream);
 }
 
 }  // namespace

@@ -256,6 +256,76 @@ extern "C" kda_status kda_ssm_fwd(const kda_ssm_args *args, void *stream)
     return launched(kda::layer::launch_ssm_chunk(p, static_cast<hipStream_t>(stream)));
 }
 
+namespace {
+
+// Sizes of a delta rule call: KDA_OK and the sequences, or what is wrong.
+kda_status check_delta_sizes(const kda_delta_args &a, Seqs *s)
+{
+    if ((a.K != 64 && a.K != 128 && a.K != 256) || a.V < 16 || a.V > kDeltaMaxV || a.V % 16 != 0 || a.seg_tokens < 0 ||
+        a.seg_tokens % kDeltaTile != 0)
+        return KDA_ERR_SHAPE;
+    if (a.H < 1 || a.H > 65536 || a.T > kDeltaMaxTokens)
+        return KDA_ERR_SIZE;
+    if (a.G < 1 || a.H % a.G != 0)
+        return KDA_ERR_SHAPE;
+    const kda_status st = check_seqs(a.cu_seqlens, a.num_seqs, a.B, a.T, s);
+    int64_t rows, n;
+    if (st == KDA_OK && (!mul_ok(a.B, a.T, &rows) || !mul_ok(rows, a.H * a.V * 2, &n) ||
+                         !mul_ok(s->N, a.H * a.K * a.V * 4, &n) || s->N * a.H > INT32_MAX))
+        return KDA_ERR_SIZE;
+    return st;
+}
+
+// How a delta rule call with valid sizes runs.
+struct DeltaPlan {
+    bool recurrent = false;
+    int64_t seg = 0;  // tokens a segment (chunked kernel), 0: whole sequences
+    kda::layer::SlabMap map = {};
+    int64_t bytes = 0;  // workspace
+};
+
+// Calls without cu_seqlens of up to kDeltaRecurrentMaxTokens tokens: the token
+// recurrence.  Of the others, few chains are cut into segments: as many as leave
+// no compute unit of 256 a second workgroup in the pass over own states, which has
+// V + K columns, 128 a workgroup.  Segments cost that pass, so there have to be
+// four for each sequence at least, and of eight tiles.  False if the workspace
+// overflows.
+bool delta_plan(const kda_delta_args &a, const Seqs &s, DeltaPlan *plan)
+{
+    constexpr int64_t kTarget = 256, kLeast = 4, kColumns = 128, kShortest = 8 * kDeltaTile;
+    if (!s.cu && s.T <= kDeltaRecurrentMaxTokens) {
+        plan->recurrent = true;
+        return true;
+    }
+    int64_t seg = a.seg_tokens;
+    if (seg == 0) {
+        const int64_t parts = kTarget / (a.H * ((a.V + a.K + kColumns - 1) / kColumns));  // segments in all
+        if (s.N < 1 || parts < kLeast * s.N)
+            return true;
+        const int64_t all = s.cu ? parts : parts / s.N;
+        seg = std::max(((s.T + all - 1) / all + kDeltaTile - 1) / kDeltaTile * kDeltaTile, kShortest);
+        if (s.T < kLeast * seg)
+            return true;
+    }
+    if (seg >= s.T)
+        return true;
+    plan->seg = seg;
+    plan->map = kda::layer::slab_map(s, seg);
+    int64_t n;
+    return mul_ok(a.H * (a.V + a.K), a.K * 4, &n) && mul_ok(plan->map.slabs, n, &plan->bytes);
+}
+
+}  // namespace
+
+extern "C" int64_t kda_delta_workspace_bytes(const kda_delta_args *args)
+{
+    Seqs s;
+    DeltaPlan plan;
+    if (!args || check_delta_sizes(*args, &s) != KDA_OK || !delta_plan(*args, s, &plan))
+        return -1;
+    return plan.bytes;
+}
+
 extern "C" kda_status kda_delta_fwd(const kda_delta_args *args, void *stream)
 {
     if (!args)
@@ -263,24 +333,18 @@ extern "C" kda_status kda_delta_fwd(const kda_delta_args *args, void *stream)
     const kda_delta_args &a = *args;
     if (a.reserved != 0)
         return KDA_ERR_OPTION;
-    if ((a.K != 64 && a.K != 128 && a.K != 256) || a.V < 16 || a.V > kDeltaMaxV || a.V % 16 != 0)
-        return KDA_ERR_SHAPE;
-    if (a.H < 1 || a.H > 65536 || a.T > kDeltaMaxTokens)
-        return KDA_ERR_SIZE;
-    if (a.G < 1 || a.H % a.G != 0)
-        return KDA_ERR_SHAPE;
-    if (!std::isfinite(a.scale) || !fp32_scale(a.scale))
-        return KDA_ERR_SCALE;
     DeltaParams p = {};
-    kda_status st = check_seqs(a.cu_seqlens, a.num_seqs, a.B, a.T, &p.seqs);
+    kda_status st = check_delta_sizes(a, &p.seqs);
+    if (st == KDA_OK && (!std::isfinite(a.scale) || !fp32_scale(a.scale)))
+        st = KDA_ERR_SCALE;
     if (st == KDA_OK)
         st = check_states(a.initial_state, a.initial_state_dtype, a.final_state, a.final_state_dtype);
     if (st != KDA_OK)
         return st;
-    int64_t tokens, n;
-    if (!mul_ok(a.B, a.T, &tokens) || !mul_ok(tokens, a.H * a.V * 2, &n) ||
-        !mul_ok(p.seqs.N, a.H * a.K * a.V * 4, &n) || p.seqs.N * a.H > INT32_MAX)
+    DeltaPlan plan;
+    if (!delta_plan(a, p.seqs, &plan))
         return KDA_ERR_SIZE;
+    const int64_t tokens = a.B * a.T;
     const int64_t state = p.seqs.N * a.H * a.K * a.V;
     int64_t nq, nk, nv, ng, nb;
     if (!extent(a.B, a.q_stride_b, a.T, a.q_stride_t, a.G * a.K, 2, &nq) ||
@@ -289,8 +353,7 @@ extern "C" kda_status kda_delta_fwd(const kda_delta_args *args, void *stream)
         !extent(a.B, a.g_stride_b, a.T, a.g_stride_t, a.H, 2, &ng) ||
         !extent(a.B, a.beta_stride_b, a.T, a.beta_stride_t, a.H, 2, &nb))
         return KDA_ERR_STRIDE;
-    const bool recurrent = !a.cu_seqlens && a.T <= kDeltaRecurrentMaxTokens;
-    if (!recurrent && a.T > 1 &&
+    if (!plan.recurrent && a.T > 1 &&
         (a.q_stride_t > kDeltaMaxStride || a.k_stride_t > kDeltaMaxStride || a.v_stride_t > kDeltaMaxStride ||
          a.g_stride_t > kDeltaMaxStride || a.beta_stride_t > kDeltaMaxStride))
         return KDA_ERR_STRIDE;
@@ -308,6 +371,9 @@ extern "C" kda_status kda_delta_fwd(const kda_delta_args *args, void *stream)
         misaligned(a.out, 16) || misaligned(a.initial_state, 16) || misaligned(a.final_state, 16) ||
         misaligned(a.A_log, 4) || misaligned(a.dt_bias, 4) || misaligned(a.cu_seqlens, 8))
         return KDA_ERR_ALIGNMENT;
+    if (plan.bytes > 0 && (!a.workspace || a.workspace_bytes < plan.bytes || misaligned(a.workspace, 16) ||
+                           any_overlap(span(a.workspace, plan.bytes), {sq, sk, sv, sg, sb, sA, sd, su, so, si, sf})))
+        return KDA_ERR_WORKSPACE;
     if (p.seqs.N == 0 || (tokens == 0 && !a.final_state))
         return KDA_OK;
     p.q = static_cast<const uint16_t *>(a.q);
@@ -337,7 +403,10 @@ extern "C" kda_status kda_delta_fwd(const kda_delta_args *args, void *stream)
     p.K = a.K;
     p.V = a.V;
     p.scale = static_cast<float>(a.scale);
-    return launched((recurrent ? launch_delta_recurrent : launch_delta_chunk)(p, static_cast<hipStream_t>(stream)));
+    p.seg = plan.seg;
+    p.map = plan.map;
+    p.slabs = static_cast<float *>(a.workspace);
+    return launched((plan.recurrent ? launch_delta_recurrent : launch_delta_chunk)(p, static_cast<hipStream_t>(stream)));
 }
 
 extern "C" kda_status kda_gated_norm(const kda_gated_norm_args *args, void *stream)

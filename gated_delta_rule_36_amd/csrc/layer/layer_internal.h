@@ -163,7 +163,14 @@ struct DeltaParams {
     Seqs seqs;
     int64_t H, G, K, V;
     float scale;
+    // the chunked kernel: tokens a segment, 0 for whole sequences; of segments the
+    // slabs [H, V + K, K] (see slab_map; nullptr where every sequence is one segment)
+    int64_t seg;
+    SlabMap map;
+    float *slabs;
 };
+// Segments are multiples of this many tokens.
+constexpr int64_t kDeltaTile = 64;
 hipError_t launch_delta_recurrent(const DeltaParams &p, hipStream_t stream);
 hipError_t launch_delta_chunk(const DeltaParams &p, hipStream_t stream);
 constexpr int64_t kDeltaMaxV = 512;

@@ -149,6 +149,25 @@ def _call(name, values, device, args=None):
         raise (KdaError if status == _lib.KDA_ERR_LAUNCH else KdaArgumentError)(status)
 
 
+def _call_with_workspace(name, size, values, device):
+    """Enqueue `values`, whose last fields, the workspace, are left out; `size` names the function that tells its bytes."""
+    workspace_bytes, pack = _entry(size)
+    args = _pack(pack, values + (0, 0))
+    nbytes = workspace_bytes(args)
+    if nbytes > 0:
+        # freed right after the call: the caching allocator hands it out
+        # again only to work ordered after this call on the same stream
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        args = _pack(pack, values + (workspace.data_ptr(), nbytes))
+    _call(name, None, device, args)
+
+
+def _segment_tokens(n):
+    """None, or a positive number of tokens."""
+    if n is not None and (not isinstance(n, int) or isinstance(n, bool) or n < 1):
+        raise ValueError(f"segment_tokens must be a positive int or None, got {n!r}")
+
+
 def short_conv(x: torch.Tensor, weight: torch.Tensor, out: torch.Tensor,
                bias: Optional[torch.Tensor] = None, *, activation: Optional[str] = "silu",
                l2norm: Optional[int] = None, l2norm_eps: float = 1e-6,
@@ -235,27 +254,18 @@ def ssm_fwd(x: torch.Tensor, dt: torch.Tensor, b: torch.Tensor, c: torch.Tensor,
     pu, num, seqs = _sequences(cu_seqlens, device, B, T, check_cu_seqlens)
     pi, icode = _typed("initial_state", initial_state, device, (seqs, H, P, N))
     pf, fcode = _typed("final_state", final_state, device, (seqs, H, P, N))
-    if segment_tokens is not None and (not isinstance(segment_tokens, int) or isinstance(segment_tokens, bool)
-                                       or segment_tokens < 1):
-        raise ValueError(f"segment_tokens must be a positive int or None, got {segment_tokens!r}")
+    _segment_tokens(segment_tokens)
     values = (px, pd, pb, pc, pz, po, xb, xt, db, dtt, bb, bt, cb, ct, zb, zt, pA, pD, pt, pi, pf, pu,
               num, B, T, H, P, G, N, icode, fcode, 1 if dt_softplus else 0, 0, segment_tokens or 0)
-    workspace_bytes, pack = _entry("kda_ssm_workspace_bytes")
-    args = _pack(pack, values + (0, 0))
-    nbytes = workspace_bytes(args)
-    if nbytes > 0:
-        # freed right after the call: the caching allocator hands it out
-        # again only to work ordered after this call on the same stream
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        args = _pack(pack, values + (workspace.data_ptr(), nbytes))
-    _call("kda_ssm_fwd", values, device, args)
+    _call_with_workspace("kda_ssm_fwd", "kda_ssm_workspace_bytes", values, device)
     return out
 
 
 def delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor, scale: float,
               out: torch.Tensor, A_log: torch.Tensor, dt_bias: Optional[torch.Tensor] = None, *,
               initial_state: Optional[torch.Tensor] = None, final_state: Optional[torch.Tensor] = None,
-              cu_seqlens: Optional[torch.Tensor] = None, check_cu_seqlens: bool = True) -> torch.Tensor:
+              cu_seqlens: Optional[torch.Tensor] = None, check_cu_seqlens: bool = True,
+              segment_tokens: Optional[int] = None) -> torch.Tensor:
     """Gated delta rule with one decay per head; writes ``out`` (and ``final_state``).
 
     Per head, with a state S of [K, V]: ``S = exp(-exp(A_log) softplus(g + dt_bias)) S``,
@@ -267,7 +277,9 @@ def delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor
     ``dt_bias`` fp32 ``[H]``.  K is 64, 128 or 256, V a multiple of 16 up to
     512.  The states are ``[N, H, V, K]`` (sequences first) in bf16 or fp32 and
     may be one buffer.  ``cu_seqlens`` and ``check_cu_seqlens`` are those of
-    :func:`fwd`.
+    :func:`fwd`.  ``segment_tokens`` (a multiple of 64) cuts long sequences
+    into segments that run in parallel, for few heads; None lets the library
+    choose.  The workspace is a temporary allocation on the same stream.
     """
     device = _device(v, "v")
     if v.dim() != 4:
@@ -289,8 +301,10 @@ def delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor
     pu, num, seqs = _sequences(cu_seqlens, device, B, T, check_cu_seqlens)
     pi, icode = _typed("initial_state", initial_state, device, (seqs, H, V, K))
     pf, fcode = _typed("final_state", final_state, device, (seqs, H, V, K))
-    _call("kda_delta_fwd", (pq, pk, pv, pg, pb, po, qb, qt, kb, kt, vb, vt, gb, gt, bb, bt, pA, pt, pi, pf, pu, num,
-                            B, T, H, G, K, V, icode, fcode, 0, scale), device)
+    _segment_tokens(segment_tokens)
+    values = (pq, pk, pv, pg, pb, po, qb, qt, kb, kt, vb, vt, gb, gt, bb, bt, pA, pt, pi, pf, pu, num,
+              B, T, H, G, K, V, icode, fcode, 0, scale, segment_tokens or 0)
+    _call_with_workspace("kda_delta_fwd", "kda_delta_workspace_bytes", values, device)
     return out
 
 

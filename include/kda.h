@@ -556,8 +556,17 @@ kda_status kda_residual_norm(const kda_residual_norm_args *args, void *stream);
  *                  (KDA_ERR_SIZE otherwise).
  *   K              64, 128 or 256; V a multiple of 16, at most 512
  *                  (KDA_ERR_SHAPE otherwise).
- *   Token strides are at most 2^24 elements where more than 8 tokens are
- *   given, or packed ones (KDA_ERR_STRIDE otherwise).
+ *   seg_tokens     tokens a segment: sequences longer than that are cut into
+ *                  segments that run in parallel, joined in fp32 (a segment
+ *                  maps the state it starts with to M S + b).  0 lets the
+ *                  library choose from the sizes; otherwise a multiple of 64
+ *                  (KDA_ERR_SHAPE).
+ *   workspace, workspace_bytes   DEVICE scratch, 16-byte aligned, at least
+ *                  kda_delta_workspace_bytes(args) bytes (which may be 0), as
+ *                  for kda_fwd_scan (KDA_ERR_WORKSPACE otherwise).
+ * Calls without cu_seqlens of at most 8 tokens run token by token, whatever
+ * seg_tokens is.  In the others token strides are at most 2^24 elements
+ * (KDA_ERR_STRIDE otherwise).
  *
  * A non-finite q reaches its own token's output alone; a non-finite k, v, g or
  * beta reaches outputs of its head (k: its group's heads) from its own token
@@ -584,8 +593,18 @@ typedef struct kda_delta_args {
     int32_t initial_state_dtype, final_state_dtype; /* kda_dtype */
     int64_t reserved;
     double scale;
+    int64_t seg_tokens;
+    void *workspace;
+    int64_t workspace_bytes;
 } kda_delta_args;
 kda_status kda_delta_fwd(const kda_delta_args *args, void *stream);
+
+/*
+ * Bytes of workspace kda_delta_fwd needs for these sizes, cu_seqlens (tested
+ * for NULL, never read) and seg_tokens; the pointers to tensors are ignored.
+ * -1 where the sizes are ones kda_delta_fwd refuses.
+ */
+int64_t kda_delta_workspace_bytes(const kda_delta_args *args);
 
 /* -------------------------------------------------------------------------
  * The attention layers that a hybrid model alternates with recurrent ones:
