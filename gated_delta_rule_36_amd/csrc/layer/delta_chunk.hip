@@ -205,6 +205,20 @@ __device__ __forceinline__ Chain find_chain(const DeltaParams &p, int all, int v
     c.width = all - c.col0 < columns ? all - c.col0 : columns;
     if (p.seg == 0) {
         c.n = slot;
+        if (p.seqs.cu && p.seqs.N <= kLaneSequences) {
+            // the longest sequences first, so that the last workgroups to end are short ones: the lane whose
+            // sequence as many others come before as the slot says
+            const uint32_t lane = __lane_id();
+            const LaneSequence q = lane_sequence(p.seqs, 1, lane);
+            const int length = lane < p.seqs.N ? static_cast<int>(q.end - q.begin) : -1;
+            int rank = 0;
+            for (int m = 0; m < static_cast<int>(p.seqs.N); ++m) {
+                const int other = __builtin_amdgcn_readlane(length, m);
+                rank += other > length || (other == length && m < static_cast<int>(lane));
+            }
+            const uint64_t found = __ballot(lane < p.seqs.N && rank == static_cast<int>(slot));
+            c.n = found ? __builtin_ctzll(found) : 0;
+        }
         c.row = p.seqs.cu ? 0 : c.n;
         c.begin = p.seqs.cu ? static_cast<int>(clamp_offset(p.seqs, c.n)) : 0;
         const int end = p.seqs.cu ? static_cast<int>(clamp_offset(p.seqs, c.n + 1)) : static_cast<int>(p.seqs.T);
