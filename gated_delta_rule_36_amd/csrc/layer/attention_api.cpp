@@ -240,23 +240,49 @@ kda_status check_attention_sizes(const kda_attention_args &a)
     return KDA_OK;
 }
 
-// Tokens a split: the same for all sequences, so that waves do the same work
-// however lengths differ, and as many splits as make kTarget waves if every
-// sequence were as long as its table allows.  Short contexts go in one split,
-// which needs neither a workspace nor a second launch; a workgroup shares it.
-constexpr int64_t kTarget = 32768, kFewest = 4 * kAttentionTile, kShared = 1024;
+// How the tokens of a sequence are cut into splits, by sizes alone (a context is
+// taken as long as its table allows, or its window).  Times in us, 128 channels.
+// - At most kShared tokens: one split, shared by a workgroup's four waves, and
+//   neither a workspace nor a second launch.
+// - pairs (of a sequence and up to 16 query heads of a key head) times tokens
+//   below kFew: kGroups splits over all, of one workgroup's four waves each, of
+//   at most kSharedMost tokens.  A wave alone on as many: 1 x 131071 tokens, 2 key heads
+//   40 (shared 37), 1 x 16384 19 (15), 4 x 65536 30 (26), 8 x 16384 of 4 key heads 21
+//   (19).  Splits of 1024: 38, 26, 30, 27.
+// - Above: one split a wave, whose neighbours take the other key heads of the
+//   same tokens and so read whole rows of the cache between them.  16 x 32768, 8 key heads 42
+//   (shared 44).  As many splits as make kTarget waves: 64 x 131072 tokens at the
+//   most, 8 key heads, for 8192 / 16384 / 32768 / 65536 waves 1034 / 886 / 826 / 857.
+//   All splits have the same size, so that waves do the same work however lengths
+//   differ; the same number of splits for every sequence took 991.
+constexpr int64_t kTarget = 32768, kFewest = 4 * kAttentionTile;
+constexpr int64_t kShared = 1024, kSharedMost = 512, kGroups = 512, kFew = 327680;
 int64_t longest(const kda_attention_args &a)
 {
     const int64_t room = a.table_width * a.page_size;
     return a.window > 0 && a.window < room ? a.window : room;
+}
+int64_t attention_pairs(const kda_attention_args &a)
+{
+    return a.N * a.Hk * ((a.Hq / a.Hk + kAttentionRows - 1) / kAttentionRows);
+}
+// Whether a workgroup's waves share a split.
+bool attention_shared(const kda_attention_args &a)
+{
+    const int64_t most = longest(a);
+    return most <= kShared || attention_pairs(a) * most < kFew;
 }
 int64_t attention_chunk(const kda_attention_args &a)
 {
     const int64_t most = longest(a);
     if (most <= kShared)
         return kShared;
-    const int64_t pairs = a.N * a.Hk * ((a.Hq / a.Hk + kAttentionRows - 1) / kAttentionRows);
-    const int64_t parts = std::max(int64_t(1), kTarget / std::max(int64_t(1), pairs));
+    if (attention_shared(a)) {
+        constexpr int64_t kStep = 4 * kAttentionTile;
+        const int64_t chunk = (attention_pairs(a) * most + kGroups - 1) / kGroups;
+        return std::min(kSharedMost, (chunk + kStep - 1) / kStep * kStep);
+    }
+    const int64_t parts = std::max(int64_t(1), kTarget / std::max(int64_t(1), attention_pairs(a)));
     const int64_t chunk = std::max((most + parts - 1) / parts, kFewest);
     return (chunk + kAttentionTile - 1) / kAttentionTile * kAttentionTile;
 }
@@ -343,7 +369,7 @@ extern "C" kda_status kda_paged_attention(const kda_attention_args *args, void *
     }
     p.splits = attention_splits(a);
     p.chunk = static_cast<int>(attention_chunk(a));
-    p.shared = p.splits == 1 && longest(a) <= kShared;
+    p.shared = attention_shared(a);
     p.scale = static_cast<float>(a.scale);
     if (p.splits > 1) {
         p.part = static_cast<float *>(a.workspace);
