@@ -343,15 +343,15 @@ extern "C" const char *kda_status_string(kda_status status)
     case KDA_ERR_VARLEN_BATCH: return "cu_seqlens requires B == 1 and num_seqs >= 0";
     case KDA_ERR_STATE_DTYPE: return "state dtype must be bf16 or fp32, and match between initial and final";
     case KDA_ERR_ALIAS: return "an output buffer overlaps an input buffer";
-    case KDA_ERR_SIZE: return "bad size (B >= 1, 1 <= H <= 65536, 0 <= T < 2^31, T < 2^31 - 128 for ssm_fwd, rows >= 0, gate_period >= 1, no int64 overflow, no grid beyond 2^32 threads)";
-    case KDA_ERR_SCALE: return "scale must be finite; for the layer operators eps must be finite and >= 0, and residual_scale and block_scale 0 or normal in fp32";
+    case KDA_ERR_SIZE: return "bad size (B >= 1, 1 <= H <= 65536, 0 <= T < 2^31, T < 2^31 - 128 for ssm_fwd and delta_fwd, rows >= 0, gate_period >= 1, window >= 0, page tables for fewer than 2^31 - 65536 tokens, no int64 overflow, no grid beyond 2^32 threads)";
+    case KDA_ERR_SCALE: return "scale must be finite; for the layer operators eps must be finite and >= 0, and residual_scale, block_scale, rotary_scale and the scales of delta_fwd and paged_attention 0 or normal in fp32";
     case KDA_ERR_LAUNCH: return "the HIP runtime rejected the kernel launch";
     case KDA_ERR_WORKSPACE: return "workspace is NULL, not 16-byte aligned, too small, or overlaps a tensor";
-    case KDA_ERR_ALIGNMENT: return "a tensor pointer is misaligned (q, k, v, g, out, states, residual_out: 16 bytes; beta and the layer operators' bf16 inputs 2; A_log, D, dt_bias and fp32 inputs 4; cu_seqlens 8)";
+    case KDA_ERR_ALIGNMENT: return "a tensor pointer is misaligned (q, k, v, g, out, states, residual_out: 16 bytes; beta and the layer operators' bf16 inputs 2; A_log, D, dt_bias, lse, page tables, lengths and fp32 inputs 4; positions, slots and cu_seqlens 8)";
     case KDA_ERR_OPTION: return "invalid options: unknown value, non-zero reserved field, or a kernel / inverse / sigmoid combination not implemented for this call";
     case KDA_ERR_SHAPE: return "a width, head, state, group or norm size is not a supported one";
     case KDA_ERR_DTYPE: return "weights, gates and residual streams must be bf16 or fp32";
-    case KDA_ERR_STRIDE: return "a stride is negative, its extent overflows int64, or a token stride of ssm_fwd is above 2^27 (x, b, c) or 2^26 (z) elements";
+    case KDA_ERR_STRIDE: return "a stride is negative, its extent overflows int64, a token stride of ssm_fwd is above 2^27 (x, b, c) or 2^26 (z) elements or of delta_fwd above 2^24, or places of a cache to be written share memory";
     }
     return "unknown status";
 }

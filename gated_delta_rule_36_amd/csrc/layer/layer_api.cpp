@@ -284,16 +284,22 @@ struct DeltaPlan {
     int64_t bytes = 0;  // workspace
 };
 
-// Calls without cu_seqlens of up to kDeltaRecurrentMaxTokens tokens: the token
-// recurrence.  Of the others, few chains are cut into segments: as many as leave
+// The token recurrence, against the chunked kernel, in us for 32 heads of 128 and fp32 states:
+// - up to kDeltaRecurrentMaxTokens tokens a sequence.  64 sequences of 1 / 4 / 8 / 12 / 16
+//   tokens 45 / 56 / 82 / 110 / 137 (chunked 113 / 111 / 114 / 114 / 117), 8 of them
+//   12 / 12 / 15 / 19 / 24 (15 / 15 / 16 / 16 / 16).
+// - packed sequences, whose lengths the host does not know, of up to two tokens
+//   on average: 64 of 1 / 2 tokens 44 / 47 (133 / 134), one of 33 and 31 of 1 38 (66), one of
+//   64 and 63 of none 68 (75).
+// Of the others, few chains are cut into segments: as many as leave
 // no compute unit of 256 a second workgroup in the pass over own states, which has
 // V + K columns, 128 a workgroup.  Segments cost that pass, so there have to be
-// four for each sequence at least, and of eight tiles.  False if the workspace
-// overflows.
+// four for each sequence at least, and of eight tiles: 8191 tokens of 12 heads 391 us whole, 111 in
+// 10 segments.  False if the workspace overflows.
 bool delta_plan(const kda_delta_args &a, const Seqs &s, DeltaPlan *plan)
 {
     constexpr int64_t kTarget = 256, kLeast = 4, kColumns = 128, kShortest = 8 * kDeltaTile;
-    if (!s.cu && s.T <= kDeltaRecurrentMaxTokens) {
+    if (s.T <= (s.cu ? 2 * s.N : kDeltaRecurrentMaxTokens) && (a.seg_tokens == 0 || a.seg_tokens >= s.T)) {
         plan->recurrent = true;
         return true;
     }
@@ -353,7 +359,7 @@ extern "C" kda_status kda_delta_fwd(const kda_delta_args *args, void *stream)
         !extent(a.B, a.g_stride_b, a.T, a.g_stride_t, a.H, 2, &ng) ||
         !extent(a.B, a.beta_stride_b, a.T, a.beta_stride_t, a.H, 2, &nb))
         return KDA_ERR_STRIDE;
-    if (!plan.recurrent && a.T > 1 &&
+    if ((p.seqs.cu ? a.T > 1 : a.T > kDeltaRecurrentMaxTokens) &&  // one rule of sizes, whichever kernel runs
         (a.q_stride_t > kDeltaMaxStride || a.k_stride_t > kDeltaMaxStride || a.v_stride_t > kDeltaMaxStride ||
          a.g_stride_t > kDeltaMaxStride || a.beta_stride_t > kDeltaMaxStride))
         return KDA_ERR_STRIDE;

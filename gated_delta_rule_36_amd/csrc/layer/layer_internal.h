@@ -178,7 +178,7 @@ constexpr int64_t kDeltaMaxV = 512;
 // a sequence's end.  Token strides (elements) whose 64 rows of a tile stay
 // within 32 bits of bytes.
 constexpr int64_t kDeltaMaxTokens = INT32_MAX - 128, kDeltaMaxStride = int64_t(1) << 24;
-// Calls without cu_seqlens of at most this many tokens take the token recurrence.
+// Sequences of at most this many tokens take the token recurrence.
 constexpr int64_t kDeltaRecurrentMaxTokens = 8;
 
 // Channels of a head that the rotation kernels take.

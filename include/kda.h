@@ -62,17 +62,19 @@ typedef enum kda_status {
                                   T > 2^31-1, sizes overflow int64, or more
                                   than 2^31-1 (sequence, head) chains; the
                                   layer operators: also rows < 0, gate_period
-                                  < 1, a grid beyond 2^32 threads, or
-                                  kda_ssm_fwd's T >= 2^31 - 128 */
+                                  < 1, a grid beyond 2^32 threads, T >= 2^31
+                                  - 128 of kda_ssm_fwd and kda_delta_fwd,
+                                  window < 0, or page tables for more than
+                                  2^31 - 65537 tokens */
     KDA_ERR_SCALE = 8,         /* scale is not finite; the layer operators: eps is
                                   not finite or negative, or a scale is not 0
                                   or a normal number of fp32 */
     KDA_ERR_LAUNCH = 9,        /* the HIP runtime rejected the launch */
-    KDA_ERR_WORKSPACE = 10,    /* kda_fwd_scan, kda_ssm_fwd: workspace NULL,
-                                  not 16-byte aligned, smaller than
-                                  kda_fwd_scan_workspace_bytes() or
-                                  kda_ssm_workspace_bytes(), or
-                                  overlapping a tensor argument */
+    KDA_ERR_WORKSPACE = 10,    /* kda_fwd_scan, kda_ssm_fwd, kda_delta_fwd,
+                                  kda_paged_attention: workspace NULL, not
+                                  16-byte aligned, smaller than the call's
+                                  ..._workspace_bytes(), or overlapping a
+                                  tensor argument */
     KDA_ERR_ALIGNMENT = 11,    /* a non-NULL pointer is misaligned: q, k, v,
                                   g, out, initial_state and final_state need
                                   16 bytes, beta 2, A_log and dt_bias 4,
@@ -91,8 +93,10 @@ typedef enum kda_status {
     KDA_ERR_DTYPE = 14,        /* layer operators: a weight, gate or residual
                                   dtype that is neither bf16 nor fp32 */
     KDA_ERR_STRIDE = 15        /* layer operators: a negative stride, one
-                                  whose extent overflows int64, or a token
-                                  stride beyond kda_ssm_fwd's */
+                                  whose extent overflows int64, a token
+                                  stride beyond kda_ssm_fwd's or
+                                  kda_delta_fwd's, or a cache to be written
+                                  whose places share memory */
 } kda_status;
 
 /* Element type of initial_state / final_state (and of the layer operators'
@@ -565,8 +569,9 @@ kda_status kda_residual_norm(const kda_residual_norm_args *args, void *stream);
  *                  kda_delta_workspace_bytes(args) bytes (which may be 0), as
  *                  for kda_fwd_scan (KDA_ERR_WORKSPACE otherwise).
  * Calls without cu_seqlens of at most 8 tokens run token by token, whatever
- * seg_tokens is.  In the others token strides are at most 2^24 elements
- * (KDA_ERR_STRIDE otherwise).
+ * seg_tokens is, and packed ones of at most two a sequence on average unless
+ * seg_tokens cuts them.  With cu_seqlens, or more than 8 tokens, token strides
+ * are at most 2^24 elements (KDA_ERR_STRIDE otherwise).
  *
  * A non-finite q reaches its own token's output alone; a non-finite k, v, g or
  * beta reaches outputs of its head (k: its group's heads) from its own token
@@ -714,6 +719,7 @@ kda_status kda_append_kv(const kda_append_args *args, void *stream);
  *                  (KDA_ERR_SHAPE otherwise).
  *   scale          0 or a normal number of fp32 (KDA_ERR_SCALE otherwise).
  *   window         >= 0; 0 = every token (KDA_ERR_SIZE otherwise).
+ *   table_width    * page_size at most 2^31 - 65537 (KDA_ERR_SIZE otherwise).
  *   workspace, workspace_bytes   DEVICE scratch, 16-byte aligned, at least
  *                  kda_paged_attention_workspace_bytes(args) bytes (which may
  *                  be 0), as for kda_fwd_scan (KDA_ERR_WORKSPACE otherwise).

@@ -346,3 +346,37 @@ def test_segments_replay_from_a_graph():
         torch.cuda.synchronize()
         for o, f in ((out, fin), eager):
             assert torch.equal(o, want) and torch.equal(f, want_fin)
+
+
+# ---------------------------------------------------------------------------
+# many packed sequences
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("cu", [list(range(9)), [0, 1, 2, 5, 5, 8, 12, 14, 14], [3] * 20 + [40], [0] + [1 + i // 2 for i in range(80)]])
+@pytest.mark.parametrize("seg", [None, 64])
+def test_packed_single_tokens(cu, seg):
+    """A decoding step of packed requests: one or two tokens each, some of none, one of more; rows behind the last."""
+    T = cu[-1] + 2
+    hold(inputs(1, T, 2, 4, 128, 96, seed=T, n=len(cu) - 1), cu=cu, seg=seg)
+
+
+@pytest.mark.parametrize("state", [F32, BF])
+def test_more_packed_sequences_than_lanes(state):
+    cu = [0]
+    for i in range(70):
+        cu.append(cu[-1] + (i * 37) % 90 * (i % 3 != 1))
+    hold(inputs(1, cu[-1] + 3, 1, 2, 64, 32, seed=151, n=70, state=state), cu=cu, state=state)
+
+
+def test_segments_on_two_streams():
+    a, b = inputs(1, 600, 1, 2, 64, 32, seed=161), inputs(1, 470, 1, 2, 64, 32, seed=162)
+    want = [call(x, seg=64) for x in (a, b)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    for _ in range(10):
+        for s, x, o in zip(streams, (a, b), got):
+            with torch.cuda.stream(s):
+                o.append(call(x, seg=64))
+    torch.cuda.synchronize()
+    for w, o in zip(want, got):
+        assert all(torch.equal(w[0], y) and torch.equal(w[1], f) for y, f in o)

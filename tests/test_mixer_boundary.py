@@ -331,3 +331,42 @@ def test_rotation_and_cache_arguments():
                        (c.float(), TypeError), (None, TypeError)):
         with pytest.raises(error):
             _cache("c", bad, cpu, 2, 16)
+
+
+# --------------------------------------------------------------------------
+# workspaces and segments of the gated delta rule
+# --------------------------------------------------------------------------
+
+def delta_workspace(**over):
+    args = _lib.DeltaArgs(**{**DELTA, **over})
+    return _lib.load().kda_delta_workspace_bytes(ctypes.byref(args))
+
+
+def test_delta_workspace():
+    assert _lib.load().kda_delta_workspace_bytes(None) == -1
+    assert delta_workspace(K=32) == -1 and delta_workspace(T=-1) == -1 and delta_workspace(seg_tokens=48) == -1
+    assert delta_workspace(T=8, seg_tokens=64) == 0 and delta_workspace(T=64, seg_tokens=64) == 0
+    # of two segments: the end of the first and what it makes of K unit vectors; the second's end is the result
+    H, K, V = (DELTA[k] for k in "HKV")
+    slab = H * K * (V + K) * 4
+    assert delta_workspace(T=65, seg_tokens=64) % slab == 0 and delta_workspace(T=65, seg_tokens=64) > 0
+    assert delta_workspace(T=65, B=3, seg_tokens=64) == 3 * delta_workspace(T=65, seg_tokens=64)
+    # packed: at most two tokens a sequence need none, unless asked for segments
+    assert delta_workspace(T=200, cu_seqlens=A[9], num_seqs=100) == 0
+    assert delta_workspace(T=200, cu_seqlens=A[9], num_seqs=100, seg_tokens=64) > 0
+    # long sequences of few heads are cut without being asked
+    assert delta_workspace(T=4096) > 0 and delta_workspace(T=4096, B=256) == 0 and delta_workspace(T=4096, H=512) == 0
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(seg_tokens=48), _lib.KDA_ERR_SHAPE),
+    (dict(seg_tokens=-64), _lib.KDA_ERR_SHAPE),
+    (dict(T=65, seg_tokens=64), _lib.KDA_ERR_WORKSPACE),
+    (dict(T=65, seg_tokens=64, workspace=WIDE[0], workspace_bytes=64), _lib.KDA_ERR_WORKSPACE),
+    (dict(T=65, seg_tokens=64, workspace=WIDE[0] + 8, workspace_bytes=1 << 30), _lib.KDA_ERR_WORKSPACE),
+    (dict(T=65, seg_tokens=64, workspace=A[0], workspace_bytes=1 << 30), _lib.KDA_ERR_WORKSPACE),
+    (dict(T=65, seg_tokens=64, workspace=A[5], workspace_bytes=1 << 30), _lib.KDA_ERR_WORKSPACE),
+    (dict(T=200, cu_seqlens=A[9], num_seqs=100, seg_tokens=64), _lib.KDA_ERR_WORKSPACE),
+])
+def test_delta_segment_errors(over, code):
+    assert call("kda_delta_fwd", _lib.DeltaArgs, DELTA, over) == code
