@@ -855,8 +855,9 @@ template <int K, int TM, bool OUT>
 hipError_t launch_pass(const DeltaParams &p, int64_t slots, hipStream_t stream)
 {
     const int64_t all = OUT ? p.V : p.V + p.K;
-    const int columns = columns_of(slots * p.H, all, p.seqs.cu && p.seg == 0);
-    const int64_t vblocks = (all + columns - 1) / columns, blocks = slots * p.H * vblocks;
+    const int most = columns_of(slots * p.H, all, p.seqs.cu && p.seg == 0);
+    const int64_t vblocks = (all + most - 1) / most, blocks = slots * p.H * vblocks;
+    const int columns = static_cast<int>((all / 16 + vblocks - 1) / vblocks * 16);  // as evenly as waves allow
     if (!grid_fits(blocks, kThreads))
         return hipErrorInvalidConfiguration;
     delta_chunk_kernel<K, TM, OUT><<<dim3(static_cast<uint32_t>(blocks)), dim3(kThreads), 0, stream>>>(p, static_cast<int>(vblocks), columns);
