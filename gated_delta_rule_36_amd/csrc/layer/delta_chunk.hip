@@ -10,13 +10,33 @@
 // taken off, and what is left multiplied by the inverse of the diagonal block,
 // which forward substitution gives.
 //
-// A workgroup of eight waves owns a (sequence, head) and up to 128 of its V
-// columns, 16 a wave, with the fp32 state [K, 16] in accumulators from the
-// sequence's first token to its last.  K, Q, V, A and P of a tile are in LDS,
-// shared by the waves: wave 0 forms and inverts the diagonal blocks of A, the
-// others the remaining blocks of A and P, and then each wave goes through the
-// tile alone.  The next tile's rows are loaded meanwhile, its decays and
-// strengths worked out by the last wave.
+// A workgroup of twelve waves owns a (sequence, head) and up to 128 of its V
+// columns.  Eight carry 16 columns of the fp32 state [K, 16] each, in accumulators
+// from the sequence's first token to its last; four prepare the tiles, which lie
+// in LDS twice over.  Two barriers a tile:
+// - state waves: K S and Q S of the tile, V's own columns through LDS.  Preparing
+//   waves: the inverses of the diagonal blocks of A (one wave), the next tile's
+//   rows from registers to LDS with its decays and strengths (another one), the
+//   loads of the one after.
+// - state waves: what is left of beta (V - 2^G K S), U, out, the state.  Preparing
+//   waves: the next tile's blocks of A and P.
+// Preparation takes no state, so all of it leaves the chain of tiles that has to
+// be gone through in order: 8 x 16384 tokens took 2.22 ms with the state waves doing it all, 1.81 after.
+//
+// Few long chains are cut into segments, for which the rule is an affine map of
+// the state: a pass forms every segment's own end and what it makes of each unit
+// vector, K columns more; a second kernel joins them in fp32; the output pass
+// starts each segment from what that gives.  8191 tokens of 12 heads of 64 x 96:
+// 391 us whole, 109 in 10 segments (57 + 8 + 43).
+//
+// What bounds it: 8 x 16384 tokens of 32 heads of 128 x 128 take 1.73 ms (2.5 TB/s, 36 % of
+// a large copy's rate), 14000 cycles a tile, of which a SIMD's matrix
+// instructions are busy 7550, vector ones 6000 and LDS 5500, mostly beside each other only
+// where a second wave is there; and a chip this busy runs at 1.9 instead of 2.4 GHz.
+// Tried and lost: 32 columns a state wave (1795 us against 1700), more priority for
+// the preparing waves (1757 against 1725), one of a SIMD's two state waves half a
+// tile ahead of the other (1768 against 1730: the second half of a tile takes two
+// thirds of it), the inverses in the same half as the blocks (packed 365 against 350).
 //
 // Operands.  In v_mfma_f32_16x16x32_bf16 lane (r = lane % 16, g = lane / 16)
 // holds row / column r, slots 8 g .. 8 g + 7, and accumulator register i is row
@@ -836,11 +856,11 @@ __global__ __launch_bounds__(4 * K) void delta_join_kernel(DeltaParams p)
     }
 }
 
-// Columns a workgroup takes.  Its tile takes 14000 cycles with eight state
+// Columns a workgroup takes at most.  Its tile takes 14000 cycles with eight state
 // waves, two a SIMD, and 7000 to 9000 with one to four, so few chains are spread:
 // as thinly as 256 workgroups, one a compute unit, allow.  Of packed sequences,
 // whose lengths differ, 512: the second half starts where short ones end.  Of
-// one of 8191 tokens with 12 heads of 64 x 96 128 columns take 567 us, 48 417, 32
+// one of 8191 tokens with 12 heads of 64 x 96, uncut, 128 columns take 567 us, 48 417, 32
 // 404 and 16 391; of 19595 tokens in 8 sequences with 32 heads of 128 x 128 128
 // take 430, 64 396 and 32 638; of 8 x 16384 128 take 1690, 64 2070.
 int columns_of(int64_t chains, int64_t all, bool packed)

@@ -11,6 +11,11 @@
 // it, one pass over the registers, and joined by
 //   scale S' q = scale (decay S q + u (k . q)).
 // All arithmetic is fp32.
+//
+// 64 sequences of one token, 32 heads of 128 x 128, fp32 states: 52 us (5.3 TB/s of
+// 272 MB, a large copy's rate) with other states in every call, 43 with the same.  Each
+// token more adds 5 to 7 us there; where that passes the chunked kernel's 113 stands
+// with the rule of which one runs.
 #include "layer_device.h"
 
 namespace kda {
