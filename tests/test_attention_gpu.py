@@ -339,3 +339,18 @@ def test_a_long_cache_past_32_bits():
     wo, wl, bo, bl = ref.attention(q, small_k, small_v, near, lengths, D ** -0.5)
     check("out", out, wo, bo)
     check("lse", lse, wl, bl)
+
+
+def test_rotary_of_more_than_2_to_31_elements():
+    T, H, D = (1 << 17) + 40, 32, 512
+    q = torch.empty(1, T, H, D, dtype=BF, device="cuda")
+    q[:, -64:] = rand(1, 64, H, D, seed=1).cuda()
+    q[:, :-64] = 1.0
+    pos = torch.arange(T, device="cuda")[None]
+    f, w = freqs(64).cuda(), rand(D, seed=2).cuda()
+    out = torch.full_like(q, NAN)
+    kda.qk_norm_rotary(q, None, pos, f, out, None, w)
+    tail = torch.full((1, 64, H, D), NAN, dtype=BF, device="cuda")
+    kda.qk_norm_rotary(q[:, -64:], None, pos[:, -64:].contiguous(), f, tail, None, w)
+    assert torch.equal(out[:, -64:], tail)
+    check("q", tail, *ref.rotary(q[:, -64:].cpu(), pos[:, -64:].cpu(), f.cpu(), w.cpu()))

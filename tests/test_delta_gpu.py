@@ -380,3 +380,45 @@ def test_segments_on_two_streams():
     torch.cuda.synchronize()
     for w, o in zip(want, got):
         assert all(torch.equal(w[0], y) and torch.equal(w[1], f) for y, f in o)
+
+
+# ---------------------------------------------------------------------------
+# offsets past 32 bits
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("T", [4, 8200])
+def test_outputs_past_32_bits(T):
+    """Values and outputs of 2^31 elements and more: the last sequence as it is by itself."""
+    H, V, K = 32, 512, 64
+    B = (1 << 31) // (T * H * V) + 2
+    g = torch.Generator("cuda").manual_seed(171)
+    def normal(*shape): return torch.randn(*shape, generator=g, device="cuda", dtype=BF)
+    k = torch.nn.functional.normalize(normal(B, T, 1, K).float(), dim=-1).to(BF)
+    q, gate, beta = normal(B, T, 1, K), normal(B, T, H), normal(B, T, H)
+    v = torch.empty(B, T, H, V, device="cuda", dtype=BF)
+    v[0].normal_(generator=g)
+    v[1:] = v[:1]  # every sequence has the first one's values
+    A = torch.zeros(H, device="cuda")
+    out = torch.empty_like(v)
+    kda.delta_fwd(q, k, v, gate, beta, 0.125, out, A)
+    for b in (0, B - 2, B - 1):
+        alone = torch.full((1, T, H, V), NAN, device="cuda", dtype=BF)
+        one = slice(b, b + 1)
+        kda.delta_fwd(q[one], k[one], v[:1], gate[one], beta[one], 0.125, alone, A, segment_tokens=8256)
+        assert torch.equal(out[b], alone[0]), b
+
+
+def test_batch_strides_past_32_bits():
+    x = inputs(2, 100, 1, 2, 64, 32, seed=181)
+    want, want_fin = call(x)
+    room = torch.empty((1 << 32) + (1 << 20), dtype=BF, device="cuda")  # 8 GiB, of which two ends are used
+    def far(name, at):
+        t = x[name].cuda()
+        n = t[0].numel()
+        y = room.as_strided(t.shape, ((1 << 32) + 2, *t.stride()[1:]), at)
+        y.copy_(t)
+        assert n < 1 << 17
+        return y
+    y = {name: far(name, 1 + (i << 17)) for i, name in enumerate(("q", "k", "v", "g", "beta"))}
+    out, fin = call(x, **y)
+    assert torch.equal(out, want) and torch.equal(fin, want_fin)
