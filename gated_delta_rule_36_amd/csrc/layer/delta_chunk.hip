@@ -581,32 +581,32 @@ __device__ __forceinline__ void state_wave(const DeltaParams &p, const Chain &ch
         if (TM < left)
             load(t0 + TM);
 
-        // K S and Q S: rows are tokens of K S, columns of (Q S)^T
+        // K S and Q S: rows are tokens of K S, columns of (Q S)^T.  Accumulators in turn, so that none waits for its
+        // own last product; rows of Q are asked for before the products of K's, and the next step's of K before those of Q
         f32x4_t u[NB], o[NB];
+        u32x4_t kr[NB], qr[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) kr[b] = lds_load<u32x4_t>(row + 32 * T::kPitch * b);
 #pragma unroll
         for (int e = 0; e < KSTEP; ++e) {
+#pragma unroll
+            for (int b = 0; OUT && b < NB; ++b) qr[b] = lds_load<u32x4_t>(row + kQ + 32 * T::kPitch * b + 64 * e);
             u32x2_t x[3], y[3];
             split<3>(s[2 * e], x);
             split<3>(s[2 * e + 1], y);
             const u32x4_t s0 = cat(x[0], y[0]), s1 = cat(x[1], y[1]), s2 = cat(x[2], y[2]);
-            // accumulators in turn, so that none waits for its own last product
-            u32x4_t kr[NB], qr[NB];
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                kr[b] = lds_load<u32x4_t>(row + 32 * T::kPitch * b + 64 * e);
-                if constexpr (OUT)
-                    qr[b] = lds_load<u32x4_t>(row + kQ + 32 * T::kPitch * b + 64 * e);
-            }
 #pragma unroll
             for (int b = 0; b < NB; ++b) u[b] = mfma(kr[b], s0, e > 0 ? u[b] : zero);
 #pragma unroll
-            for (int b = 0; OUT && b < NB; ++b) o[b] = mfma(s0, qr[b], e > 0 ? o[b] : zero);
-#pragma unroll
             for (int b = 0; b < NB; ++b) u[b] = mfma(kr[b], s1, u[b]);
 #pragma unroll
-            for (int b = 0; OUT && b < NB; ++b) o[b] = mfma(s1, qr[b], o[b]);
-#pragma unroll
             for (int b = 0; b < NB; ++b) u[b] = mfma(kr[b], s2, u[b]);
+#pragma unroll
+            for (int b = 0; e + 1 < KSTEP && b < NB; ++b) kr[b] = lds_load<u32x4_t>(row + 32 * T::kPitch * b + 64 * (e + 1));
+#pragma unroll
+            for (int b = 0; OUT && b < NB; ++b) o[b] = mfma(s0, qr[b], e > 0 ? o[b] : zero);
+#pragma unroll
+            for (int b = 0; OUT && b < NB; ++b) o[b] = mfma(s1, qr[b], o[b]);
         }
         // what the residual takes is there already
         const uint32_t vaddr = lds_addr(&sh.v[wave][here(lane) / 4][4 * (here(lane) & 3)]);  // 4 g + r / 4
