@@ -255,7 +255,11 @@ kda_status check_attention_sizes(const kda_attention_args &a)
 //   most, 8 key heads, for 8192 / 16384 / 32768 / 65536 waves 1034 / 886 / 826 / 857.
 //   All splits have the same size, so that waves do the same work however lengths
 //   differ; the same number of splits for every sequence took 991.
-constexpr int64_t kTarget = 32768, kFewest = 4 * kAttentionTile;
+//   At least kFewest tokens, or up to kEnough if the splits still make kWaves: 16 x 32768, 8
+//   key heads, splits of 128 / 160 / 192 / 320 tokens 42 / 46 / 51 / 55; 16 x 65536 68 / 70 / 65 / 81, 1 x
+//   131072 129 / 118 / 118 / 118, 64 x 262144 of 4 key heads 136 / 134 / 131 / 137, 64 x 65536 of
+//   8 with 256 channels 190 / 160 / 161 / 164.
+constexpr int64_t kTarget = 32768, kFewest = 4 * kAttentionTile, kEnough = 6 * kAttentionTile, kWaves = 5120;
 constexpr int64_t kShared = 1024, kSharedMost = 512, kGroups = 512, kFew = 327680;
 int64_t longest(const kda_attention_args &a)
 {
@@ -264,7 +268,8 @@ int64_t longest(const kda_attention_args &a)
 }
 int64_t attention_pairs(const kda_attention_args &a)
 {
-    return a.N * a.Hk * ((a.Hq / a.Hk + kAttentionRows - 1) / kAttentionRows);
+    // more than this no grid takes; times tokens it stays within 64 bits
+    return std::min<int64_t>(a.N * a.Hk * ((a.Hq / a.Hk + kAttentionRows - 1) / kAttentionRows), INT32_MAX);
 }
 // Whether a workgroup's waves share a split.
 bool attention_shared(const kda_attention_args &a)
@@ -282,8 +287,9 @@ int64_t attention_chunk(const kda_attention_args &a)
         const int64_t chunk = (attention_pairs(a) * most + kGroups - 1) / kGroups;
         return std::min(kSharedMost, (chunk + kStep - 1) / kStep * kStep);
     }
-    const int64_t parts = std::max(int64_t(1), kTarget / std::max(int64_t(1), attention_pairs(a)));
-    const int64_t chunk = std::max((most + parts - 1) / parts, kFewest);
+    const int64_t pairs = std::max(int64_t(1), attention_pairs(a)), parts = std::max(int64_t(1), kTarget / pairs);
+    const int64_t least = std::min(kEnough, std::max(kFewest, pairs * most / kWaves));
+    const int64_t chunk = std::max((most + parts - 1) / parts, least);
     return (chunk + kAttentionTile - 1) / kAttentionTile * kAttentionTile;
 }
 int64_t attention_splits(const kda_attention_args &a)

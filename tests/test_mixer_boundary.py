@@ -370,3 +370,11 @@ def test_delta_workspace():
 ])
 def test_delta_segment_errors(over, code):
     assert call("kda_delta_fwd", _lib.DeltaArgs, DELTA, over) == code
+
+
+def test_attention_of_more_heads_than_a_grid_takes():
+    most = dict(N=(1 << 31) - 1, Hq=65536, Hk=65536, D=16, page_size=1 << 20, table_width=2000)
+    assert workspace(**most) == 0
+    fields = {**ATTENTION, **{k: WIDE[i] for i, k in enumerate(k for k, v in ATTENTION.items() if v in A)}}
+    fields.update(q_stride=0, table_stride=0, k_cache_stride_head=0, v_cache_stride_head=0)
+    assert call("kda_paged_attention", _lib.AttentionArgs, fields, most) != OK
