@@ -109,8 +109,11 @@ __device__ __forceinline__ Visible visible(const AttentionParams &p, int64_t n)
 // SHARED: a workgroup's waves share its (sequence, key head, split) and join in
 // LDS; otherwise each has its own.  KS steps of 32 channels; a head of D channels
 // half fills the last one, or all of it.
+// Waves a SIMD by what the registers hold without spilling: of 224 channels two (64
+// x 65536 tokens, 8 key heads 125 us, 150 with one), of 256 one (161; two spill 8
+// registers: 153 there, but 148 against 138 for 16 x 262144 of 2 key heads).
 template <int KS, bool SHARED>
-__global__ __launch_bounds__(kThreads, KS <= 4 ? 3 : KS <= 6 ? 2 : 1) void paged_attention_kernel(AttentionParams p, int row_tiles, int64_t items)
+__global__ __launch_bounds__(kThreads, KS <= 4 ? 3 : KS <= 7 ? 2 : 1) void paged_attention_kernel(AttentionParams p, int row_tiles, int64_t items)
 {
     constexpr int D = 32 * KS, kPitch = D + 16, kOutPitch = D + 4;
     __shared__ union {
