@@ -860,16 +860,20 @@ __global__ __launch_bounds__(4 * K) void delta_join_kernel(DeltaParams p)
 
 // Columns a workgroup takes at most.  Its tile takes 14000 cycles with eight state
 // waves, two a SIMD, and 7000 to 9000 with one to four, so few chains are spread:
-// as thinly as 256 workgroups, one a compute unit, allow.  Of packed sequences,
-// whose lengths differ, 512: the second half starts where short ones end.  Of
+// as thinly as 256 workgroups, one a compute unit, allow.  Of
 // one of 8191 tokens with 12 heads of 64 x 96, uncut, 128 columns take 567 us, 48 417, 32
-// 404 and 16 391; of 19595 tokens in 8 sequences with 32 heads of 128 x 128 128
-// take 430, 64 396 and 32 638; of 8 x 16384 128 take 1690, 64 2070.
-int columns_of(int64_t chains, int64_t all, bool packed)
+// 404 and 16 391; of 8 x 16384 with 32 heads of 128 128 take 1690, 64 2070.  Of packed
+// sequences of unequal lengths 512 with 64 columns: the second half starts where short
+// ones end (19595 tokens in 8 sequences with 32 heads 128 take 430, 64 396 and 32 638; 16384
+// in 3 with 60 heads 128 630 to 970, 64 520 to 640), but with fewer columns, which save
+// nothing more, 256 (2 with 40 heads: 64 560 to 840, 32 670 to 810; 4 with 32
+// 320 to 540, 32 510 to 530).
+int columns_of(int64_t chains, int64_t all, bool unequal)
 {
-    const int64_t most = packed ? 512 : 256;
     int columns = 16;
-    while (columns < kColumns && columns < all && chains * ((all + columns - 1) / columns) > most) columns *= 2;
+    while (columns < kColumns && columns < all &&
+           chains * ((all + columns - 1) / columns) > (unequal && columns >= kColumns / 2 ? 512 : 256))
+        columns *= 2;
     return columns < all ? columns : static_cast<int>(all);
 }
 
@@ -877,7 +881,7 @@ template <int K, int TM, bool OUT>
 hipError_t launch_pass(const DeltaParams &p, int64_t slots, hipStream_t stream)
 {
     const int64_t all = OUT ? p.V : p.V + p.K;
-    const int most = columns_of(slots * p.H, all, p.seqs.cu && p.seg == 0);
+    const int most = columns_of(slots * p.H, all, p.seqs.cu && p.seqs.N > 1 && p.seg == 0);
     const int64_t vblocks = (all + most - 1) / most, blocks = slots * p.H * vblocks;
     const int columns = static_cast<int>((all / 16 + vblocks - 1) / vblocks * 16);  // as evenly as waves allow
     if (!grid_fits(blocks, kThreads))

@@ -291,14 +291,22 @@ struct DeltaPlan {
 // - packed sequences, whose lengths the host does not know, of up to two tokens
 //   on average: 64 of 1 / 2 tokens 44 / 47 (133 / 134), one of 33 and 31 of 1 38 (66), one of
 //   64 and 63 of none 68 (75).
-// Of the others, few chains are cut into segments: as many as leave
-// no compute unit of 256 a second workgroup in the pass over own states, which has
-// V + K columns, 128 a workgroup.  Segments cost that pass, so there have to be
-// four for each sequence at least, and of eight tiles: 8191 tokens of 12 heads 391 us whole, 111 in
-// 10 segments.  False if the workspace overflows.
+// Of the others, few chains are cut into segments: as many as leave no compute unit of
+// 256 a second workgroup in the pass over own states, which has V + K columns, 128 a
+// workgroup, and of eight tiles at least.  That pass does again what the output
+// pass does, so a sequence has to be 2.5 segments long, or packed ones of unequal lengths 1.9 on
+// average, since the longest of these is what segments shorten.  In us, whole and cut, heads of 128:
+//   one sequence of 8191 tokens, 12 heads of 64 x 96   391  109 (10 segments)
+//   one of 8192, 32 / 40 / 64 heads                    450  320 (4) / 464  379 (3) / 468  545 (2)
+//   one of 1024, 32 heads                              61   70 (2)
+//   16384 tokens in 2 packed, 24 heads                 530 to 800  551 (5 in all)
+//   in 4, 12 heads                                     297 to 520  289 to 406 (10)
+//   in 8, 8 / 16 heads                                 183 to 247  190 to 264 (16) / 194 to 257  345 (8)
+//   8000 in 12, 4 heads                                74   87 (16)
+// False if the workspace overflows.
 bool delta_plan(const kda_delta_args &a, const Seqs &s, DeltaPlan *plan)
 {
-    constexpr int64_t kTarget = 256, kLeast = 4, kColumns = 128, kShortest = 8 * kDeltaTile;
+    constexpr int64_t kTarget = 256, kColumns = 128, kShortest = 8 * kDeltaTile;
     if (s.T <= (s.cu ? 2 * s.N : kDeltaRecurrentMaxTokens) && (a.seg_tokens == 0 || a.seg_tokens >= s.T)) {
         plan->recurrent = true;
         return true;
@@ -306,11 +314,12 @@ bool delta_plan(const kda_delta_args &a, const Seqs &s, DeltaPlan *plan)
     int64_t seg = a.seg_tokens;
     if (seg == 0) {
         const int64_t parts = kTarget / (a.H * ((a.V + a.K + kColumns - 1) / kColumns));  // segments in all
-        if (s.N < 1 || parts < kLeast * s.N)
+        if (s.N < 1 || parts < s.N)
             return true;
-        const int64_t all = s.cu ? parts : parts / s.N;
+        const bool unequal = s.cu && s.N > 1;
+        const int64_t all = unequal ? parts : parts / s.N, each = unequal ? s.T / s.N : s.T;
         seg = std::max(((s.T + all - 1) / all + kDeltaTile - 1) / kDeltaTile * kDeltaTile, kShortest);
-        if (s.T < kLeast * seg)
+        if (8 * each < (unequal ? 15 : 20) * seg)
             return true;
     }
     if (seg >= s.T)
