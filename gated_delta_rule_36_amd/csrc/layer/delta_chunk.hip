@@ -27,9 +27,9 @@
 // the state: a pass forms every segment's own end and what it makes of each unit
 // vector, K columns more; a second kernel joins them in fp32; the output pass
 // starts each segment from what that gives.  8191 tokens of 12 heads of 64 x 96:
-// 391 us whole, 109 in 10 segments (57 + 8 + 43).
+// 391 us whole, 107 in 10 segments, of which the join is 8 and either pass half the rest.
 //
-// What bounds it: 8 x 16384 tokens of 32 heads of 128 x 128 take 1.73 ms (2.5 TB/s, 36 % of
+// What bounds it: 8 x 16384 tokens of 32 heads of 128 x 128 take 1.72 ms (1.9 TB/s, 38 % of
 // a large copy's rate), 14000 cycles a tile, of which a SIMD's matrix
 // instructions are busy 7550, vector ones 6000 and LDS 5500, mostly beside each other only
 // where a second wave is there; and a chip this busy runs at 1.9 instead of 2.4 GHz.

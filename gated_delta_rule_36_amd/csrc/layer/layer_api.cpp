@@ -296,7 +296,7 @@ struct DeltaPlan {
 // workgroup, and of eight tiles at least.  That pass does again what the output
 // pass does, so a sequence has to be 2.5 segments long, or packed ones of unequal lengths 1.9 on
 // average, since the longest of these is what segments shorten.  In us, whole and cut, heads of 128:
-//   one sequence of 8191 tokens, 12 heads of 64 x 96   391  109 (10 segments)
+//   one sequence of 8191 tokens, 12 heads of 64 x 96   391  107 (10 segments)
 //   one of 8192, 32 / 40 / 64 heads                    450  320 (4) / 464  379 (3) / 468  545 (2)
 //   one of 1024, 32 heads                              61   70 (2)
 //   16384 tokens in 2 packed, 24 heads                 530 to 800  551 (5 in all)

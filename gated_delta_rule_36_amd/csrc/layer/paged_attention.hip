@@ -11,10 +11,10 @@
 // lie side by side in the usual cache; with waves of one head next to each
 // other the same bytes came at 4.8 TB/s against 5.7 of a cache that keeps a head's
 // tokens together.  With few tokens in all, a workgroup's four waves
-// share a split and join in LDS instead.  Splits of one sequence leave unnormalised results,
-// which a second launch joins.  64 sequences of 8 key heads and 32 query heads, 128 channels, lengths
-// up to 131072: 826 us (5.2 TB/s), the rate of a large copy; one of 131071 tokens, 2 key heads
-// 37 us (3.6 TB/s), two launches.
+// share a split and join in LDS instead.  Splits of one sequence leave unnormalised
+// results, which a second launch joins.  64 sequences of 8 key heads and 32 query heads,
+// 128 channels, lengths up to 131072: 815 us (5.3 TB/s), the rate of a large copy; one of
+// 131071 tokens, 2 key heads 35 us (3.8 TB/s; 5.1 in the first of its two launches).
 //
 // Operands of v_mfma_f32_16x16x32_bf16: lane (r = lane % 16, g = lane / 16)
 // holds row / column r, slots 8 g .. 8 g + 7; accumulator register i is row
