@@ -31,7 +31,7 @@
 //
 // What bounds it: 8 x 16384 tokens of 32 heads of 128 x 128 take 1.72 ms (1.9 TB/s, 38 % of
 // a large copy's rate), 14000 cycles a tile, of which a SIMD's matrix
-// instructions are busy 7550, vector ones 6000 and LDS 5500, mostly beside each other only
+// instructions are busy 7550, vector ones 4900 and LDS 5400, beside each other only
 // where a second wave is there; and a chip this busy runs at 1.9 instead of 2.4 GHz.
 // Tried and lost: 32 columns a state wave (1795 us against 1700), more priority for
 // the preparing waves (1757 against 1725), one of a SIMD's two state waves half a
