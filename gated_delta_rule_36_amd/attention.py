@@ -71,8 +71,8 @@ def qk_norm_rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: Option
         raise ValueError("k and k_out go together")
     pk = pko = kb = kt = Hk = 0
     if k is not None:
-        _tensor("k", k, device, _BF16)
-        if k.dim() != 4:
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            _tensor("k", k, device, _BF16)
             raise ValueError(f"k must be [B,T,H,D], got {list(k.shape)}")
         Hk = k.shape[2]
         pk, kb, kt = _tokens("k", k, device, (B, T, Hk, D))

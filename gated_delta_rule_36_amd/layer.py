@@ -285,8 +285,8 @@ def delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor
     if v.dim() != 4:
         raise ValueError(f"v must be [B,T,H,V], got {list(v.shape)}")
     B, T, H, V = shape = v.shape
-    _tensor("k", k, device, _BF16)
-    if k.dim() != 4:
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        _tensor("k", k, device, _BF16)
         raise ValueError(f"k must be [B,T,G,K], got {list(k.shape)}")
     G, K = k.shape[2], k.shape[3]
     pv, vb, vt = _tokens("v", v, device, shape)
@@ -295,9 +295,10 @@ def delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor
     pg, gb, gt = _tokens("g", g, device, (B, T, H)) if g is not None else _tensor("g", g, device, _BF16)
     pb, bb, bt = _tokens("beta", beta, device, (B, T, H)) if beta is not None else _tensor("beta", beta, device, _BF16)
     po = _dense("out", out, device, shape, _BF16)
-    _tensor("A_log", A_log, device, torch.float32)
-    pA = _dense("A_log", A_log, device, (H,), torch.float32)
-    pt = _dense("dt_bias", dt_bias, device, (H,), torch.float32)
+    if A_log is None:
+        _tensor("A_log", A_log, device, _FP32)
+    pA = _dense("A_log", A_log, device, (H,), _FP32)
+    pt = _dense("dt_bias", dt_bias, device, (H,), _FP32)
     pu, num, seqs = _sequences(cu_seqlens, device, B, T, check_cu_seqlens)
     pi, icode = _typed("initial_state", initial_state, device, (seqs, H, V, K))
     pf, fcode = _typed("final_state", final_state, device, (seqs, H, V, K))
