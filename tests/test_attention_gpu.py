@@ -354,3 +354,47 @@ def test_rotary_of_more_than_2_to_31_elements():
     kda.qk_norm_rotary(q[:, -64:], None, pos[:, -64:].contiguous(), f, tail, None, w)
     assert torch.equal(out[:, -64:], tail)
     check("q", tail, *ref.rotary(q[:, -64:].cpu(), pos[:, -64:].cpu(), f.cpu(), w.cpu()))
+
+
+# ---------------------------------------------------------------------------
+# tables for many tokens: a wave a split
+# ---------------------------------------------------------------------------
+
+WIDE = 1 << 18  # tokens that a table has room for
+
+
+@pytest.mark.parametrize("Hq,Hk,D", [(2, 2, 16), (4, 4, 64), (16, 2, 128), (6, 2, 48), (10, 2, 96), (40, 2, 128),
+                                     (34, 2, 80), (16, 16, 32), (4, 2, 256), (3, 3, 192), (9, 3, 160), (12, 2, 224)])
+def test_attention_wide_tables_heads(Hq, Hk, D):
+    hold(*case([1, 33, 0, 1300], Hq, Hk, D, 16, D + Hq, width=WIDE // 16), D ** -0.5)
+
+
+@pytest.mark.parametrize("page", [1, 3, 100, 1000])
+@pytest.mark.parametrize("layout", ["tokens", "heads", "woven"])
+def test_attention_wide_tables_pages(page, layout):
+    hold(*case([1, 31, 32, 127, 128, 129, 191, 192, 193, 385, 0, 700], 4, 2, 64, page, page, layout, width=WIDE // page), 0.125)
+
+
+@pytest.mark.parametrize("lengths", [[5000, 0], [1, 30000, 0, 2049], [384] * 3, [191, 192, 193, 383, 384, 385]])
+@pytest.mark.parametrize("window", [None, 130, 200000])
+def test_attention_wide_tables_splits(lengths, window):
+    hold(*case(lengths, 8, 4, 128, 64, len(lengths), width=WIDE // 64), 128 ** -0.5, window)
+
+
+def test_attention_wide_tables_bad_pages_and_values():
+    q, kc, vc, table, lengths = case([900, 900, 900, 64], 4, 2, 64, 16, 188, width=WIDE // 16)
+    table[0, 3], table[0, 32], table[1, :] = -7, 1 << 30, -1
+    table[2, 5] = kc.shape[0]
+    lengths[3] = 1 << 30  # as far as the table goes, whose other pages are none
+    out, lse = hold(q, kc, vc, table, lengths, 0.125)
+    assert not out[1].any() and torch.isinf(lse[1]).all()
+    kc[table[0, 2], 3, 1, 7] = NAN
+    vc[table[2, 4], 2, 0, 9] = math.inf
+    bad, bad_lse = attend(q, kc, vc, table, lengths, 0.125)
+    assert bad[0, 2:].isnan().all() and bad_lse[0, 2:].isnan().all() and torch.isinf(bad[2, :2, 9]).all()
+    assert torch.equal(bad[0, :2], out[0, :2]) and torch.equal(bad[1], out[1]) and torch.equal(bad[2, 2:], out[2, 2:])
+
+
+@pytest.mark.parametrize("Hq,Hk,D", [(4, 2, 16), (4, 1, 48), (8, 2, 144), (17, 1, 192), (4, 4, 256)])
+def test_attention_splits_of_other_widths(Hq, Hk, D):
+    hold(*case([5000, 1, 0, 2049, 512, 513], Hq, Hk, D, 64, D, width=100), D ** -0.5)
