@@ -422,3 +422,54 @@ def test_batch_strides_past_32_bits():
     y = {name: far(name, 1 + (i << 17)) for i, name in enumerate(("q", "k", "v", "g", "beta"))}
     out, fin = call(x, **y)
     assert torch.equal(out, want) and torch.equal(fin, want_fin)
+
+
+# ---------------------------------------------------------------------------
+# workgroups of every width
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("T", [9, 150])
+@pytest.mark.parametrize("B,G,H,K,V", [(33, 2, 4, 64, 256), (33, 4, 4, 128, 128), (17, 4, 8, 256, 128), (16, 8, 8, 128, 128),
+                                       (16, 2, 4, 128, 160), (65, 1, 2, 128, 272), (40, 1, 2, 64, 96), (33, 4, 4, 256, 80)])
+def test_many_chains(B, G, H, K, V, T):
+    """So many chains that a workgroup takes 32 to 128 columns."""
+    hold(inputs(B, T, G, H, K, V, seed=B + T))
+
+
+@pytest.mark.parametrize("K", [64, 128, 256])
+@pytest.mark.parametrize("where", ["q", "k", "v", "g", "beta"])
+def test_non_finite_inputs_with_many_chains(where, K):
+    x = inputs(65, 150, 2, 4, K, 128, seed=191)
+    clean, clean_fin = call(x)
+    t, b = 77, 31
+    bad = x[where].clone()
+    if where in ("g", "beta"):
+        bad[b, t, 0] = NAN
+    else:
+        bad[b, t, 0, 5] = NAN
+    out, fin = call(x, **{where: bad})
+    other = torch.arange(65, device="cuda") != b
+    assert torch.equal(out[other], clean[other]) and torch.equal(fin[other], clean_fin[other])
+    assert torch.equal(out[b, :t], clean[b, :t]) and torch.equal(out[b, :, 2:], clean[b, :, 2:])
+    if where == "q":
+        assert torch.equal(out[b, t + 1:], clean[b, t + 1:]) and torch.equal(fin, clean_fin)
+        assert out[b, t, :2].isnan().all()
+    elif where == "k":
+        assert out[b, t:, :2].isnan().all() and fin[b, :2].isnan().all()
+    elif where == "v":
+        rest = torch.arange(128, device="cuda") != 5
+        assert torch.equal(out[b, :, 0][:, rest], clean[b, :, 0][:, rest]) and torch.equal(fin[b, 0][rest], clean_fin[b, 0][rest])
+        assert out[b, t:, 0, 5].isnan().all() and fin[b, 0, 5].isnan().all()
+    else:
+        assert out[b, t:, 0].isnan().all() and torch.equal(out[b, :, 1], clean[b, :, 1])
+
+
+def test_the_library_cuts_packed_sequences():
+    from gated_delta_rule_36_amd import _lib
+    cu = [0, 100, 3000, 3001, 4500]
+    args = _lib.DeltaArgs(B=1, T=4500, H=2, G=1, K=128, V=128, cu_seqlens=256, num_seqs=4)
+    assert _lib.load().kda_delta_workspace_bytes(args) > 0
+    x = inputs(1, 4500, 1, 2, 128, 128, seed=201, n=4)
+    x["A_log"] -= 4.0
+    _, fin, want = hold(x, cu=cu)
+    assert float((fin.cpu().double() - want).norm() / want.norm()) <= 2.0 ** -20
