@@ -38,7 +38,8 @@
 // tile ahead of the other (1768 against 1730: the second half of a tile takes two
 // thirds of it), the inverses in the same half as the blocks (packed 365 against 350),
 // the solve's products below the diagonal by bf16 parts (1773 against 1755, packed 356
-// against 350: a third fewer matrix cycles there, but the parts stand in the chain).
+// against 350: a third fewer matrix cycles there, but the parts stand in the chain), the
+// output's products of all blocks in turn (packed 355 against 345).
 //
 // Operands.  In v_mfma_f32_16x16x32_bf16 lane (r = lane % 16, g = lane / 16)
 // holds row / column r, slots 8 g .. 8 g + 7, and accumulator register i is row
