@@ -64,6 +64,10 @@ __device__ __forceinline__ uint32_t cut_bf16x2(float a, float b)
 {
     return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302);
 }
+// e^(x - top).  The difference comes first: scores stay as the scale leaves them, so
+// that every one that fp32 holds counts as it is; times log2(e) those above 2.36e38,
+// or a scale that large by itself, would be infinite.
+__device__ __forceinline__ float weight(float x, float top) { return exp2_f32((x - top) * kLog2eF); }
 // The largest (the sum) over the four lanes of a column.
 __device__ __forceinline__ float column_max(float x)
 {
@@ -200,7 +204,6 @@ __global__ __launch_bounds__(kThreads, KS <= 4 ? 3 : KS <= 7 ? 2 : 1) void paged
 #pragma unroll
     for (int d = 0; d < 2 * KS; ++d) o[d] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     float top = -__builtin_inff(), sum = 0.0f;
-    const float scale2 = p.scale * kLog2eF;
     const uint32_t vaddr = lds_addr(&sh.v[wave][4 * g + r / 4][4 * (r & 3)]);
 
     int base = t0 + (SHARED ? wave * TOK : 0);
@@ -228,26 +231,26 @@ __global__ __launch_bounds__(kThreads, KS <= 4 ? 3 : KS <= 7 ? 2 : 1) void paged
             load(base + kStep);
             look_up(base + 2 * kStep);
         }
-        float most = -__builtin_inff(), x2[8];
+        float most = -__builtin_inff(), x[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float x = (j < 4 ? score0[j & 3] : score1[j & 3]) * scale2;
-            x2[j] = mine >> (j < 4 ? j : 12 + j) & 1 ? x : -__builtin_inff();
-            most = fmaxf(most, x2[j]);
+            const float score = (j < 4 ? score0[j & 3] : score1[j & 3]) * p.scale;
+            x[j] = mine >> (j < 4 ? j : 12 + j) & 1 ? score : -__builtin_inff();
+            most = fmaxf(most, x[j]);
         }
         const float next = fmaxf(top, column_max(most));
         const float from_top = next == -__builtin_inff() ? 0.0f : next;
-        const float keep = exp2_f32(top - from_top);
+        const float keep = weight(top, from_top);
         top = next;
         sum *= keep;
         u32x4_t hi, lo;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float x = exp2_f32(x2[2 * j] - from_top), y = exp2_f32(x2[2 * j + 1] - from_top);
-            sum += x + y;
-            const uint32_t h = cut_bf16x2(x * kBelow, y * kBelow);
+            const float a = weight(x[2 * j], from_top), b = weight(x[2 * j + 1], from_top);
+            sum += a + b;
+            const uint32_t h = cut_bf16x2(a * kBelow, b * kBelow);
             hi[j] = h;
-            lo[j] = pack_bf16x2(x - lo_f32(h), y - hi_f32(h));
+            lo[j] = pack_bf16x2(a - lo_f32(h), b - hi_f32(h));
         }
         if (__any(keep != 1.0f)) {
 #pragma unroll
@@ -284,7 +287,7 @@ __global__ __launch_bounds__(kThreads, KS <= 4 ? 3 : KS <= 7 ? 2 : 1) void paged
         sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-            f[w] = exp2_f32(shared_top[w][r] - from_top);
+            f[w] = weight(shared_top[w][r], from_top);
             sum = fmaf(f[w], shared_sum[w][r], sum);
         }
 #pragma unroll
@@ -308,7 +311,7 @@ __global__ __launch_bounds__(kThreads, KS <= 4 ? 3 : KS <= 7 ? 2 : 1) void paged
                 *reinterpret_cast<u32x2_t *>(p.out + head * p.D + 16 * d + 4 * g) =
                     u32x2_t{pack_bf16x2(o[d][0] * f, o[d][1] * f), pack_bf16x2(o[d][2] * f, o[d][3] * f)};
         if (first && p.lse)
-            p.lse[head] = sum == 0.0f ? -__builtin_inff() : (top + log2f(sum)) * kLn2F;
+            p.lse[head] = sum == 0.0f ? -__builtin_inff() : fmaf(log2f(sum), kLn2F, top);
     } else {
         const int64_t slot = head * p.splits + split;
 #pragma unroll
@@ -347,7 +350,7 @@ __global__ __launch_bounds__(kJoinThreads) void paged_attention_join_kernel(Atte
 #pragma unroll 4
     for (int s = grp; s < vis.used; s += GROUPS) {
         const float m = stats[2 * s], next = fmaxf(top, m), from_top = next == -__builtin_inff() ? 0.0f : next;
-        const float keep = exp2_f32(top - from_top), f = exp2_f32(m - from_top);
+        const float keep = weight(top, from_top), f = weight(m, from_top);
         total = fmaf(f, stats[2 * s + 1], total * keep);
         x = f * *reinterpret_cast<const f32x4_t *>(src + s * p.D) + x * keep;
         top = next;
@@ -367,7 +370,7 @@ __global__ __launch_bounds__(kJoinThreads) void paged_attention_join_kernel(Atte
     total = 0.0f;
 #pragma unroll 4
     for (int k = 0; k < GROUPS; ++k) {
-        const float f = exp2_f32(tops[k] - from_top);
+        const float f = weight(tops[k], from_top);
         total = fmaf(f, sums[k], total);
         x += f * *reinterpret_cast<const f32x4_t *>(&part[k][4 * l]);
     }
@@ -375,7 +378,7 @@ __global__ __launch_bounds__(kJoinThreads) void paged_attention_join_kernel(Atte
     *reinterpret_cast<u32x2_t *>(p.out + head * p.D + d) =
         u32x2_t{pack_bf16x2(x[0] * f, x[1] * f), pack_bf16x2(x[2] * f, x[3] * f)};
     if (d == 0 && p.lse)
-        p.lse[head] = total == 0.0f ? -__builtin_inff() : (from_top + log2f(total)) * kLn2F;
+        p.lse[head] = total == 0.0f ? -__builtin_inff() : fmaf(log2f(total), kLn2F, from_top);
 }
 
 template <int LANES>

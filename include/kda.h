@@ -718,6 +718,7 @@ kda_status kda_append_kv(const kda_append_args *args, void *stream);
  *   D              a multiple of 16, at most 256; Hk divides Hq
  *                  (KDA_ERR_SHAPE otherwise).
  *   scale          0 or a normal number of fp32 (KDA_ERR_SCALE otherwise).
+ *                  Scores are fp32: one that this does not hold is infinite.
  *   window         >= 0; 0 = every token (KDA_ERR_SIZE otherwise).
  *   table_width    * page_size at most 2^31 - 65537 (KDA_ERR_SIZE otherwise).
  *   workspace, workspace_bytes   DEVICE scratch, 16-byte aligned, at least

@@ -1,0 +1,55 @@
+"""paged_attention at the limits of its numbers: the largest scales, on every
+way through the kernels (one split, splits shared by a workgroup's waves, a wave
+a split, joins of few and of many splits)."""
+import math
+
+import pytest
+import torch
+
+import mixer_ref as ref
+from mixer_ref import check
+from test_attention_gpu import WIDE, attend, case
+
+pytestmark = pytest.mark.gpu
+
+# (lengths, key heads, channels, tokens that the table has room for)
+WAYS = [([5, 200, 0], 2, 64, 208), ([3000, 5, 0, 700], 2, 64, 3008), ([3000, 5], 2, 256, 3008),
+        ([900, 5, 0, 193], 4, 128, WIDE), ([130, 2000], 4, 256, WIDE), ([20000, 9], 8, 64, WIDE),
+        ([700, 0] + [3] * 62, 4, 64, 1 << 14), ([700, 0] + [3] * 62, 4, 144, 1 << 14)]
+
+
+def build(lengths, Hk, D, room, seed):
+    return case(lengths, 2 * Hk, Hk, D, 16, seed, width=-(-room // 16))
+
+
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("scale", [3.3e38, -3.3e38])
+def test_the_largest_scales_with_queries_of_zero(way, scale):
+    """Every score is 0: the mean of the values, and the logarithm of the number of tokens."""
+    q, kc, vc, table, lengths = build(*way, 211)
+    q.zero_()
+    out, lse = attend(q, kc, vc, table, lengths, scale)
+    wo, wl, bo, bl = ref.attention(q, kc.cpu(), vc.cpu(), table, lengths, scale)
+    check("out", out, wo, bo)
+    check("lse", lse, wl, bl)
+
+
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_scores_up_to_the_largest_numbers(way, sign):
+    """Scores of 1, 2 and 3 times 1e38, exact as they are formed: the tokens with the largest share the weight,
+    the others' is 0, and the maximum is the logarithm of the sum."""
+    q, kc, vc, table, lengths = build(*way, 221)
+    q.zero_()
+    q[..., 0] = 1.0
+    pages, page = kc.shape[:2]
+    seen = ~kc[..., 0, 0].isnan()
+    level = torch.randint(1, 4, (pages, page), generator=torch.Generator().manual_seed(5)).cuda()
+    kc[..., 0] = torch.where(seen, sign * level, math.nan)[..., None].to(kc.dtype)
+    out, lse = attend(q, kc, vc, table, lengths, 1e38)
+    # the same weights as of scores of 1, 2 and 3 times 1000, where exp(-1000) is 0 in 64 bits, too
+    wo, wl, _, _ = ref.attention(q, kc.cpu(), vc.cpu(), table, lengths, 1000.0)
+    # of n equal probabilities the sum, its reciprocal and the product are rounded, and the parts leave 2^-16; a
+    # value is below 8 here.  The score is one product's rounding off, and so is its logarithm
+    check("out", out, wo, torch.tensor(8 * (2.0 ** -16 + (max(way[0]) + 16) * ref.U32), dtype=torch.float64))
+    check("lse", lse, 1e38 * torch.round(wl / 1000), torch.tensor(3e38 * 4 * ref.U32, dtype=torch.float64))
