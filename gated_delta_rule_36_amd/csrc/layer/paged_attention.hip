@@ -42,6 +42,7 @@ constexpr int kWaves = 4, kThreads = 64 * kWaves, TOK = 32;  // tokens of a wave
 constexpr int ROWS = static_cast<int>(kAttentionRows);
 constexpr float kBelow = 1.0f - 0x1p-10f;
 constexpr float kLn2F = 0.693147180559945f;
+constexpr float kLowest = -3.402823466e38f;
 
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 __device__ __forceinline__ uint32_t lds_addr(const void *p)
@@ -177,7 +178,7 @@ __global__ __launch_bounds__(kThreads, KS <= 4 ? 3 : KS <= 7 ? 2 : 1) void paged
     const bool past = 32 * (KS - 1) + 8 * g >= width;
     const int last_step = past ? -8 * g : 32 * (KS - 1);
     u32x4_t kt[2][KS], vt[2][KS];
-    uint32_t seen = 0;  // bit t: token t of the tile is visible
+    uint32_t seen = 0, ever = 0;  // bit t: token t of the tile (of any tile) is visible
     const auto load_half = [&](int t, int pg, u32x4_t (&kx)[KS], u32x4_t (&vx)[KS]) {
         const u32x4_t none = {0, 0, 0, 0};
         const bool in = t < t1 && pg >= 0 && pg < p.pages;
@@ -198,6 +199,7 @@ __global__ __launch_bounds__(kThreads, KS <= 4 ? 3 : KS <= 7 ? 2 : 1) void paged
     const auto load = [&](int base) {
         const uint32_t low = load_half(base + r, page[0], kt[0], vt[0]);
         seen = low | load_half(base + 16 + r, page[1], kt[1], vt[1]) << 16;
+        ever |= seen;
     };
 
     f32x4_t o[2 * KS];
@@ -268,6 +270,10 @@ __global__ __launch_bounds__(kThreads, KS <= 4 ? 3 : KS <= 7 ? 2 : 1) void paged
     }
 
     sum = column_sum(sum);
+    // Scores that are all -inf leave no weight to divide by, NaN; only a row without a visible token is 0.  The lowest
+    // number tells them apart from here on, and beside any score in other splits it comes to nothing.
+    if (ever != 0 && top == -__builtin_inff())
+        top = kLowest;
     if constexpr (SHARED) {
         // the waves' results, one after the other in LDS; each goes on with a quarter of the channels
         __syncthreads();
@@ -304,14 +310,15 @@ __global__ __launch_bounds__(kThreads, KS <= 4 ? 3 : KS <= 7 ? 2 : 1) void paged
         return;
     const int64_t head = n * p.Hq + static_cast<int64_t>(hk) * group + row0 + r;
     if (vis.used <= 1) {
-        const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const bool none = top == -__builtin_inff();
+        const float f = none ? 0.0f : 1.0f / sum;
 #pragma unroll
         for (int d = 0; d < 2 * KS; ++d)
             if (mine(d))
                 *reinterpret_cast<u32x2_t *>(p.out + head * p.D + 16 * d + 4 * g) =
                     u32x2_t{pack_bf16x2(o[d][0] * f, o[d][1] * f), pack_bf16x2(o[d][2] * f, o[d][3] * f)};
         if (first && p.lse)
-            p.lse[head] = sum == 0.0f ? -__builtin_inff() : fmaf(log2f(sum), kLn2F, top);
+            p.lse[head] = none ? top : fmaf(log2f(sum), kLn2F, top);
     } else {
         const int64_t slot = head * p.splits + split;
 #pragma unroll
@@ -374,11 +381,12 @@ __global__ __launch_bounds__(kJoinThreads) void paged_attention_join_kernel(Atte
         total = fmaf(f, sums[k], total);
         x += f * *reinterpret_cast<const f32x4_t *>(&part[k][4 * l]);
     }
-    const float f = total == 0.0f ? 0.0f : 1.0f / total;
+    const bool none = most == -__builtin_inff();
+    const float f = none ? 0.0f : 1.0f / total;
     *reinterpret_cast<u32x2_t *>(p.out + head * p.D + d) =
         u32x2_t{pack_bf16x2(x[0] * f, x[1] * f), pack_bf16x2(x[2] * f, x[3] * f)};
     if (d == 0 && p.lse)
-        p.lse[head] = total == 0.0f ? -__builtin_inff() : fmaf(log2f(total), kLn2F, from_top);
+        p.lse[head] = none ? most : fmaf(log2f(total), kLn2F, from_top);
 }
 
 template <int LANES>

@@ -713,7 +713,8 @@ kda_status kda_append_kv(const kda_append_args *args, void *stream);
  *   lengths        int32 [N]; clamped to [0, table_width * page_size].
  *   out            bf16 [N,Hq,D], contiguous.
  *   lse            fp32 [N,Hq], contiguous; NULL = not written.
- *                  Sequences without a visible token get out = 0, lse = -inf.
+ *                  Sequences without a visible token get out = 0, lse = -inf;
+ *                  where every visible one's score is -inf, out is NaN.
  *                  Tokens that are not visible may hold anything.
  *   D              a multiple of 16, at most 256; Hk divides Hq
  *                  (KDA_ERR_SHAPE otherwise).

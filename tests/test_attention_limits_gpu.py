@@ -53,3 +53,36 @@ def test_scores_up_to_the_largest_numbers(way, sign):
     # value is below 8 here.  The score is one product's rounding off, and so is its logarithm
     check("out", out, wo, torch.tensor(8 * (2.0 ** -16 + (max(way[0]) + 16) * ref.U32), dtype=torch.float64))
     check("lse", lse, 1e38 * torch.round(wl / 1000), torch.tensor(3e38 * 4 * ref.U32, dtype=torch.float64))
+
+
+@pytest.mark.parametrize("way", WAYS)
+def test_scores_of_minus_infinity(way):
+    """Such tokens have no weight beside others; where every visible one is such there is no softmax: NaN, and a
+    logarithm of -inf.  Zeros are of sequences without a visible token alone."""
+    q, kc, vc, table, lengths = build(*way, 231)
+    q[..., 0] = 1.0
+    k0 = kc[..., 0].clone()
+    # every other page, as a sequence's own run of pages: in the reference these pages are none
+    part = table.clone()
+    for n, length in enumerate(way[0]):
+        used = -(-length // 16)
+        for j in range(used):
+            if used > 1 and j % 2 == 0:
+                kc[table[n, j], ..., 0] = -math.inf
+                part[n, j] = -1
+    clean = kc.clone()
+    clean[..., 0] = k0
+    out, lse = attend(q, kc, vc, table, lengths, 0.125)
+    wo, wl, bo, bl = ref.attention(q, clean.cpu(), vc.cpu(), part, lengths, 0.125)
+    check("out", out, wo, bo)
+    check("lse", lse, wl, bl)
+    kc[..., 0] = -math.inf
+    out, lse = attend(q, kc, vc, table, lengths, 0.125)
+    some = (lengths > 0).cuda()
+    assert out[some].isnan().all() and not out[~some].any()
+    assert torch.equal(lse, torch.full_like(lse, -math.inf))
+    table[0] = -1  # pages that are none: not visible
+    out, lse = attend(q, kc, vc, table, lengths, 0.125)
+    some[0] = False
+    assert out[some].isnan().all() and not out[~some].any()
+    assert torch.equal(lse, torch.full_like(lse, -math.inf))
