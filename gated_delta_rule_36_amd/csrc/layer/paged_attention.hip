@@ -42,7 +42,7 @@ constexpr int kWaves = 4, kThreads = 64 * kWaves, TOK = 32;  // tokens of a wave
 constexpr int ROWS = static_cast<int>(kAttentionRows);
 constexpr float kBelow = 1.0f - 0x1p-10f;
 constexpr float kLn2F = 0.693147180559945f;
-constexpr float kLowest = -3.402823466e38f;
+constexpr float kLowest = -3.402823466e38f, kLargest = 3.402823466e38f;
 
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 __device__ __forceinline__ uint32_t lds_addr(const void *p)
@@ -68,6 +68,9 @@ __device__ __forceinline__ uint32_t cut_bf16x2(float a, float b)
 // e^(x - top).  The difference comes first: scores stay as the scale leaves them, so
 // that every one that fp32 holds counts as it is; times log2(e) those above 2.36e38,
 // or a scale that large by itself, would be infinite.
+//   top itself is a number: taken off from what is infinite it leaves that infinite,
+// so scores of -inf weigh nothing and a score of inf makes the sum so.
+__device__ __forceinline__ float number(float top) { return __builtin_amdgcn_fmed3f(top, kLowest, kLargest); }
 __device__ __forceinline__ float weight(float x, float top) { return exp2_f32((x - top) * kLog2eF); }
 // The largest (the sum) over the four lanes of a column.
 __device__ __forceinline__ float column_max(float x)
@@ -241,8 +244,8 @@ __global__ __launch_bounds__(kThreads, KS <= 4 ? 3 : KS <= 7 ? 2 : 1) void paged
             most = fmaxf(most, x[j]);
         }
         const float next = fmaxf(top, column_max(most));
-        const float from_top = next == -__builtin_inff() ? 0.0f : next;
-        const float keep = weight(top, from_top);
+        const float from_top = number(next);
+        const float keep = weight(number(top), from_top);
         top = next;
         sum *= keep;
         u32x4_t hi, lo;
@@ -287,7 +290,7 @@ __global__ __launch_bounds__(kThreads, KS <= 4 ? 3 : KS <= 7 ? 2 : 1) void paged
         float most = shared_top[0][r];
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) most = fmaxf(most, shared_top[w][r]);
-        const float from_top = most == -__builtin_inff() ? 0.0f : most;
+        const float from_top = number(most);
         float f[kWaves];
         top = most;
         sum = 0.0f;
@@ -356,8 +359,8 @@ __global__ __launch_bounds__(kJoinThreads) void paged_attention_join_kernel(Atte
     float top = -__builtin_inff(), total = 0.0f;
 #pragma unroll 4
     for (int s = grp; s < vis.used; s += GROUPS) {
-        const float m = stats[2 * s], next = fmaxf(top, m), from_top = next == -__builtin_inff() ? 0.0f : next;
-        const float keep = weight(top, from_top), f = weight(m, from_top);
+        const float m = stats[2 * s], next = fmaxf(top, m), from_top = number(next);
+        const float keep = weight(number(top), from_top), f = weight(m, from_top);
         total = fmaf(f, stats[2 * s + 1], total * keep);
         x = f * *reinterpret_cast<const f32x4_t *>(src + s * p.D) + x * keep;
         top = next;
@@ -372,7 +375,7 @@ __global__ __launch_bounds__(kJoinThreads) void paged_attention_join_kernel(Atte
         return;
     float most = tops[0];
     for (int k = 1; k < GROUPS; ++k) most = fmaxf(most, tops[k]);
-    const float from_top = most == -__builtin_inff() ? 0.0f : most;
+    const float from_top = number(most);
     x = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     total = 0.0f;
 #pragma unroll 4
@@ -386,7 +389,7 @@ __global__ __launch_bounds__(kJoinThreads) void paged_attention_join_kernel(Atte
     *reinterpret_cast<u32x2_t *>(p.out + head * p.D + d) =
         u32x2_t{pack_bf16x2(x[0] * f, x[1] * f), pack_bf16x2(x[2] * f, x[3] * f)};
     if (d == 0 && p.lse)
-        p.lse[head] = none ? most : fmaf(log2f(total), kLn2F, from_top);
+        p.lse[head] = none ? most : fmaf(log2f(total), kLn2F, most);
 }
 
 template <int LANES>

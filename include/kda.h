@@ -714,7 +714,8 @@ kda_status kda_append_kv(const kda_append_args *args, void *stream);
  *   out            bf16 [N,Hq,D], contiguous.
  *   lse            fp32 [N,Hq], contiguous; NULL = not written.
  *                  Sequences without a visible token get out = 0, lse = -inf;
- *                  where every visible one's score is -inf, out is NaN.
+ *                  where every visible one's score is -inf, or one's inf,
+ *                  out is NaN and lse that infinity.
  *                  Tokens that are not visible may hold anything.
  *   D              a multiple of 16, at most 256; Hk divides Hq
  *                  (KDA_ERR_SHAPE otherwise).

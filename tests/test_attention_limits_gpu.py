@@ -86,3 +86,23 @@ def test_scores_of_minus_infinity(way):
     some[0] = False
     assert out[some].isnan().all() and not out[~some].any()
     assert torch.equal(lse, torch.full_like(lse, -math.inf))
+
+
+@pytest.mark.parametrize("way", WAYS)
+def test_scores_of_plus_infinity(way):
+    """A key that is infinite where the query is positive: no softmax, but a sum, whose logarithm is infinite; NaN
+    beside it leaves neither."""
+    q, kc, vc, table, lengths = build(*way, 241)
+    q[..., 0] = 1.0
+    n = max(range(len(way[0])), key=lambda i: way[0][i])
+    for t in {0, way[0][n] // 2, way[0][n] - 1}:
+        clean, clean_lse = attend(q, kc, vc, table, lengths, 0.125)
+        bad = kc.clone()
+        bad[table[n, t // 16], t % 16, 1, 0] = math.inf
+        out, lse = attend(q, bad, vc, table, lengths, 0.125)
+        assert out[n, 2:4].isnan().all() and (lse[n, 2:4] == math.inf).all()
+        out[n, 2:4], lse[n, 2:4] = clean[n, 2:4], clean_lse[n, 2:4]
+        assert torch.equal(out, clean) and torch.equal(lse, clean_lse)
+        bad[table[n, (t + 1) % way[0][n] // 16], (t + 1) % way[0][n] % 16, 1, 3] = math.nan
+        out, lse = attend(q, bad, vc, table, lengths, 0.125)
+        assert out[n, 2:4].isnan().all() and lse[n, 2:4].isnan().all()
