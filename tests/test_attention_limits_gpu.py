@@ -106,3 +106,12 @@ def test_scores_of_plus_infinity(way):
         bad[table[n, (t + 1) % way[0][n] // 16], (t + 1) % way[0][n] % 16, 1, 3] = math.nan
         out, lse = attend(q, bad, vc, table, lengths, 0.125)
         assert out[n, 2:4].isnan().all() and lse[n, 2:4].isnan().all()
+
+
+def test_more_queries_than_a_join_of_them_would_have_workgroups_for():
+    """2^22 query heads of 128 channels: one split each, so nothing is joined."""
+    q, kc, vc, table, lengths = case([1 + i % 16 for i in range(64)], 32, 1, 128, 16, 251)
+    few, few_lse = attend(q, kc, vc, table, lengths, 0.125)
+    n = 1 << 11
+    out, lse = attend(q.repeat(n, 1, 1), kc, vc, table.repeat(n, 1), lengths.repeat(n), 0.125)
+    assert (out.unflatten(0, (n, 64)) == few).all() and (lse.unflatten(0, (n, 64)) == few_lse).all()
