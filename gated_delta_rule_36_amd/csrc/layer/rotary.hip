@@ -191,8 +191,9 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryParams p, int pe
                 if (inside(i)) {
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
-                        row.a[i][e] *= s * (!APPEND && row.second ? wa[1][i][e] : wa[0][i][e]);
-                        row.c[i][e] *= s * (!APPEND && row.second ? wc[1][i][e] : wc[0][i][e]);
+                        // the row first: s w by itself may be beyond fp32 where the row times s is near 1
+                        row.a[i][e] = row.a[i][e] * s * (!APPEND && row.second ? wa[1][i][e] : wa[0][i][e]);
+                        row.c[i][e] = row.c[i][e] * s * (!APPEND && row.second ? wc[1][i][e] : wc[0][i][e]);
                     }
                 }
         }
