@@ -1,14 +1,16 @@
-"""paged_attention at the limits of its numbers: the largest scales, on every
-way through the kernels (one split, splits shared by a workgroup's waves, a wave
-a split, joins of few and of many splits)."""
+"""paged_attention at the limits of its numbers and places: the largest scales and
+scores, infinite ones, more queries than a join takes, caches at odd elements (and
+append_kv's), on every way through the kernels: one split, splits shared by a
+workgroup's waves, a wave a split, joins of few and of many splits."""
 import math
 
 import pytest
 import torch
 
+import gated_delta_rule_36_amd as kda
 import mixer_ref as ref
 from mixer_ref import check
-from test_attention_gpu import WIDE, attend, case
+from test_attention_gpu import WIDE, attend, case, freqs, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -115,3 +117,38 @@ def test_more_queries_than_a_join_of_them_would_have_workgroups_for():
     n = 1 << 11
     out, lse = attend(q.repeat(n, 1, 1), kc, vc, table.repeat(n, 1), lengths.repeat(n), 0.125)
     assert (out.unflatten(0, (n, 64)) == few).all() and (lse.unflatten(0, (n, 64)) == few_lse).all()
+
+
+def odd(t):
+    """t's numbers at an odd element of wider rows, NaN between them."""
+    room = torch.full((t.numel() // t.shape[-1] * (t.shape[-1] + 3) + 1,), math.nan, dtype=t.dtype, device="cuda")
+    y = room[1:].view(*t.shape[:-1], t.shape[-1] + 3)[..., :t.shape[-1]]
+    y.copy_(t)
+    return room, y
+
+
+@pytest.mark.parametrize("way", WAYS)
+def test_caches_at_odd_places(way):
+    q, kc, vc, table, lengths = build(*way, 261)
+    out, lse = attend(q, kc, vc, table, lengths, 0.125)
+    wide = torch.full((q.shape[0], q[0].numel() + 3), math.nan, dtype=q.dtype)
+    wide[:, 1:-2] = q.flatten(1)
+    queries = wide.cuda()[:, 1:-2].unflatten(1, q.shape[1:])
+    again, again_lse = attend(queries, odd(kc)[1], odd(vc)[1], table, lengths, 0.125)
+    assert torch.equal(again, out) and torch.equal(again_lse, lse)
+
+
+@pytest.mark.parametrize("D,R", [(16, 8), (64, 64), (80, 20), (128, 32), (256, 256), (6, 2)])
+def test_append_to_caches_at_odd_places(D, R):
+    """The numbers of the call on contiguous caches, and nothing between the rows or behind the last is written."""
+    k, v = rand(2, 7, 3, D, seed=1).cuda(), rand(2, 7, 3, D, seed=2).cuda()
+    kc, vc = rand(5, 4, 3, D, seed=3).cuda(), rand(5, 4, 3, D, seed=4).cuda()
+    slots = torch.randperm(20, generator=torch.Generator().manual_seed(5))[:14].view(2, 7).cuda()
+    slots[1, 3] = -1
+    positions, f, w = torch.arange(14, device="cuda").view(2, 7), freqs(R).cuda(), rand(D, seed=6).cuda()
+    (kroom, ko), (vroom, vo) = odd(kc), odd(vc)
+    for caches in ((kc, vc), (ko, vo)):
+        kda.append_kv(k, v, *caches, slots, positions, f, w)
+    for (room, got), want in (((kroom, ko), kc), ((vroom, vo), vc)):
+        again, y = odd(want)
+        assert torch.equal(got, want) and torch.equal(room.view(torch.int16), again.view(torch.int16))
