@@ -152,3 +152,35 @@ def test_append_to_caches_at_odd_places(D, R):
     for (room, got), want in (((kroom, ko), kc), ((vroom, vo), vc)):
         again, y = odd(want)
         assert torch.equal(got, want) and torch.equal(room.view(torch.int16), again.view(torch.int16))
+
+
+@pytest.mark.parametrize("Hk,D,room", [(4, 16, 16), (4, 128, 16), (4, 64, WIDE), (2, 256, WIDE)])
+def test_probabilities_keep_their_digits(Hk, D, room):
+    """Four tokens whose values cancel to 2^-17 of their weighted sizes, so that out shows the probabilities' errors and
+    not its own rounding.
+
+    The scores are multiples of 1/8 up to 1 and exact, as are their differences.  A probability is off by 1.25 2^-24 of
+    the multiplication with log2(e), 2^-23 of the exponential and 1.25 2^-23 of its parts; twelve products and their sums
+    leave 12 2^-24, the sum of the probabilities, its reciprocal and the product with it 5 2^-24: 2^-19.5 in all.
+    Probabilities good to 2^-16 are past it."""
+    n = 16
+    q, kc, vc, table, lengths = build([4] * n, Hk, D, room, 281)
+    gen = torch.Generator().manual_seed(282)
+    pick = lambda: torch.stack([torch.randperm(9, generator=gen)[:4] for _ in range(n * Hk)]).view(n, Hk, 4).transpose(1, 2)  # noqa: E731
+    level = pick().double()  # [n, 4, Hk], each token's score times 8
+    q.zero_()
+    q[..., 0] = 1.0
+    p = torch.softmax(level / 8, 1)[..., None]
+    v = torch.randn(n, 4, Hk, D, generator=gen).clamp(-2, 2).to(q.dtype).double()
+    v[:, 2:] = 0
+    for t in (2, 3):  # what is left of the ones before, rounded
+        v[:, t] = (-(p * v).sum(1) / p[:, t]).to(q.dtype).double()
+    at = table[:, 0].long()
+    kc[at, :4] = level[..., None].expand(n, 4, Hk, D).to(kc.dtype).cuda()
+    vc[at, :4] = v.to(vc.dtype).cuda()
+    out, lse = attend(q, kc, vc, table, lengths, 0.125)
+    want = (p * v).sum(1).repeat_interleave(2, 1)
+    size = (p * v.abs()).sum(1).repeat_interleave(2, 1)
+    assert (want.abs() <= 2.0 ** -16 * size).double().mean() > 0.9
+    check("out", out, want, 2.0 ** -19.5 * size)
+    check("lse", lse, torch.logsumexp(level / 8, 1).repeat_interleave(2, 1), torch.tensor(2.0 ** -20, dtype=torch.float64))
