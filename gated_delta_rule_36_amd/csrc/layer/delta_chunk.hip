@@ -77,38 +77,19 @@ namespace kda {
 namespace layer {
 namespace {
 
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef short s16x4_t __attribute__((ext_vector_type(4)));
-
 // Waves with 16 columns of the state each, and waves that prepare tiles.
 constexpr int kStateWaves = 8, kProducers = 4, kThreads = 64 * (kStateWaves + kProducers), kColumns = 16 * kStateWaves;
 // Magnitudes from here on round to infinity as bf16 (or are not finite).
 constexpr uint32_t kOddBits = 0x7f7f8000u;
 constexpr float kGone = -1000.0f;  // log decay below which nothing is left, also in 64 tokens' sum
 
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
-__device__ __forceinline__ uint32_t lds_addr(const void *p)
-{
-    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_u8 *)p));
-}
-// Transposing LDS read: within each 16-lane row, lane L points at four bf16
-// X[L][0..3]; lane i receives X[4 r + i / 4][i % 4] for r = 0..3.
-__device__ __forceinline__ u32x2_t lds_tr(uint32_t a)
-{
-    return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                           (__attribute__((address_space(3))) s16x4_t *)(uintptr_t)a));
-}
 template <class T>
 __device__ __forceinline__ T lds_load(uint32_t a)
 {
     return *(const __attribute__((address_space(3))) T *)(uintptr_t)a;
 }
 __device__ __forceinline__ u32x4_t cat(u32x2_t a, u32x2_t b) { return u32x4_t{a[0], a[1], b[0], b[1]}; }
-__device__ __forceinline__ f32x4_t mfma(u32x4_t a, u32x4_t b, f32x4_t c)
-{
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
-}
-// The same over 16 slots, 4 g .. 4 g + 3 in a lane.
+// The product over 16 slots, 4 g .. 4 g + 3 in a lane.
 __device__ __forceinline__ f32x4_t mfma16(u32x2_t a, u32x2_t b, f32x4_t c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4_t, a), __builtin_bit_cast(s16x4_t, b), c, 0, 0, 0);
@@ -120,11 +101,6 @@ __device__ __forceinline__ f32x4_t mfma_f32(f32x4_t a, f32x4_t b, f32x4_t c)
 #pragma unroll
     for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
     return c;
-}
-// Workgroup barrier that orders LDS only: loads to registers stay in flight.
-__device__ __forceinline__ void lds_barrier()
-{
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 // Nothing is scheduled across this.
 __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }

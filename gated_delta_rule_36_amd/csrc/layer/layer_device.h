@@ -1,6 +1,6 @@
 // Device helpers shared by the layer kernels: eight-element loads and stores
-// at any element alignment, sums over lanes, and the map from work slots to
-// sequences.
+// at any element alignment, LDS reads and matrix products, sums over lanes, and
+// the map from work slots to sequences.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -13,6 +13,8 @@ namespace kda {
 namespace layer {
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
@@ -43,6 +45,29 @@ __device__ __forceinline__ u32x4_t pack8(const float f[8])
 {
     return u32x4_t{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                    pack_bf16x2(f[6], f[7])};
+}
+
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+__device__ __forceinline__ uint32_t lds_addr(const void *p)
+{
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_u8 *)p));
+}
+// Transposing LDS read: within each 16-lane row, lane L points at four bf16
+// X[L][0..3]; lane i receives X[4 r + i / 4][i % 4] for r = 0..3.
+__device__ __forceinline__ u32x2_t lds_tr(uint32_t a)
+{
+    return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                           (__attribute__((address_space(3))) s16x4_t *)(uintptr_t)a));
+}
+// Workgroup barrier that orders LDS only: loads to registers stay in flight.
+__device__ __forceinline__ void lds_barrier()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+// c + a b of the matrix unit, 16 x 16 over 32 slots.
+__device__ __forceinline__ f32x4_t mfma(u32x4_t a, u32x4_t b, f32x4_t c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
 }
 
 // The eight elements a lane takes of a row of `size`: from `at` on.  The last

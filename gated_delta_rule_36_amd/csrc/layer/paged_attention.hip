@@ -37,31 +37,12 @@ namespace kda {
 namespace layer {
 namespace {
 
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef short s16x4_t __attribute__((ext_vector_type(4)));
-
 constexpr int kWaves = 4, kThreads = 64 * kWaves, TOK = 32;  // tokens of a wave's tile
 constexpr int ROWS = static_cast<int>(kAttentionRows);
 constexpr float kBelow = 1.0f - 0x1p-10f;
 constexpr float kLn2F = 0.693147180559945f;
 constexpr float kLowest = -3.402823466e38f, kLargest = 3.402823466e38f;
 
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
-__device__ __forceinline__ uint32_t lds_addr(const void *p)
-{
-    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_u8 *)p));
-}
-// Transposing LDS read: within each 16-lane row, lane L points at four bf16
-// X[L][0..3]; lane i receives X[4 r + i / 4][i % 4] for r = 0..3.
-__device__ __forceinline__ u32x2_t lds_tr(uint32_t a)
-{
-    return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                           (__attribute__((address_space(3))) s16x4_t *)(uintptr_t)a));
-}
-__device__ __forceinline__ f32x4_t mfma(u32x4_t a, u32x4_t b, f32x4_t c)
-{
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
-}
 // The upper halves of two numbers: cut to bf16 towards zero.
 __device__ __forceinline__ uint32_t cut_bf16x2(float a, float b)
 {

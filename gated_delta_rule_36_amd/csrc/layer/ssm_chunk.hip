@@ -75,8 +75,6 @@ namespace kda {
 namespace layer {
 namespace {
 
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 constexpr int CH = static_cast<int>(kSsmChunk);  // tokens a block
@@ -100,18 +98,6 @@ struct Int {
 constexpr int kThreads = 64 * NW;
 constexpr int kXPitch = NW * 32 + 4;  // bf16 elements of an x row in LDS
 
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
-__device__ __forceinline__ uint32_t lds_addr(const void *p)
-{
-    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_u8 *)p));
-}
-// Transposing LDS read: within each 16-lane row, lane L points at four bf16
-// X[L][0..3]; lane i receives X[4 r + i / 4][i % 4] for r = 0..3.
-__device__ __forceinline__ u32x2_t lds_tr(uint32_t a)
-{
-    return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                           (__attribute__((address_space(3))) s16x4_t *)(uintptr_t)a));
-}
 __device__ __forceinline__ bf16x8_t cat8(u32x2_t a, u32x2_t b)
 {
     return __builtin_bit_cast(bf16x8_t, u32x4_t{a[0], a[1], b[0], b[1]});
@@ -119,11 +105,6 @@ __device__ __forceinline__ bf16x8_t cat8(u32x2_t a, u32x2_t b)
 __device__ __forceinline__ f32x16_t mfma(bf16x8_t a, bf16x8_t b, f32x16_t c)
 {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-}
-// Workgroup barrier that orders LDS only: loads to registers stay in flight.
-__device__ __forceinline__ void lds_barrier()
-{
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 // Nothing is scheduled across this.
 __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
