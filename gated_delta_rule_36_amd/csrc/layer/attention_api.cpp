@@ -1,7 +1,9 @@
 // C-ABI front end of the attention layers' operators: argument checks on the
 // host, then the hand-off to the kernels.  Nothing here touches device memory.
 #include <algorithm>
+#include <cstddef>
 #include <cstdint>
+#include <utility>
 
 #include "layer_checks.h"
 
@@ -24,13 +26,14 @@ bool cache_extent(int64_t pages, int64_t page_size, int64_t heads, int64_t D, co
            add_ok(a, b, &n) && add_ok(n, c, &n) && add_ok(n, D, &n) && mul_ok(n, 2, bytes);
 }
 
-// Whether no two places share memory: from the smallest stride up, each step
-// passes all that lies below it.
-bool places_apart(int64_t pages, int64_t page_size, int64_t heads, int64_t D, const CacheStrides &s)
+// Whether no two rows of `width` elements share memory, given their dimensions
+// as (stride, size): from the smallest stride up, each step passes all that lies
+// below it.
+template <size_t N>
+bool rows_apart(int64_t width, std::pair<int64_t, int64_t> (&&dims)[N])
 {
-    std::pair<int64_t, int64_t> dims[3] = {{s.page, pages}, {s.token, page_size}, {s.head, heads}};
-    std::sort(dims, dims + 3);
-    int64_t below = D;
+    std::sort(dims, dims + N);
+    int64_t below = width;
     for (const auto &d : dims) {
         if (d.second <= 1)
             continue;
@@ -39,6 +42,10 @@ bool places_apart(int64_t pages, int64_t page_size, int64_t heads, int64_t D, co
         below += (d.second - 1) * d.first;
     }
     return true;
+}
+bool places_apart(int64_t pages, int64_t page_size, int64_t heads, int64_t D, const CacheStrides &s)
+{
+    return rows_apart(D, {{s.page, pages}, {s.token, page_size}, {s.head, heads}});
 }
 
 // Widths, weights and scales of the rotation's two entry points.
@@ -170,23 +177,11 @@ extern "C" kda_status kda_append_kv(const kda_append_args *args, void *stream)
     // The two caches may be interleaved in one buffer (a dimension of keys and
     // values): apart if every row of one lies in the gaps of the other.
     const auto woven = [&] {
-        const int64_t gap = (reinterpret_cast<intptr_t>(a.v_cache) - reinterpret_cast<intptr_t>(a.k_cache)) / 2;
-        if ((reinterpret_cast<intptr_t>(a.v_cache) - reinterpret_cast<intptr_t>(a.k_cache)) % 2 != 0 ||
-            kc.page != vc.page || kc.token != vc.token || kc.head != vc.head)
+        const int64_t gap = reinterpret_cast<intptr_t>(a.v_cache) - reinterpret_cast<intptr_t>(a.k_cache);
+        if (gap % 2 != 0 || kc.page != vc.page || kc.token != vc.token || kc.head != vc.head)
             return false;
         // as a fourth dimension of size 2
-        std::pair<int64_t, int64_t> dims[4] = {{kc.page, a.pages}, {kc.token, a.page_size}, {kc.head, a.Hk},
-                                               {gap < 0 ? -gap : gap, 2}};
-        std::sort(dims, dims + 4);
-        int64_t below = a.D;
-        for (const auto &d : dims) {
-            if (d.second <= 1)
-                continue;
-            if (d.first < below)
-                return false;
-            below += (d.second - 1) * d.first;
-        }
-        return true;
+        return rows_apart(a.D, {{kc.page, a.pages}, {kc.token, a.page_size}, {kc.head, a.Hk}, {(gap < 0 ? -gap : gap) / 2, 2}});
     };
     if (any_overlap(skc, {sk, sv, ss, sp, sf, sw}) || any_overlap(svc, {sk, sv, ss, sp, sf, sw}) ||
         (skc.overlaps(svc) && !woven()))
