@@ -139,7 +139,8 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     ``[N, Hq]`` takes the logarithm of the softmax's sum.  A sequence without a
     visible token gets zeros and -inf; pages outside the cache are not read and
     their tokens not visible.  The workspace is a temporary allocation on the
-    same stream, sized by ``width``.
+    same stream, sized by ``width``, by which a sequence is also split: a table far
+    wider than the lengths need costs time.
     """
     device = _device(q, "q")
     if q.dim() != 3:

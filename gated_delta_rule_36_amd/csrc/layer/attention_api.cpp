@@ -235,8 +235,12 @@ kda_status check_attention_sizes(const kda_attention_args &a)
     return KDA_OK;
 }
 
-// How the tokens of a sequence are cut into splits, by sizes alone (a context is
-// taken as long as its table allows, or its window).  Times in us, 128 channels.
+// How the tokens of a sequence are cut into splits, by sizes alone: a context is
+// taken as long as its table allows, or its window, since the host does not know the
+// lengths.  So a table much wider than the contexts leaves few waves for each: 64
+// requests of 2000 tokens, 8 key heads, with a table for as many, 8 and 64 times as many
+// 118 / 157 / 945 us; of 16384 812 / 1067 / 7611; 256 of 1024 217 / 1002 / 1953.
+// Times in us, 128 channels; n x t are n sequences of t tokens in all, of lengths that differ.
 // - At most kShared tokens: one split, shared by a workgroup's four waves, and
 //   neither a workspace nor a second launch.
 // - pairs (of a sequence and up to 16 query heads of a key head) times tokens
@@ -247,7 +251,7 @@ kda_status check_attention_sizes(const kda_attention_args &a)
 // - Above: one split a wave, whose neighbours take the other key heads of the
 //   same tokens and so read whole rows of the cache between them.  16 x 32768, 8 key heads 42
 //   (shared 44).  As many splits as make kTarget waves: 64 x 131072 tokens at the
-//   most, 8 key heads, for 8192 / 16384 / 32768 / 65536 waves 1034 / 886 / 826 / 857.
+//   most each, 8 key heads, for 8192 / 16384 / 32768 / 65536 waves 1034 / 886 / 826 / 857.
 //   All splits have the same size, so that waves do the same work however lengths
 //   differ; the same number of splits for every sequence took 991.
 //   At least kFewest tokens, or up to kEnough if the splits still make kWaves: 16 x 32768, 8

@@ -29,7 +29,7 @@
 // starts each segment from what that gives.  8191 tokens of 12 heads of 64 x 96:
 // 391 us whole, 107 in 10 segments, of which the join is 8 and either pass half the rest.
 //
-// What bounds it: 8 x 16384 tokens of 32 heads of 128 x 128 take 1.72 ms (1.9 TB/s, 38 % of
+// What bounds it: 8 x 16384 tokens of 32 heads of 128 x 128 take 1.69 to 1.74 ms (1.9 TB/s, 38 % of
 // a large copy's rate), 14000 cycles a tile, of which a SIMD's matrix
 // instructions are busy 7550, vector ones 4900 and LDS 5400, beside each other only
 // where a second wave is there; and a chip this busy runs at 1.9 instead of 2.4 GHz.
@@ -60,9 +60,13 @@
 // Numerics.  k, q and v are bf16 and enter as they are.  Of what is fp32, S
 // enters K S and the weighted U enters S as three bf16 parts, which hold all 24
 // bits; the solve is fp32 throughout.  S enters Q S, and P and U enter P U, as two
-// parts, good to 2^-17 (out is rounded to 2^-8); of their products the last times
-// the last is left out.  G is summed in 64 bits and kept as two floats, since
-// differences of sums lose a small decay beside a strong one.
+// parts, good to 2^-17 (out is rounded to 2^-8; bf16 outputs are 1.2e-4 of their norm
+// off the rounded definition, 1.7e-3 off the definition either way); of their products
+// the last times the last is left out.  Third parts of S and of U there and the product
+// left out would take 1880 us for 1735 and leave 8.9e-5; of P they do not fit in LDS.
+// One part of everything, the solve in fp32 as it is, takes 1227 us for 1690, packed 294
+// for 340, long 94 for 107, at the price of the state's digits.  G is summed in 64 bits
+// and kept as two floats, since differences of sums lose a small decay beside a strong one.
 //
 // What is not finite must not reach earlier tokens through the zeros of a
 // block's upper half: where what U is solved from is not, it and all behind it in

@@ -290,19 +290,30 @@ struct DeltaPlan {
 //   12 / 12 / 15 / 19 / 24 (15 / 15 / 16 / 16 / 16).
 // - packed sequences, whose lengths the host does not know, of up to two tokens
 //   on average: 64 of 1 / 2 tokens 44 / 47 (133 / 134), one of 33 and 31 of 1 38 (66), one of
-//   64 and 63 of none 68 (75).
+//   64 and 63 of none 68 (75), 256 of 1 and one of 257 309 (470); but where nearly all are empty
+//   one long sequence is gone through alone: 2048 tokens and 1023 of none 1933 (841).
 // Of the others, few chains are cut into segments: as many as leave no compute unit of
 // 256 a second workgroup in the pass over own states, which has V + K columns, 128 a
 // workgroup, and of eight tiles at least.  That pass does again what the output
 // pass does, so a sequence has to be 2.5 segments long, or packed ones of unequal lengths 1.9 on
-// average, since the longest of these is what segments shorten.  In us, whole and cut, heads of 128:
+// average, since the longest of these is what segments shorten.  At 1.9 to 2 segments both take
+// about as long (-2 to +6 % by the mean); at 2.5 cutting wins.  In us, whole and cut, heads of 128 (packed ones: five sets of
+// lengths and their mean):
 //   one sequence of 8191 tokens, 12 heads of 64 x 96   391  107 (10 segments)
 //   one of 8192, 32 / 40 / 64 heads                    450  320 (4) / 464  379 (3) / 468  545 (2)
 //   one of 1024, 32 heads                              61   70 (2)
-//   16384 tokens in 2 packed, 24 heads                 530 to 800  551 (5 in all)
-//   in 4, 12 heads                                     297 to 520  289 to 406 (10)
-//   in 8, 8 / 16 heads                                 183 to 247  190 to 264 (16) / 194 to 257  345 (8)
-//   8000 in 12, 4 heads                                74   87 (16)
+//   16384 tokens in 2 packed, 24 heads                 536 to 808, 662  551 to 562, 556 (5 in all, 2.5 each)
+//   in 4, 12 heads                                     298 to 520, 375  294 to 407, 322 (10, 2.5)
+//   in 8, 6 heads                                      182 to 246, 207  164 to 226, 179 (21, 2.5)
+//   in 8, 8 heads                                      183 to 247, 207  194 to 264, 210 (16, 2.0)
+//   in 10, 6 heads                                     155 to 179, 165  163 to 221, 175 (21, 2.0)
+//   in 6, 10 heads                                     206 to 344, 257  249 to 254, 252 (12, 1.9)
+//   in 9, 7 heads                                      166 to 205, 185  181 to 249, 197 (18, 1.9)
+//   in 8, 16 heads                                     194 to 258, 219  345 (8, 1.0)
+//   8000 in 12, 4 heads                                72 to 77, 74     87 to 90, 88 (16, 1.3)
+// Packed calls of more sequences than that many segments stay whole, also where one is far
+// longer than the others, which the host does not know: a prompt of 16384 tokens and 15 / 63 /
+// 255 single ones, 32 heads 1460 / 1462 / 1464, in segments of 4096 699 / 709 / 1032.
 // False if the workspace overflows.
 bool delta_plan(const kda_delta_args &a, const Seqs &s, DeltaPlan *plan)
 {

@@ -13,8 +13,8 @@
 // tokens together.  With few tokens in all, a workgroup's four waves
 // share a split and join in LDS instead.  Splits of one sequence leave unnormalised
 // results, which a second launch joins.  64 sequences of 8 key heads and 32 query heads,
-// 128 channels, lengths up to 131072: 815 us (5.3 TB/s), the rate of a large copy; one of
-// 131071 tokens, 2 key heads 35 us (3.8 TB/s; 5.1 in the first of its two launches).
+// 128 channels, 1048576 tokens in all: 804 to 822 us (5.3 TB/s), the rate of a large copy; one of
+// 131071 tokens, 2 key heads 35 us (3.8 TB/s; 5.0 in the first of its two launches).
 //
 // Operands of v_mfma_f32_16x16x32_bf16: lane (r = lane % 16, g = lane / 16)
 // holds row / column r, slots 8 g .. 8 g + 7; accumulator register i is row
@@ -101,8 +101,8 @@ __device__ __forceinline__ Visible visible(const AttentionParams &p, int64_t n)
 // LDS; otherwise each has its own.  KS steps of 32 channels; a head of D channels
 // half fills the last one, or all of it.
 // Waves a SIMD by what the registers hold without spilling: of 224 channels two (64
-// x 65536 tokens, 8 key heads 125 us, 150 with one), of 256 one (161; two spill 8
-// registers: 153 there, but 148 against 138 for 16 x 262144 of 2 key heads).
+// requests, 65536 tokens in all, 8 key heads 126 us, 149 with one), of 256 one (156; two
+// spill 24 registers and take 170, and 170 against 137 for 16, 262144 tokens and 2 key heads).
 template <int KS, bool SHARED>
 __global__ __launch_bounds__(kThreads, KS <= 4 ? 3 : KS <= 7 ? 2 : 1) void paged_attention_kernel(AttentionParams p, int row_tiles, int64_t items)
 {

@@ -279,7 +279,8 @@ def delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor
     may be one buffer.  ``cu_seqlens`` and ``check_cu_seqlens`` are those of
     :func:`fwd`.  ``segment_tokens`` (a multiple of 64) cuts long sequences
     into segments that run in parallel, for few heads; None lets the library
-    choose.  The workspace is a temporary allocation on the same stream.
+    choose, which keeps many packed sequences whole, also where one is far longer
+    than the others.  The workspace is a temporary allocation on the same stream.
     """
     device = _device(v, "v")
     if v.dim() != 4:

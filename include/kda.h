@@ -563,8 +563,9 @@ kda_status kda_residual_norm(const kda_residual_norm_args *args, void *stream);
  *   seg_tokens     tokens a segment: sequences longer than that are cut into
  *                  segments that run in parallel, joined in fp32 (a segment
  *                  maps the state it starts with to M S + b).  0 lets the
- *                  library choose from the sizes; otherwise a multiple of 64
- *                  (KDA_ERR_SHAPE).
+ *                  library choose from the sizes (it keeps many packed sequences
+ *                  whole, also where one is far longer than the others);
+ *                  otherwise a multiple of 64 (KDA_ERR_SHAPE).
  *   workspace, workspace_bytes   DEVICE scratch, 16-byte aligned, at least
  *                  kda_delta_workspace_bytes(args) bytes (which may be 0), as
  *                  for kda_fwd_scan (KDA_ERR_WORKSPACE otherwise).
@@ -720,14 +721,17 @@ kda_status kda_append_kv(const kda_append_args *args, void *stream);
  *   D              a multiple of 16, at most 256; Hk divides Hq
  *                  (KDA_ERR_SHAPE otherwise).
  *   scale          0 or a normal number of fp32 (KDA_ERR_SCALE otherwise).
- *                  Scores are fp32: one that this does not hold is infinite.
+ *                  q . k and scores are formed in fp32: one that this does
+ *                  not hold is infinite.
  *   window         >= 0; 0 = every token (KDA_ERR_SIZE otherwise).
  *   table_width    * page_size at most 2^31 - 65537 (KDA_ERR_SIZE otherwise).
  *   workspace, workspace_bytes   DEVICE scratch, 16-byte aligned, at least
  *                  kda_paged_attention_workspace_bytes(args) bytes (which may
  *                  be 0), as for kda_fwd_scan (KDA_ERR_WORKSPACE otherwise).
  * N = 0 does nothing.  The contents of block_table and lengths are not read on
- * the host; table_width bounds the work that is launched.
+ * the host; table_width bounds the work that is launched, and a sequence is split
+ * by it: one far wider than the lengths need costs time (64 requests of 2000
+ * tokens, 8 key heads of 128, with room for 2000 / 16000 / 128000: 118 / 157 / 945 us).
  */
 typedef struct kda_attention_args {
     const void *q;
