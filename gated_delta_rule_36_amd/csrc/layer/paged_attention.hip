@@ -26,7 +26,8 @@
 //     16 a + 4 g + i, and V comes in the same order from LDS by reads that
 //     transpose.
 // Probabilities enter as three bf16 parts, the first two cut from just below the
-// number, so that all are positive and an infinite v stays one.  A part leaves less
+// number, so that all are positive and an infinite v stays one (down to 2^-112, where
+// the last leaves bf16's numbers).  A part leaves less
 // than 1.25 2^-7 of what it is taken from, counted by powers of two, the last one half
 // a step, 2^-9, of that: 1.25 2^-23 in all, next to nothing beside fp32's own
 // roundings, and out is off by its rounding alone.  The products have time to spare:

@@ -716,7 +716,8 @@ kda_status kda_append_kv(const kda_append_args *args, void *stream);
  *   lse            fp32 [N,Hq], contiguous; NULL = not written.
  *                  Sequences without a visible token get out = 0, lse = -inf;
  *                  where every visible one's score is -inf, or one's inf,
- *                  out is NaN and lse that infinity.
+ *                  out is NaN and lse that infinity.  A v that is infinite
+ *                  makes out so, or NaN where its p is below 2^-112.
  *                  Tokens that are not visible may hold anything.
  *   D              a multiple of 16, at most 256; Hk divides Hq
  *                  (KDA_ERR_SHAPE otherwise).
